@@ -1,0 +1,105 @@
+/*
+ * selscan_lm.h - C ABI of libselscan_lm: the operators that stand next to the scan of
+ * selscan.h when Mamba layers serve and train a language model, as hand-written HIP kernels
+ * for MI355X (gfx950):
+ *   - the short causal convolution and the selective scan on packed prompts of different
+ *     lengths, with each prompt's state kept in a cache, and on one token per sequence.
+ *
+ * Conventions: those of selscan.h (status codes, device pointers owned by the caller, work only
+ * enqueued on `stream`, nothing allocated or kept by the library, host validation before any HIP
+ * call), and further:
+ *  - Row-major; a `*_stride` argument is the distance between consecutive rows of that array in
+ *    elements (at least the row length, SELSCAN_E_SHAPE otherwise); the elements of a row are
+ *    adjacent.  Arrays without a stride argument are contiguous.
+ *  - Index arrays (cu_seqlens, slots, targets) live in device memory and are read by the kernels
+ *    alone.  What they hold cannot be checked on the host: a kernel never follows an index out of
+ *    its array, as each call says below.
+ *  - No output may overlap an input or another output unless a call says so (SELSCAN_E_ALIAS).
+ *  - All sums are in a fixed order: results are the same from run to run.
+ */
+#ifndef SELSCAN_LM_H
+#define SELSCAN_LM_H
+
+#include "selscan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SELSCAN_LM_ABI_VERSION 1
+
+/*
+ * Packed prompts.  The tokens of nseq sequences lie one after another in arrays of `tokens` rows;
+ * sequence s has rows cu_seqlens[s] <= t < cu_seqlens[s+1] (int32 [nseq+1], rising, from 0 to
+ * tokens; a sequence may be empty).  Offsets are clamped to [0, tokens], and a pair that falls
+ * counts as an empty sequence; then, and for rows that no sequence holds, outputs are unspecified.
+ *
+ * The cache has nslots entries.  slots[s] (int32 [nseq], NULL: slots[s] = s, which needs
+ * nslots >= nseq) is the entry of sequence s; a value outside [0, nslots) means none: the sequence
+ * starts from zeros and its state is not kept.  The entries of one call must differ from one
+ * another (if two sequences name one, its content is unspecified).  carry[s] != 0 (uint8 [nseq],
+ * NULL: all 0): the sequence continues from what its entry holds; else it starts from zeros.
+ * Either way the entry then receives the state after the sequence's last token (an empty
+ * sequence's: the state it starts from).
+ */
+
+/*
+ * causal_conv1d_packed_fwd - causal_conv1d_fwd on packed prompts: for token t of a sequence
+ *     out = act(bias[d] + sum_{i<width} weight[d][i] * x[t-(width-1)+i][d]),
+ * rows before the sequence's first being its cached rows (carry) or zeros.
+ *   x          : [tokens][dim] io_dtype, row stride x_stride;  out : [tokens][dim]
+ *   weight     : [dim][width] fp32, width 1..4;  bias : [dim] fp32, nullable
+ *   conv_state : [nslots][width-1][dim] io_dtype, nullable (no cache: slots and carry are ignored);
+ *                oldest row first.  Read and written in place.
+ *   flags      : SELSCAN_FLAG_SILU or 0
+ */
+int causal_conv1d_packed_fwd(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                             const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *carry, void *conv_state,
+                             unsigned flags, void *out, int64_t tokens, int64_t nseq, int64_t nslots, int64_t dim,
+                             int64_t width, int io_dtype, void *stream);
+
+/*
+ * selscan_packed_fwd - selscan_fwd on packed prompts: every sequence is scanned by itself.
+ *   x, delta, z, y : [tokens][dim] io_dtype; z (nullable) has row stride z_stride
+ *   B, C           : [tokens][dstate] io_dtype, both with row stride bc_stride
+ *   A [dim][dstate], D, delta_bias [dim], flags : as for selscan_fwd (dstate must be 16)
+ *   h_state        : [nslots][dim][dstate] fp32, 16-byte aligned, nullable (no cache); in place
+ *   max_seqlen     : the longest sequence's length, or any bound on it (tokens if unknown).  It
+ *                    only chooses how the work is split and never changes what is computed.
+ *   workspace      : selscan_packed_workspace_bytes(...) bytes, 16-byte aligned (0 where the
+ *                    sequences alone fill the chip: NULL will do).  Where it is not 0, a sequence is
+ *                    scanned in segments side by side: each segment's end state from zero, the
+ *                    segments' states joined in order, then each segment from its true start.
+ */
+int selscan_packed_fwd(const void *x, const void *delta, const float *A, const void *B, const void *C,
+                       int64_t bc_stride, const float *D, const void *z, int64_t z_stride, const float *delta_bias,
+                       unsigned flags, const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *carry,
+                       float *h_state, void *y, int64_t tokens, int64_t nseq, int64_t nslots, int64_t max_seqlen,
+                       int64_t dim, int64_t dstate, int io_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
+size_t selscan_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim, int64_t dstate);
+
+/*
+ * causal_conv1d_step, selscan_step - one token for each of `rows` running sequences: the two calls
+ * above with every sequence one token long, carried, and row r on cache entry slots[r] (NULL: r,
+ * which needs nslots >= rows).  A row whose slot is outside [0, nslots) starts from zeros and keeps
+ * nothing.
+ *   x, out, delta, z, y : [rows][dim] io_dtype (x of the convolution and z with a row stride)
+ *   B, C                : [rows][dstate] io_dtype, row stride bc_stride
+ */
+int causal_conv1d_step(const void *x, int64_t x_stride, const float *weight, const float *bias, const int32_t *slots,
+                       void *conv_state, unsigned flags, void *out, int64_t rows, int64_t nslots, int64_t dim,
+                       int64_t width, int io_dtype, void *stream);
+int selscan_step(const void *x, const void *delta, const float *A, const void *B, const void *C, int64_t bc_stride,
+                 const float *D, const void *z, int64_t z_stride, const float *delta_bias, unsigned flags,
+                 const int32_t *slots, float *h_state, void *y, int64_t rows, int64_t nslots, int64_t dim,
+                 int64_t dstate, int io_dtype, void *stream);
+
+int selscan_lm_abi_version(void);
+/* text of the calling thread's most recent launch that the HIP runtime rejected */
+const char *selscan_lm_last_hip_error(void);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -32,9 +32,9 @@ STATUS = {
 
 
 class SelscanError(RuntimeError):
-    def __init__(self, status: int, what: str):
+    def __init__(self, status: int, what: str, hip_error=None):
         self.status = status
-        extra = f"; HIP: {lib.selscan_last_hip_error().decode()}" if status == 7 else ""
+        extra = f"; HIP: {(hip_error or lib.selscan_last_hip_error)().decode()}" if status == 7 else ""
         super().__init__(f"{what}: {STATUS.get(status, status)} ({status_str(status)}){extra}")
 
 
@@ -677,3 +677,9 @@ def dwconv2d_bwd(x, weight, H, W, dout, bias=None, silu=True, workspace=None, st
                           _stream(stream))
     _check(rc, "dwconv2d_bwd")
     return g
+
+
+# the operators next to the scan (libselscan_lm.so, include/selscan_lm.h)
+from .lm import (  # noqa: E402
+    LM_HEADER, LM_LIB_PATH, causal_conv1d_packed_fwd, causal_conv1d_step, lm_abi_version, lm_lib, selscan_packed_fwd,
+    selscan_packed_workspace_bytes, selscan_step)

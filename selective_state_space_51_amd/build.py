@@ -1,5 +1,5 @@
-"""Build libselscan.so in-tree with hipcc for gfx950 (cross-compiles without a GPU), and beside it
-two diagnostic libraries: libselscan_ubench.so (the microbenchmarks) and libselscan_phases.so (the
+"""Build libselscan.so and libselscan_lm.so (the operators next to the scan in a language model) in-tree
+with hipcc for gfx950 (cross-compiles without a GPU), and beside them two diagnostic libraries: libselscan_ubench.so (the microbenchmarks) and libselscan_phases.so (the
 scan library with the backward's per-wave phase clocks compiled in).  The sources compile in
 parallel to objects in a temporary directory, then link."""
 from __future__ import annotations
@@ -15,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("selscan_fwd.hip", "selscan_bwd.hip", "selscan_conv.hip")]
 OUT = os.path.join(PKG, "libselscan.so")
+LM_SRCS = [os.path.join(CSRC, f) for f in ("lm_scan.hip",)]
+LM_OUT = os.path.join(PKG, "libselscan_lm.so")
 UBENCH_SRCS = [os.path.join(CSRC, "ubench.hip")]
 UBENCH_OUT = os.path.join(PKG, "libselscan_ubench.so")
 PHASES_OUT = os.path.join(PKG, "libselscan_phases.so")
@@ -58,9 +60,11 @@ def build(extra=None, out=OUT, srcs=None, verbose=False) -> str:
 
 
 def build_all(extra=None, verbose=False) -> None:
-    """The scan library and the two diagnostic libraries, compiled side by side."""
-    with cf.ThreadPoolExecutor(max_workers=3) as ex:
+    """The scan library, the language-model operators and the two diagnostic libraries, compiled side
+    by side."""
+    with cf.ThreadPoolExecutor(max_workers=4) as ex:
         futs = [ex.submit(build, extra, OUT, SRCS, verbose),
+                ex.submit(build, extra, LM_OUT, LM_SRCS, verbose),
                 ex.submit(build, extra, UBENCH_OUT, UBENCH_SRCS, verbose),
                 ex.submit(build, [*(extra or []), "-DSELSCAN_PHASE_CLOCKS"], PHASES_OUT, SRCS, verbose)]
         for f in futs:

@@ -1,0 +1,77 @@
+// lm_common.h - what the sources of libselscan_lm share beyond selscan_common.h: host-side argument
+// checks and launches, unaligned vector reads, reductions across a wave and a workgroup.
+#pragma once
+
+#include "selscan_common.h"
+#include "selscan_lm.h"
+
+namespace {
+
+// ------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------
+
+inline bool io_known(int dtype) { return dtype == SELSCAN_F32 || dtype == SELSCAN_BF16; }
+inline size_t io_bytes(int dtype) { return dtype == SELSCAN_BF16 ? 2 : 4; }
+
+// bytes from the first to the last element of `rows` rows of `width` elements, `stride` apart
+inline size_t strided_bytes(int64_t rows, int64_t width, int64_t stride, size_t elem) {
+    return rows <= 0 || width <= 0 ? 0 : ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * elem;
+}
+
+inline bool span_aligned(const void *p, size_t a) { return !p || aligned(p, a); }
+
+// a * b for non-negative sizes, or -1 where it passes 2^62 (then no array of that size exists)
+inline int64_t mul_size(int64_t a, int64_t b) {
+    if (a == 0 || b == 0) return 0;
+    return a > (INT64_C(1) << 62) / b ? -1 : a * b;
+}
+
+// every output against every input and every other output
+inline bool any_alias(const Span *in, int nin, const Span *out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i], in[j])) return true;
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+template <class P>
+int enqueue(void (*kernel)(P), dim3 grid, dim3 block, const P &p, void *stream) {
+    P copy = p;
+    void *args[] = {&copy};
+    const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, args, 0, (hipStream_t)stream);
+    if (e != hipSuccess) {
+        record_hip_error(e);
+        return SELSCAN_E_HIP;
+    }
+    return SELSCAN_OK;
+}
+
+// ------------------------------------------------------------------------------------
+// device side
+// ------------------------------------------------------------------------------------
+
+// 4 floats from an address that is 4-byte aligned (one 16-byte load)
+__device__ __forceinline__ float4 load_f4(const float *p) {
+    struct __attribute__((packed, aligned(4))) U {
+        float a, b, c, d;
+    };
+    const U u = *(const U *)p;
+    return make_float4(u.a, u.b, u.c, u.d);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+
+}  // namespace

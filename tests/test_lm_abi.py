@@ -1,0 +1,109 @@
+"""CPU tests of libselscan_lm's C ABI: it exports what include/selscan_lm.h declares and refuses bad arguments
+on the host before any HIP call (every call here returns from validation; pointers are never followed)."""
+import re
+import subprocess
+
+import pytest
+
+import selective_state_space_51_amd as S
+
+L = S.lm_lib
+P = 0x10000
+MB = 1 << 20
+OK, NULL, SHAPE, ALIGN, ALIAS, UNSUPPORTED, WORKSPACE = range(7)
+
+
+def test_exports_every_declared_symbol():
+    text = open(S.LM_HEADER).read()
+    declared = set(re.findall(r"^(?:int|size_t|const char \*)\s*\**\s*(\w+)\s*\(", text, re.M))
+    out = subprocess.run(["nm", "-D", "--defined-only", S.LM_LIB_PATH], capture_output=True, text=True, check=True).stdout
+    exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
+    assert declared and declared <= exported
+    assert S.lm_abi_version() == 1
+    assert all(hasattr(L, n) for n in declared)
+
+
+def conv(x=P, xs=64, w=P + MB, b=None, cu=P + 2 * MB, slots=None, carry=None, st=P + 3 * MB, flags=4, out=P + 4 * MB,
+         tokens=10, nseq=3, nslots=3, dim=64, width=4, dt=1):
+    return L.causal_conv1d_packed_fwd(x, xs, w, b, cu, slots, carry, st, flags, out, tokens, nseq, nslots, dim, width, dt, None)
+
+
+def test_conv_packed_refusals():
+    for kw in ("x", "w", "cu", "out"):
+        assert conv(**{kw: None}) == NULL, kw
+    for kw in ("tokens", "nseq", "nslots", "dim"):
+        assert conv(**{kw: -1}) == SHAPE, kw
+    assert conv(xs=63) == SHAPE
+    assert conv(nslots=2) == SHAPE  # no slots: sequence s is on entry s
+    assert conv(nseq=0) == SHAPE  # tokens without a sequence
+    assert conv(nseq=0, tokens=0, x=None) == OK and conv(dim=0, x=None) == OK
+    assert conv(width=5) == UNSUPPORTED and conv(width=0) == UNSUPPORTED
+    assert conv(dt=2) == UNSUPPORTED and conv(flags=1) == UNSUPPORTED
+    assert conv(tokens=1 << 31) == UNSUPPORTED
+    assert conv(x=P + 1) == ALIGN and conv(w=P + MB + 2) == ALIGN and conv(cu=P + 2 * MB + 1) == ALIGN
+    assert conv(st=P + 3 * MB + 1) == ALIGN and conv(b=P + 5 * MB + 2) == ALIGN and conv(slots=P + 5 * MB + 2) == ALIGN
+    assert conv(out=P + 16) == ALIAS and conv(st=P + 128) == ALIAS and conv(st=P + 4 * MB) == ALIAS
+    assert conv(out=P + 2 * 64, xs=128) == ALIAS  # between the columns of strided rows
+
+
+def step(x=P, xs=64, w=P + MB, slots=None, st=P + 3 * MB, flags=4, out=P + 4 * MB, rows=3, nslots=3, dim=64, width=4, dt=1):
+    return L.causal_conv1d_step(x, xs, w, None, slots, st, flags, out, rows, nslots, dim, width, dt, None)
+
+
+def test_conv_step_refusals():
+    for kw in ("x", "w", "st", "out"):
+        assert step(**{kw: None}) == NULL, kw
+    assert step(rows=-1) == SHAPE and step(nslots=2) == SHAPE and step(xs=8) == SHAPE
+    assert step(rows=0, x=None) == OK
+    assert step(width=6) == UNSUPPORTED
+    assert step(out=P) == ALIAS
+
+
+def scan(x=P, d=P + MB, A=P + 2 * MB, B=P + 3 * MB, C=P + 4 * MB, bcs=32, D=None, z=None, zs=64, bias=None, flags=0,
+         cu=P + 5 * MB, slots=None, carry=None, h=P + 6 * MB, y=P + 7 * MB, tokens=1000, nseq=2, nslots=2, longest=1000,
+         dim=64, N=16, dt=1, ws=P + 16 * MB, wsb=1 << 24):
+    return L.selscan_packed_fwd(x, d, A, B, C, bcs, D, z, zs, bias, flags, cu, slots, carry, h, y, tokens, nseq, nslots,
+                                longest, dim, N, dt, ws, wsb, None)
+
+
+def test_scan_packed_refusals():
+    for kw in ("x", "d", "A", "B", "C", "cu", "y"):
+        assert scan(**{kw: None}) == NULL, kw
+    for kw in ("tokens", "nseq", "nslots", "dim", "longest", "N"):
+        assert scan(**{kw: -1}) == SHAPE, kw
+    assert scan(bcs=15) == SHAPE and scan(z=P + 8 * MB, zs=63) == SHAPE and scan(nslots=1) == SHAPE
+    assert scan(nseq=0) == SHAPE and scan(nseq=0, tokens=0) == OK and scan(dim=0) == OK
+    assert scan(N=8) == UNSUPPORTED and scan(dt=3) == UNSUPPORTED and scan(flags=4) == UNSUPPORTED
+    assert scan(A=P + 2 * MB + 2) == ALIGN and scan(h=P + 6 * MB + 4) == ALIGN and scan(B=P + 3 * MB + 1) == ALIGN
+    need = S.selscan_packed_workspace_bytes(1000, 2, 1000, 64)
+    assert need > 0
+    assert scan(wsb=need - 1) == WORKSPACE and scan(ws=None) == WORKSPACE and scan(ws=P + 16 * MB + 4) == ALIGN
+    assert scan(y=P + 2) == ALIAS and scan(h=P + MB) == ALIAS and scan(ws=P + 7 * MB) == ALIAS
+    assert S.selscan_packed_workspace_bytes(0, 2, 10, 64) == 0
+    assert S.selscan_packed_workspace_bytes(64, 2, 32, 64) == 0
+
+
+def sstep(x=P, d=P + MB, A=P + 2 * MB, B=P + 3 * MB, C=P + 4 * MB, bcs=32, z=None, zs=64, slots=None, h=P + 6 * MB,
+          y=P + 7 * MB, rows=3, nslots=3, dim=64, N=16, dt=1, flags=0):
+    return L.selscan_step(x, d, A, B, C, bcs, None, z, zs, None, flags, slots, h, y, rows, nslots, dim, N, dt, None)
+
+
+def test_scan_step_refusals():
+    for kw in ("x", "d", "A", "B", "C", "h", "y"):
+        assert sstep(**{kw: None}) == NULL, kw
+    assert sstep(rows=-1) == SHAPE and sstep(nslots=2) == SHAPE and sstep(bcs=8) == SHAPE
+    assert sstep(N=4) == UNSUPPORTED and sstep(flags=8) == UNSUPPORTED
+    assert sstep(h=P + 6 * MB + 8) == ALIGN
+    assert sstep(y=P) == ALIAS and sstep(h=P + 64) == ALIAS
+    assert sstep(rows=0) == OK
+
+
+def test_binding_refusals():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="device tensor"):
+        S.causal_conv1d_step(x, torch.zeros(8, 4), torch.zeros(4, 3, 8))
+    with pytest.raises(ValueError, match="shape"):
+        S.selscan_step(x, torch.zeros(4, 9), torch.zeros(8, 16), torch.zeros(4, 16), torch.zeros(4, 16), torch.zeros(4, 8, 16))
+    with pytest.raises(ValueError, match="shape"):
+        S.causal_conv1d_packed_fwd(x, torch.zeros(8, 4), torch.zeros(3, dtype=torch.int32), torch.zeros(2, 4, 8))
