@@ -3,7 +3,8 @@
  * selscan.h when Mamba layers serve and train a language model, as hand-written HIP kernels
  * for MI355X (gfx950):
  *   - the short causal convolution and the selective scan on packed prompts of different
- *     lengths, with each prompt's state kept in a cache, and on one token per sequence.
+ *     lengths, with each prompt's state kept in a cache, and on one token per sequence;
+ *   - residual addition + root-mean-square norm, with an 8-bit output, and its gradients.
  *
  * Conventions: those of selscan.h (status codes, device pointers owned by the caller, work only
  * enqueued on `stream`, nothing allocated or kept by the library, host validation before any HIP
@@ -27,6 +28,9 @@ extern "C" {
 #endif
 
 #define SELSCAN_LM_ABI_VERSION 1
+
+/* output kinds of add_rms_norm_fwd */
+typedef enum { SELSCAN_LM_OUT_IO = 0, SELSCAN_LM_OUT_INT8 = 1, SELSCAN_LM_OUT_FP8 = 2 } selscan_lm_out;
 
 /*
  * Packed prompts.  The tokens of nseq sequences lie one after another in arrays of `tokens` rows;
@@ -94,6 +98,46 @@ int selscan_step(const void *x, const void *delta, const float *A, const void *B
                  const float *D, const void *z, int64_t z_stride, const float *delta_bias, unsigned flags,
                  const int32_t *slots, float *h_state, void *y, int64_t rows, int64_t nslots, int64_t dim,
                  int64_t dstate, int io_dtype, void *stream);
+
+/*
+ * add_rms_norm_fwd - residual addition and root-mean-square norm of each row:
+ *     s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight
+ *   x            : [rows][width] io_dtype, row stride x_stride
+ *   residual     : [rows][width] residual_dtype (SELSCAN_F32, or io_dtype), nullable (s = x)
+ *   residual_out : [rows][width] residual_dtype, nullable; written with s, and may be `residual`
+ *                  itself.  y is formed from s before it is rounded to residual_dtype.
+ *   weight       : [width] fp32
+ *   out_kind, y  : SELSCAN_LM_OUT_IO: [rows][width] io_dtype; SELSCAN_LM_OUT_INT8: int8,
+ *                  SELSCAN_LM_OUT_FP8: 8-bit floats (e4m3, largest value 448)
+ *   scale        : [rows] fp32, written for the 8-bit outputs and required then: y stands for
+ *                  scale[r] * y[r][c], scale = max|row| / 127 (/ 448), each element rounded to
+ *                  nearest even.  A row of zeros (or smaller than 1e-32) has scale 0 and zeros; a row whose
+ *                  sum of squares is not finite has scale NaN and zeros.
+ *   rstd         : [rows] fp32, nullable
+ *   eps          : >= 0, finite (SELSCAN_E_UNSUPPORTED); width at most 32768 (SELSCAN_E_UNSUPPORTED)
+ */
+int add_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, const float *weight, float eps,
+                     int out_kind, void *y, void *residual_out, float *scale, float *rstd, int64_t rows, int64_t width,
+                     int io_dtype, int residual_dtype, void *stream);
+
+/*
+ * add_rms_norm_bwd - gradients of add_rms_norm_fwd (SELSCAN_LM_OUT_IO).  With xhat = s * rstd and
+ * g = dy * weight:
+ *     ds = rstd * (g - xhat * mean(g * xhat)) + dresidual_out,  dx = dresidual = ds,
+ *     dweight[c] = sum_rows dy * xhat
+ *   dy             : [rows][width] io_dtype
+ *   s              : [rows][width] residual_dtype, the forward's residual_out;  rstd : its rstd
+ *   dresidual_out  : [rows][width] residual_dtype, nullable (no gradient through residual_out)
+ *   dx             : [rows][width] io_dtype, nullable;  dresidual : [rows][width] residual_dtype,
+ *                    nullable (both are ds, each in its type)
+ *   dweight        : [width] fp32, nullable (written with zeros when rows == 0)
+ *   workspace      : add_rms_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (per-workgroup
+ *                    sums of dweight); required with dweight
+ */
+int add_rms_norm_bwd(const void *dy, const void *s, const float *weight, const float *rstd, const void *dresidual_out,
+                     void *dx, void *dresidual, float *dweight, int64_t rows, int64_t width, int io_dtype,
+                     int residual_dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
 
 int selscan_lm_abi_version(void);
 /* text of the calling thread's most recent launch that the HIP runtime rejected */

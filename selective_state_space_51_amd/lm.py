@@ -41,6 +41,9 @@ def _load(path=None):
     sig("selscan_packed_fwd", [vp] * 5 + [i64, vp, vp, i64, vp, cu] + [vp] * 5 + [i64] * 6 + [ci, vp, sz, vp])
     sig("selscan_packed_workspace_bytes", [i64] * 5, sz)
     sig("selscan_step", [vp] * 5 + [i64, vp, vp, i64, vp, cu] + [vp] * 3 + [i64] * 4 + [ci, vp])
+    sig("add_rms_norm_fwd", [vp, i64, vp, vp, cf, ci] + [vp] * 4 + [i64, i64, ci, ci, vp])
+    sig("add_rms_norm_bwd", [vp] * 8 + [i64, i64, ci, ci, vp, sz, vp])
+    sig("add_rms_norm_bwd_workspace_bytes", [i64, i64], sz)
     sig("selscan_lm_abi_version", [])
     sig("selscan_lm_last_hip_error", [], ctypes.c_char_p)
     return lib
@@ -234,3 +237,64 @@ def selscan_step(x, delta, A, B, C, h_state, D=None, z=None, delta_bias=None, de
                              _dtype_code(x), _stream(stream))
     _check(rc, "selscan_step")
     return y
+
+
+@_on_launch_stream
+def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out="io", residual_dtype=None, rstd=False, stream=None):
+    """s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight over the rows of x [rows, width].
+
+    residual: [rows, width], fp32 or x's dtype (None: s = x, kept as residual_dtype, by default x's).
+    out: "io" (y in x's dtype), "int8" or "fp8" (e4m3; y stands for scale[:, None] * y).
+    Returns (y, s[, scale][, rstd]): s in the residual's dtype, scale fp32 [rows] for the 8-bit outputs, rstd
+    fp32 [rows] when asked for (add_rms_norm_bwd takes it)."""
+    torch = _torch()
+    rows, width = x.shape
+    io = x.dtype
+    if out not in _OUT_KINDS:
+        raise ValueError(f"out must be one of {sorted(_OUT_KINDS)}")
+    rdt = residual.dtype if residual is not None else residual_dtype or io
+    if rdt not in (torch.float32, io):
+        raise TypeError("the residual must be float32 or have the io dtype")
+    _shape_check("weight", weight, (width,))
+    _shape_check("residual", residual, (rows, width))
+    y = torch.empty(rows, width, dtype={"io": io, "int8": torch.int8, "fp8": torch.float8_e4m3fn}[out], device=x.device)
+    s = torch.empty(rows, width, dtype=rdt, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device) if out != "io" else None
+    rs = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd else None
+    xp, xs = _rows(x, "x", io)
+    rc = lm_lib.add_rms_norm_fwd(xp, xs, _ptr(residual, "residual", rdt), _ptr(weight, "weight", f32=True), eps,
+                                 _OUT_KINDS[out], _ptr(y, "y"), _ptr(s, "s"), _ptr(scale, "scale"), _ptr(rs, "rstd"),
+                                 rows, width, _dtype_code(x), _dtype_code(s), _stream(stream))
+    _check(rc, "add_rms_norm_fwd")
+    return (y, s) + ((scale,) if scale is not None else ()) + ((rs,) if rstd else ())
+
+
+def add_rms_norm_bwd_workspace_bytes(rows: int, width: int) -> int:
+    return int(lm_lib.add_rms_norm_bwd_workspace_bytes(rows, width))
+
+
+@_on_launch_stream
+def add_rms_norm_bwd(dy, s, weight, rstd, x_dtype=None, dresidual_out=None, workspace=None, stream=None):
+    """Gradients of add_rms_norm_fwd's "io" output: dy [rows, width]; s and rstd from the forward; dresidual_out
+    the gradient that reaches s by the residual path (None: none).  Returns a dict: dx (x_dtype, which is dy's),
+    dresidual (the same numbers in s's dtype; dx itself where the dtypes agree) and dweight (fp32 [width])."""
+    torch = _torch()
+    rows, width = dy.shape
+    io = dy.dtype
+    if x_dtype not in (None, io):
+        raise TypeError("dy must have x's dtype")
+    for n_, t_, s_ in (("s", s, (rows, width)), ("weight", weight, (width,)), ("rstd", rstd, (rows,)),
+                       ("dresidual_out", dresidual_out, (rows, width))):
+        _shape_check(n_, t_, s_)
+    g = {"dx": torch.empty(rows, width, dtype=io, device=dy.device),
+         "dresidual": torch.empty_like(s) if s.dtype != io else None,
+         "dweight": torch.empty(width, dtype=torch.float32, device=dy.device)}
+    ws, wsb, _keep = _workspace(add_rms_norm_bwd_workspace_bytes(rows, width), workspace, dy.device)
+    rc = lm_lib.add_rms_norm_bwd(_ptr(dy, "dy"), _ptr(s, "s"), _ptr(weight, "weight", f32=True),
+                                 _ptr(rstd, "rstd", f32=True), _ptr(dresidual_out, "dresidual_out", s.dtype),
+                                 _ptr(g["dx"], "dx"), _ptr(g["dresidual"], "dresidual"), _ptr(g["dweight"], "dweight"),
+                                 rows, width, _dtype_code(dy), _dtype_code(s), ws, wsb, _stream(stream))
+    _check(rc, "add_rms_norm_bwd")
+    if g["dresidual"] is None:
+        g["dresidual"] = g["dx"]
+    return g

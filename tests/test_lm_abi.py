@@ -107,3 +107,40 @@ def test_binding_refusals():
         S.selscan_step(x, torch.zeros(4, 9), torch.zeros(8, 16), torch.zeros(4, 16), torch.zeros(4, 16), torch.zeros(4, 8, 16))
     with pytest.raises(ValueError, match="shape"):
         S.causal_conv1d_packed_fwd(x, torch.zeros(8, 4), torch.zeros(3, dtype=torch.int32), torch.zeros(2, 4, 8))
+
+
+def norm(x=P, xs=64, res=P + MB, w=P + 2 * MB, eps=1e-5, kind=0, y=P + 3 * MB, ro=P + 4 * MB, scale=None, rstd=None,
+         rows=8, width=64, dt=1, rdt=0):
+    return L.add_rms_norm_fwd(x, xs, res, w, eps, kind, y, ro, scale, rstd, rows, width, dt, rdt, None)
+
+
+def test_norm_refusals():
+    for kw in ("x", "w", "y"):
+        assert norm(**{kw: None}) == NULL, kw
+    assert norm(kind=1) == NULL  # an 8-bit output needs its scales
+    assert norm(rows=-1) == SHAPE and norm(width=-1) == SHAPE and norm(xs=63) == SHAPE
+    assert norm(rows=0, x=None) == OK and norm(width=0) == OK
+    assert norm(kind=3) == UNSUPPORTED and norm(dt=2) == UNSUPPORTED and norm(dt=0, rdt=1) == UNSUPPORTED
+    assert norm(width=32769, xs=32769) == UNSUPPORTED
+    for eps in (-1e-5, float("nan"), float("inf")):
+        assert norm(eps=eps) == UNSUPPORTED
+    assert norm(x=P + 1) == ALIGN and norm(res=P + MB + 2) == ALIGN and norm(w=P + 2 * MB + 1) == ALIGN
+    assert norm(y=P) == ALIAS and norm(ro=P + MB + 64) == ALIAS and norm(rstd=P + 3 * MB) == ALIAS
+    assert norm(ro=P + 16) == ALIAS
+
+
+def norm_bwd(dy=P, s=P + MB, w=P + 2 * MB, rstd=P + 3 * MB, dres=None, dx=P + 4 * MB, dr=P + 5 * MB, dw=P + 6 * MB, rows=8,
+             width=64, dt=1, rdt=0, ws=P + 7 * MB, wsb=MB):
+    return L.add_rms_norm_bwd(dy, s, w, rstd, dres, dx, dr, dw, rows, width, dt, rdt, ws, wsb, None)
+
+
+def test_norm_bwd_refusals():
+    for kw in ("dy", "s", "w", "rstd"):
+        assert norm_bwd(**{kw: None}) == NULL, kw
+    assert norm_bwd(rows=-1) == SHAPE and norm_bwd(dt=9) == UNSUPPORTED
+    assert norm_bwd(rows=0, dw=None) == OK
+    need = S.add_rms_norm_bwd_workspace_bytes(8, 64)
+    assert need == 8 * 64 * 4 and S.add_rms_norm_bwd_workspace_bytes(0, 64) == 0
+    assert norm_bwd(wsb=need - 1) == WORKSPACE and norm_bwd(ws=None) == WORKSPACE
+    assert norm_bwd(ws=P + 7 * MB + 4) == ALIGN and norm_bwd(s=P + MB + 2) == ALIGN
+    assert norm_bwd(dx=P) == ALIAS and norm_bwd(dr=P + 4 * MB) == ALIAS and norm_bwd(ws=P + 6 * MB) == ALIAS
