@@ -4,7 +4,8 @@
  * for MI355X (gfx950):
  *   - the short causal convolution and the selective scan on packed prompts of different
  *     lengths, with each prompt's state kept in a cache, and on one token per sequence;
- *   - residual addition + root-mean-square norm, with an 8-bit output, and its gradients.
+ *   - residual addition + root-mean-square norm, with an 8-bit output, and its gradients;
+ *   - log probability of a token, entropy and top alternatives from logits, and their gradient.
  *
  * Conventions: those of selscan.h (status codes, device pointers owned by the caller, work only
  * enqueued on `stream`, nothing allocated or kept by the library, host validation before any HIP
@@ -138,6 +139,42 @@ int add_rms_norm_bwd(const void *dy, const void *s, const float *weight, const f
                      void *dx, void *dresidual, float *dweight, int64_t rows, int64_t width, int io_dtype,
                      int residual_dtype, void *workspace, size_t workspace_bytes, void *stream);
 size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
+
+/*
+ * token_logprobs_fwd - from the logits of a row, with v = scale * logits and p = softmax(v):
+ *     logprob = v[target] - log sum exp(v),  entropy = -sum p log p  (0 log 0 = 0),
+ *     and the `top` largest logits as (log probability, index), largest first, equal ones by index
+ *   logits      : [rows][vocab] io_dtype, row stride logits_stride
+ *   targets     : [rows] int64; a target outside [0, vocab) gives logprob 0 (an ignored token)
+ *   logprob, entropy : [rows] fp32
+ *   stats       : [rows][2] fp32: the largest logit x, and log sum exp(v - scale * x); their sum, scale * x +
+ *                 log sum, is the log of the softmax's denominator.  Apart, they lose nothing to the logits' size
+ *                 (the gradient takes them).
+ *   top         : 0..32 (SELSCAN_E_UNSUPPORTED above; no more than vocab, SELSCAN_E_SHAPE)
+ *   top_logprob : [rows][top] fp32, top_index : [rows][top] int64; entries without probability
+ *                 (a logit of -inf) are (-inf, -1)
+ *   scale       : finite and > 0 (SELSCAN_E_UNSUPPORTED)
+ * A logit of -inf has probability 0.  A row of nothing but -inf has stats -inf, logprob -inf and
+ * entropy 0.  A row with a NaN or +inf has NaN for its log sum, logprob, entropy and alternatives (index -1).
+ *   workspace   : token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
+ */
+int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t *targets, float scale, int top,
+                       float *logprob, float *entropy, float *stats, float *top_logprob, int64_t *top_index, int64_t rows,
+                       int64_t vocab, int io_dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
+
+/*
+ * token_logprobs_bwd - gradient of sum(dlogprob * logprob + dentropy * entropy) for the logits:
+ *     dlogits = scale * (dlogprob * (1[target] - p) - dentropy * p * (log p + entropy))
+ *   stats, entropy : the forward's;  dlogprob, dentropy : [rows] fp32, nullable (0), not both
+ *                  (SELSCAN_E_NULL)
+ *   dlogits      : [rows][vocab] io_dtype, contiguous
+ * The alternatives carry no gradient; an ignored target's logprob carries none.  A row of nothing
+ * but -inf has gradient 0.
+ */
+int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t *targets, const float *stats,
+                       const float *entropy, const float *dlogprob, const float *dentropy, float scale, void *dlogits,
+                       int64_t rows, int64_t vocab, int io_dtype, void *stream);
 
 int selscan_lm_abi_version(void);
 /* text of the calling thread's most recent launch that the HIP runtime rejected */

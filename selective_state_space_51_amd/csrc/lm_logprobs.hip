@@ -1,0 +1,425 @@
+// libselscan_lm - log probability of a token, entropy and top alternatives from logits, and the
+// gradient of the first two (token_logprobs_fwd, token_logprobs_bwd of include/selscan_lm.h).
+// MI355X (gfx950).
+//
+// With c = scale log2 e, m the largest logit of a row and a = c (x - m):
+//     s = sum 2^a,  t = sum 2^a a,  logprob = ln 2 (a[target] - log2 s),  entropy = ln 2 (log2 s - t / s).
+// (x - m before the product: a row of the type's lowest value, whose c x overflows, is a row of equal logits.)
+// A row is cut into slices that a workgroup holds in registers, so the logits are read once; the
+// slices' (m, s, t) and their best alternatives are joined by a second, small kernel.  HBM bound.
+#include "lm_common.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTop = 32;
+constexpr int kCand = 512;  // candidates a slice ranks directly
+
+struct LpParams {
+    const void *x;
+    const int64_t *targets;
+    float *logprob, *entropy, *stats, *top_logprob;
+    int64_t *top_index;
+    float4 *part;               // [rows][nsl]: m, s, t
+    unsigned long long *cand;   // [rows][nsl][top]: order of the logit above, complement of its index below; 0: none
+    const float *in_stats, *in_entropy, *dlogprob, *dentropy;
+    void *dx;
+    int64_t rows, stride;
+    int vocab, nsl, top;
+    float c, scale;
+};
+
+// 8 elements from any address aligned to the element
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_any8(const T *p) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U {
+        uint32_t w[sizeof(T) * 2];
+    };
+    const U u = *(const U *)p;
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 2; ++i) r.w[i] = u.w[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_any8(T *p, const float (&v)[8]) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U {
+        uint32_t w[sizeof(T) * 2];
+    };
+    U u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.w[i] = Io<T>::to2(v[2 * i], v[2 * i + 1]);
+    }
+    *(U *)p = u;
+}
+
+// elements [at, at + 8) of a row of n; those past its end are -inf
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_logits(const T *row, int at, int n) {
+    if (at + 8 <= n) return load_any8(row + at);
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.w[e] = at + e < n ? __float_as_uint(row[at + e]) : 0xFF800000u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = at + 2 * e < n ? row[at + 2 * e] : 0xFF80u, hi = at + 2 * e + 1 < n ? row[at + 2 * e + 1] : 0xFF80u;
+            r.w[e] = lo | hi << 16;
+        }
+    }
+    return r;
+}
+
+// floats in the order of their values as unsigned numbers (both zeros alike), and back
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ unsigned long long entry(float x, int index) {
+    return (unsigned long long)order_of(x) << 32 | (uint32_t)~index;
+}
+
+// The k-th largest of the 64 lanes' values (k <= 64), bit by bit from the top; bf16 values differ in
+// their upper 16 bits only.
+template <typename T>
+__device__ __forceinline__ float kth_of_wave(float v, int k) {
+    const uint32_t o = sizeof(T) == 2 ? order_of(v) >> 16 : order_of(v);
+    uint32_t best = 0;
+#pragma unroll
+    for (int b = sizeof(T) == 2 ? 15 : 31; b >= 0; --b) {
+        const uint32_t cand = best | 1u << b;
+        if (__popcll(__ballot(o >= cand)) >= k) best = cand;
+    }
+    // (of a negative number's bits below, all are set in the order)
+    return value_of(sizeof(T) == 2 ? (best << 16) | (best & 0x8000u ? 0u : 0xFFFFu) : best);
+}
+
+// One workgroup: PIECES x 256 x 8 logits of one row, in registers.
+//
+// Alternatives: the `top`-th largest of a wave's 64 per-lane maxima is no larger than the slice's `top`-th
+// largest logit, so every logit of the slice that can be among the best is at or above the largest of the four
+// waves' bounds.  Those few (some hundred for top = 32) are gathered in LDS and ranked by counting.  If equal
+// values make them too many, the best are taken out one after another instead.
+template <typename T, int PIECES>
+__global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
+    __shared__ float red[4];
+    __shared__ float red2[4][2];
+    __shared__ float bound[4];
+    __shared__ unsigned long long cand[kCand], pick[4];
+    __shared__ int ncand;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int64_t blk = blockIdx.x, row = blk / p.nsl;
+    const int base = (int)(blk - row * p.nsl) * (PIECES * kThreads * 8);
+    const T *x = (const T *)p.x + row * p.stride;
+    Raw8<T> r[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) r[i] = load_logits(x, base + (i * kThreads + tid) * 8, p.vocab);
+    if (tid == 0) ncand = 0;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, raw_f32(r[i], e));
+    const float mine = m;
+    m = wave_max(m);
+    if (lane == 0) red[wave] = m;
+    if (p.top) {
+        const float b = kth_of_wave<T>(mine, p.top);
+        if (lane == 0) bound[wave] = b;
+    }
+    lds_barrier();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float mm = m == -INFINITY ? 0.f : m;
+    float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = (raw_f32(r[i], e) - mm) * p.c, w = __builtin_amdgcn_exp2f(a);
+            s += w;
+            t = fmaf(w, fmaxf(a, -200.f), t);  // 2^-200 is 0: no 0 * inf for a logit of -inf
+        }
+    s = wave_sum(s), t = wave_sum(t);
+    if (lane == 0) red2[wave][0] = s, red2[wave][1] = t;
+    if (p.top) {
+        const float b = fmaxf(fmaxf(bound[0], bound[1]), fmaxf(bound[2], bound[3]));
+        if (mine >= b && mine > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = raw_f32(r[i], e);
+                    if (v >= b && v > -INFINITY) {
+                        const int at = atomicAdd(&ncand, 1);
+                        if (at < kCand) cand[at] = entry(v, base + (i * kThreads + tid) * 8 + e);
+                    }
+                }
+        }
+    }
+    lds_barrier();
+    if (tid == 0) {
+        s = (red2[0][0] + red2[1][0]) + (red2[2][0] + red2[3][0]);
+        t = (red2[0][1] + red2[1][1]) + (red2[2][1] + red2[3][1]);
+        p.part[blk] = make_float4(m, s, t, 0.f);
+    }
+    if (!p.top) return;
+    unsigned long long *out = p.cand + blk * p.top;
+    const int n = ncand;
+    if (n <= kCand) {
+        for (int i = tid; i < n; i += kThreads) {
+            const unsigned long long k = cand[i];
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += cand[j] > k ? 1 : 0;
+            if (rank < p.top) out[rank] = k;
+        }
+        for (int i = n + tid; i < p.top; i += kThreads) out[i] = 0;
+        return;
+    }
+    unsigned long long last = ~0ull;
+    for (int k = 0; k < p.top; ++k) {
+        unsigned long long best = 0;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = raw_f32(r[i], e);
+                const unsigned long long q = entry(v, base + (i * kThreads + tid) * 8 + e);
+                if (v > -INFINITY && q < last && q > best) best = q;
+            }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) {
+            const unsigned long long q = __shfl_xor(best, o);
+            best = q > best ? q : best;
+        }
+        if (lane == 0) pick[wave] = best;
+        lds_barrier();
+        best = pick[0];
+        for (int i = 1; i < 4; ++i) best = pick[i] > best ? pick[i] : best;
+        if (tid == 0) out[k] = best;
+        last = best;
+        lds_barrier();  // every wave has read the picks before the next round writes them
+    }
+}
+
+// One wave per row: joins the slices.  An alternative's rank is the number of better ones in all slices, each
+// of which is sorted: the count walks a slice's list only as far as it is better.
+template <typename T>
+__global__ __launch_bounds__(64) void logprobs_join(LpParams p) {
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x;
+    const float4 *part = p.part + row * p.nsl;
+    float M = -INFINITY;
+    for (int i = lane; i < p.nsl; i += 64) M = fmaxf(M, part[i].x);
+    M = wave_max(M);
+    float s = 0.f, t = 0.f;
+    for (int i = lane; i < p.nsl; i += 64) {
+        const float4 q = part[i];
+        // a slice of nothing but -inf has s = t = 0, or NaN where it holds one: taken as it is
+        const bool none = q.x == -INFINITY;
+        const float d = none ? 0.f : (q.x - M) * p.c, f = none ? 1.f : __builtin_amdgcn_exp2f(d);
+        s = fmaf(q.y, f, s);
+        t = fmaf(f, fmaf(q.y, fmaxf(d, -200.f), q.z), t);
+    }
+    s = wave_sum(s), t = wave_sum(t);
+    const bool empty = s == 0.f;
+    const float ls = __builtin_amdgcn_logf(s);
+    if (lane == 0) {
+        p.stats[2 * row] = M;
+        p.stats[2 * row + 1] = ls * kLn2;
+        p.entropy[row] = empty ? 0.f : (ls - t / s) * kLn2;
+        const int64_t y = p.targets[row];
+        float lp = 0.f;
+        if (y >= 0 && y < p.vocab) {
+            const float v = Io<T>::f32(((const T *)p.x)[row * p.stride + y]);
+            lp = empty ? -INFINITY : fmaf(v - M, p.c, -ls) * kLn2;
+        }
+        p.logprob[row] = lp;
+    }
+    if (!p.top) return;
+    const unsigned long long *cand = p.cand + row * p.nsl * p.top;
+    const int n = p.nsl * p.top;
+    float *val = p.top_logprob + row * p.top;
+    int64_t *idx = p.top_index + row * p.top;
+    const bool nan = s != s;
+    int have = 0;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const int i = i0 + lane;
+        const unsigned long long k = i < n ? cand[i] : 0;
+        have += __popcll(__ballot(k != 0));
+        if (k == 0 || nan) continue;
+        int rank = i % p.top;  // the better ones of its own slice come before it
+        const int own = i / p.top;
+        for (int q = 0; q < p.nsl && rank < p.top; ++q) {
+            if (q == own) continue;
+            for (int j = 0; j < p.top && rank < p.top && cand[q * p.top + j] > k; ++j) ++rank;
+        }
+        if (rank < p.top) {
+            const float v = value_of((uint32_t)(k >> 32));
+            val[rank] = fmaf(v - M, p.c, -ls) * kLn2;
+            idx[rank] = (int64_t)(uint32_t)~(uint32_t)k;
+        }
+    }
+    // fewer logits with a probability than alternatives asked for; or none of a row with a NaN
+    for (int i = (nan ? 0 : have) + lane; i < p.top; i += 64) {
+        val[i] = nan ? NAN : -INFINITY;
+        idx[i] = -1;
+    }
+}
+
+constexpr int kBwdPieces = 4;
+
+// gradient: reads a logit, writes its gradient; HBM bound
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
+    const int64_t blk = blockIdx.x, row = blk / p.nsl;
+    const int base = (int)(blk - row * p.nsl) * (kBwdPieces * kThreads * 8);
+    const T *x = (const T *)p.x + row * p.stride;
+    T *dx = (T *)p.dx + row * p.vocab;
+    const int64_t y = p.targets[row];
+    const bool valid = y >= 0 && y < p.vocab;
+    const float gl = p.dlogprob && valid ? p.dlogprob[row] * p.scale : 0.f;
+    const float gh = p.dentropy ? p.dentropy[row] * p.scale : 0.f;
+    const float m = p.in_stats[2 * row], ls = p.in_stats[2 * row + 1] * kLog2e;
+    const bool empty = m == -INFINITY && !(ls != ls);
+    // -gl p - gh p (ln 2 a + H) = p (k0 + k1 a), a = log2 p
+    const float k0 = -fmaf(gh, p.in_entropy[row], gl), k1 = -gh * kLn2;
+    Raw8<T> r[kBwdPieces];
+#pragma unroll
+    for (int i = 0; i < kBwdPieces; ++i) r[i] = load_logits(x, base + (i * kThreads + (int)threadIdx.x) * 8, p.vocab);
+#pragma unroll
+    for (int i = 0; i < kBwdPieces; ++i) {
+        const int at = base + (i * kThreads + (int)threadIdx.x) * 8;
+        if (at >= p.vocab) break;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = fmaf(raw_f32(r[i], e) - m, p.c, -ls);
+            v[e] = empty ? 0.f : __builtin_amdgcn_exp2f(a) * fmaf(k1, fmaxf(a, -200.f), k0);
+        }
+        const int64_t hot = y - at;
+        if (valid && !empty && hot >= 0 && hot < 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += e == hot ? gl : 0.f;
+        }
+        if (at + 8 <= p.vocab) {
+            store_any8(dx + at, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e < p.vocab) dx[at + e] = Io<T>::to(v[e]);
+        }
+    }
+}
+
+// 8-logit pieces per thread of a slice: 8 (16,384 logits), or 2 where slices that long would leave the chip's
+// compute units without four workgroups each
+int pieces_for(int64_t rows, int64_t vocab) {
+    const int64_t big = 8 * kThreads * 8;
+    return rows * ((vocab + big - 1) / big) >= 1024 ? 8 : 2;
+}
+int64_t slices_for(int64_t rows, int64_t vocab) {
+    const int64_t n = (int64_t)pieces_for(rows, vocab) * kThreads * 8;
+    return (vocab + n - 1) / n;
+}
+
+int lp_check(const void *logits, int64_t stride, const int64_t *targets, float scale, int64_t rows, int64_t vocab, int dtype) {
+    if (rows < 0 || vocab < 0) return SELSCAN_E_SHAPE;
+    if (!io_known(dtype) || !(scale > 0.f) || !(scale < INFINITY) || vocab > (1 << 30)) return SELSCAN_E_UNSUPPORTED;
+    if (rows == 0 || vocab == 0) return SELSCAN_OK;
+    if (stride < vocab || mul_size(rows, stride) < 0) return SELSCAN_E_SHAPE;
+    if (!logits || !targets) return SELSCAN_E_NULL;
+    if (!span_aligned(logits, io_bytes(dtype)) || !span_aligned(targets, 8)) return SELSCAN_E_ALIGN;
+    return SELSCAN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
+    if (rows <= 0 || vocab <= 0 || vocab > (1 << 30) || top < 0 || top > kMaxTop) return 0;
+    const size_t n = (size_t)rows * (size_t)slices_for(rows, vocab);
+    return n * (sizeof(float4) + (size_t)top * 8);
+}
+
+int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t *targets, float scale, int top,
+                       float *logprob, float *entropy, float *stats, float *top_logprob, int64_t *top_index, int64_t rows,
+                       int64_t vocab, int io_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = lp_check(logits, logits_stride, targets, scale, rows, vocab, io_dtype);
+    if (rc != SELSCAN_OK) return rc;
+    if (top < 0 || top > kMaxTop) return SELSCAN_E_UNSUPPORTED;
+    if (rows == 0) return SELSCAN_OK;
+    if (vocab == 0 || top > vocab) return SELSCAN_E_SHAPE;
+    if (!logprob || !entropy || !stats || (top && (!top_logprob || !top_index))) return SELSCAN_E_NULL;
+    if (!span_aligned(logprob, 4) || !span_aligned(entropy, 4) || !span_aligned(stats, 4) ||
+        (top && (!span_aligned(top_logprob, 4) || !span_aligned(top_index, 8))) || !span_aligned(workspace, 16))
+        return SELSCAN_E_ALIGN;
+    const size_t need = token_logprobs_workspace_bytes(rows, vocab, top);
+    if (!workspace || workspace_bytes < need) return SELSCAN_E_WORKSPACE;
+    const Span in[] = {{logits, strided_bytes(rows, vocab, logits_stride, io_bytes(io_dtype))}, {targets, (size_t)rows * 8}};
+    const Span out[] = {{logprob, (size_t)rows * 4},
+                        {entropy, (size_t)rows * 4},
+                        {stats, (size_t)rows * 8},
+                        {top ? top_logprob : nullptr, (size_t)rows * top * 4},
+                        {top ? top_index : nullptr, (size_t)rows * top * 8},
+                        {workspace, need}};
+    if (any_alias(in, 2, out, 6)) return SELSCAN_E_ALIAS;
+    LpParams p{};
+    p.x = logits, p.targets = targets, p.logprob = logprob, p.entropy = entropy, p.stats = stats;
+    p.top_logprob = top_logprob, p.top_index = top_index;
+    p.rows = rows, p.stride = logits_stride, p.vocab = (int)vocab, p.top = top;
+    p.scale = scale, p.c = scale * kLog2e;
+    const int pieces = pieces_for(rows, vocab);
+    p.nsl = (int)slices_for(rows, vocab);
+    const int64_t blocks = rows * p.nsl;
+    if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    p.part = (float4 *)workspace;
+    p.cand = (unsigned long long *)(p.part + blocks);
+    const bool bf = io_dtype == SELSCAN_BF16;
+    void (*k)(LpParams) = pieces == 8 ? (bf ? logprobs_slice<uint16_t, 8> : logprobs_slice<float, 8>)
+                                      : (bf ? logprobs_slice<uint16_t, 2> : logprobs_slice<float, 2>);
+    rc = enqueue(k, dim3((unsigned)blocks), dim3(kThreads), p, stream);
+    if (rc != SELSCAN_OK) return rc;
+    return enqueue(bf ? logprobs_join<uint16_t> : logprobs_join<float>, dim3((unsigned)rows), dim3(64), p, stream);
+}
+
+int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t *targets, const float *stats,
+                       const float *entropy, const float *dlogprob, const float *dentropy, float scale, void *dlogits,
+                       int64_t rows, int64_t vocab, int io_dtype, void *stream) {
+    const int rc = lp_check(logits, logits_stride, targets, scale, rows, vocab, io_dtype);
+    if (rc != SELSCAN_OK) return rc;
+    if (rows == 0 || vocab == 0) return SELSCAN_OK;
+    if (!stats || !entropy || (!dlogprob && !dentropy) || !dlogits) return SELSCAN_E_NULL;
+    const size_t s = io_bytes(io_dtype);
+    if (!span_aligned(stats, 4) || !span_aligned(entropy, 4) || !span_aligned(dlogprob, 4) || !span_aligned(dentropy, 4) ||
+        !span_aligned(dlogits, s))
+        return SELSCAN_E_ALIGN;
+    const Span in[] = {{logits, strided_bytes(rows, vocab, logits_stride, s)},
+                       {targets, (size_t)rows * 8},
+                       {stats, (size_t)rows * 8},
+                       {entropy, (size_t)rows * 4},
+                       {dlogprob, (size_t)rows * 4},
+                       {dentropy, (size_t)rows * 4}};
+    const Span out[] = {{dlogits, (size_t)rows * vocab * s}};
+    if (any_alias(in, 6, out, 1)) return SELSCAN_E_ALIAS;
+    LpParams p{};
+    p.x = logits, p.targets = targets, p.in_stats = stats, p.in_entropy = entropy, p.dlogprob = dlogprob, p.dentropy = dentropy;
+    p.dx = dlogits, p.rows = rows, p.stride = logits_stride, p.vocab = (int)vocab;
+    p.scale = scale, p.c = scale * kLog2e;
+    const int64_t per = kBwdPieces * kThreads * 8;
+    p.nsl = (int)((vocab + per - 1) / per);
+    const int64_t blocks = rows * p.nsl;
+    if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    return enqueue(io_dtype == SELSCAN_BF16 ? logprobs_bwd<uint16_t> : logprobs_bwd<float>, dim3((unsigned)blocks), dim3(kThreads),
+                   p, stream);
+}
+
+}  // extern "C"

@@ -44,6 +44,9 @@ def _load(path=None):
     sig("add_rms_norm_fwd", [vp, i64, vp, vp, cf, ci] + [vp] * 4 + [i64, i64, ci, ci, vp])
     sig("add_rms_norm_bwd", [vp] * 8 + [i64, i64, ci, ci, vp, sz, vp])
     sig("add_rms_norm_bwd_workspace_bytes", [i64, i64], sz)
+    sig("token_logprobs_fwd", [vp, i64, vp, cf, ci] + [vp] * 5 + [i64, i64, ci, vp, sz, vp])
+    sig("token_logprobs_workspace_bytes", [i64, i64, ci], sz)
+    sig("token_logprobs_bwd", [vp, i64] + [vp] * 5 + [cf, vp, i64, i64, ci, vp])
     sig("selscan_lm_abi_version", [])
     sig("selscan_lm_last_hip_error", [], ctypes.c_char_p)
     return lib
@@ -298,3 +301,51 @@ def add_rms_norm_bwd(dy, s, weight, rstd, x_dtype=None, dresidual_out=None, work
     if g["dresidual"] is None:
         g["dresidual"] = g["dx"]
     return g
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0) -> int:
+    return int(lm_lib.token_logprobs_workspace_bytes(rows, vocab, top))
+
+
+@_on_launch_stream
+def token_logprobs_fwd(logits, targets, top=0, scale=1.0, workspace=None, stream=None):
+    """Log probability of targets (int64 [rows]; outside [0, vocab): 0) under softmax(scale * logits), logits
+    [rows, vocab], and the entropy.  Returns (logprob, entropy, stats), fp32 [rows], [rows] and [rows, 2]
+    (the largest logit; log sum exp of scale * (logits - it)), and with top > 0 also (top_logprob fp32,
+    top_index int64), [rows, top], largest first, equal logits by index."""
+    torch = _torch()
+    rows, vocab = logits.shape
+    io = logits.dtype
+    _shape_check("targets", targets, (rows,))
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    out = [torch.empty(rows, **f32), torch.empty(rows, **f32), torch.empty(rows, 2, **f32)]
+    if top:
+        out += [torch.empty(rows, top, **f32), torch.empty(rows, top, dtype=torch.int64, device=logits.device)]
+    val, idx = out[3:] if top else (None, None)
+    ws, wsb, _keep = _workspace(token_logprobs_workspace_bytes(rows, vocab, top), workspace, logits.device)
+    xp, xs = _rows(logits, "logits", io)
+    rc = lm_lib.token_logprobs_fwd(xp, xs, _typed(targets, "targets", torch.int64), scale, top, _ptr(out[0], "logprob"),
+                                   _ptr(out[1], "entropy"), _ptr(out[2], "stats"), _ptr(val, "top_logprob"),
+                                   _ptr(idx, "top_index"), rows, vocab, _dtype_code(logits), ws, wsb, _stream(stream))
+    _check(rc, "token_logprobs_fwd")
+    return tuple(out)
+
+
+@_on_launch_stream
+def token_logprobs_bwd(logits, targets, stats, entropy, dlogprob=None, dentropy=None, scale=1.0, stream=None):
+    """Gradient of sum(dlogprob * logprob + dentropy * entropy) for the logits (contiguous, their dtype); stats and
+    entropy from token_logprobs_fwd with the same scale; dlogprob, dentropy fp32 [rows], one at least."""
+    torch = _torch()
+    rows, vocab = logits.shape
+    io = logits.dtype
+    for n_, t_ in (("targets", targets), ("entropy", entropy), ("dlogprob", dlogprob), ("dentropy", dentropy)):
+        _shape_check(n_, t_, (rows,))
+    _shape_check("stats", stats, (rows, 2))
+    dx = torch.empty(rows, vocab, dtype=io, device=logits.device)
+    xp, xs = _rows(logits, "logits", io)
+    rc = lm_lib.token_logprobs_bwd(xp, xs, _typed(targets, "targets", torch.int64), _ptr(stats, "stats", f32=True),
+                                   _ptr(entropy, "entropy", f32=True), _ptr(dlogprob, "dlogprob", f32=True),
+                                   _ptr(dentropy, "dentropy", f32=True), scale, _ptr(dx, "dlogits"), rows, vocab,
+                                   _dtype_code(logits), _stream(stream))
+    _check(rc, "token_logprobs_bwd")
+    return dx

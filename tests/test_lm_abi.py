@@ -144,3 +144,37 @@ def test_norm_bwd_refusals():
     assert norm_bwd(wsb=need - 1) == WORKSPACE and norm_bwd(ws=None) == WORKSPACE
     assert norm_bwd(ws=P + 7 * MB + 4) == ALIGN and norm_bwd(s=P + MB + 2) == ALIGN
     assert norm_bwd(dx=P) == ALIAS and norm_bwd(dr=P + 4 * MB) == ALIAS and norm_bwd(ws=P + 6 * MB) == ALIAS
+
+
+def lp_fwd(x=P, xs=100, t=P + MB, scale=1.0, top=0, lp=P + 2 * MB, ent=P + 3 * MB, st=P + 4 * MB, tv=None, ti=None, rows=4,
+           vocab=100, dt=1, ws=P + 5 * MB, wsb=MB):
+    return L.token_logprobs_fwd(x, xs, t, scale, top, lp, ent, st, tv, ti, rows, vocab, dt, ws, wsb, None)
+
+
+def test_logprobs_refusals():
+    for kw in ("x", "t", "lp", "ent", "st"):
+        assert lp_fwd(**{kw: None}) == NULL, kw
+    assert lp_fwd(top=3) == NULL
+    assert lp_fwd(rows=-1) == SHAPE and lp_fwd(vocab=-1) == SHAPE and lp_fwd(xs=99) == SHAPE
+    assert lp_fwd(vocab=0) == SHAPE and lp_fwd(rows=0) == OK
+    assert lp_fwd(top=30, vocab=20, tv=P + 6 * MB, ti=P + 7 * MB) == SHAPE
+    assert lp_fwd(top=33) == UNSUPPORTED and lp_fwd(top=-1) == UNSUPPORTED and lp_fwd(dt=4) == UNSUPPORTED
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert lp_fwd(scale=s) == UNSUPPORTED
+    assert lp_fwd(t=P + MB + 4) == ALIGN and lp_fwd(ws=P + 5 * MB + 8) == ALIGN and lp_fwd(x=P + 1) == ALIGN
+    need = S.token_logprobs_workspace_bytes(4, 100, 0)
+    assert need > 0 and lp_fwd(wsb=need - 1) == WORKSPACE and lp_fwd(ws=None) == WORKSPACE
+    assert lp_fwd(lp=P + 8) == ALIAS and lp_fwd(ent=P + 2 * MB) == ALIAS and lp_fwd(ws=P + 4 * MB) == ALIAS
+
+
+def lp_bwd(x=P, xs=100, t=P + MB, st=P + 2 * MB, ent=P + 3 * MB, dl=P + 4 * MB, dh=None, scale=1.0, dx=P + 5 * MB, rows=4,
+           vocab=100, dt=1):
+    return L.token_logprobs_bwd(x, xs, t, st, ent, dl, dh, scale, dx, rows, vocab, dt, None)
+
+
+def test_logprobs_bwd_refusals():
+    for kw in ("x", "t", "st", "ent", "dl", "dx"):
+        assert lp_bwd(**{kw: None}) == NULL, kw
+    assert lp_bwd(rows=0) == OK and lp_bwd(vocab=0) == OK
+    assert lp_bwd(xs=10) == SHAPE and lp_bwd(scale=0.0) == UNSUPPORTED
+    assert lp_bwd(dx=P + 1) == ALIGN and lp_bwd(dx=P) == ALIAS
