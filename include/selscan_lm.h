@@ -5,7 +5,8 @@
  *   - the short causal convolution and the selective scan on packed prompts of different
  *     lengths, with each prompt's state kept in a cache, and on one token per sequence;
  *   - residual addition + root-mean-square norm, with an 8-bit output, and its gradients;
- *   - log probability of a token, entropy and top alternatives from logits, and their gradient.
+ *   - log probability of a token, entropy and top alternatives from logits, and their gradient;
+ *   - a few rows times a 4-bit weight matrix with group scales.
  *
  * Conventions: those of selscan.h (status codes, device pointers owned by the caller, work only
  * enqueued on `stream`, nothing allocated or kept by the library, host validation before any HIP
@@ -175,6 +176,21 @@ size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
 int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t *targets, const float *stats,
                        const float *entropy, const float *dlogprob, const float *dentropy, float scale, void *dlogits,
                        int64_t rows, int64_t vocab, int io_dtype, void *stream);
+
+/*
+ * w4_matvec - y[r][j] = bias[j] + sum_k x[r][k] * (q[j][k] - zero[j][k / group]) * scale[j][k / group]
+ *   x       : [rows][k] io_dtype, row stride x_stride
+ *   qweight : [n][k / 2] bytes, 16-byte aligned: q[j][2i] in the low, q[j][2i+1] in the high 4 bits
+ *             of byte i, unsigned (0..15)
+ *   scales  : [n][k / group] bf16;  zeros : [n][k / group] bytes, the low 4 bits count, nullable (8)
+ *   bias    : [n] fp32, nullable;  y : [rows][n] io_dtype
+ *   group   : 32, 64 or 128 (SELSCAN_E_UNSUPPORTED), dividing k (SELSCAN_E_SHAPE)
+ * The products and sums of a group are exact up to fp32 accumulation; fp32 x is not rounded.
+ * Meant for few rows; any number is computed, 32 at a time per pass over the weights.
+ */
+int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *scales, const void *zeros,
+              const float *bias, void *y, int64_t rows, int64_t n, int64_t k, int64_t group, int io_dtype,
+              void *stream);
 
 int selscan_lm_abi_version(void);
 /* text of the calling thread's most recent launch that the HIP runtime rejected */

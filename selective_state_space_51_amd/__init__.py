@@ -683,4 +683,4 @@ def dwconv2d_bwd(x, weight, H, W, dout, bias=None, silu=True, workspace=None, st
 from .lm import (  # noqa: E402
     LM_HEADER, LM_LIB_PATH, add_rms_norm_bwd, add_rms_norm_bwd_workspace_bytes, add_rms_norm_fwd, causal_conv1d_packed_fwd, causal_conv1d_step, lm_abi_version, lm_lib, selscan_packed_fwd,
     selscan_packed_workspace_bytes, selscan_step, token_logprobs_bwd, token_logprobs_fwd,
-    token_logprobs_workspace_bytes)
+    token_logprobs_workspace_bytes, w4_matvec)

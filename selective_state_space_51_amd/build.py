@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("selscan_fwd.hip", "selscan_bwd.hip", "selscan_conv.hip")]
 OUT = os.path.join(PKG, "libselscan.so")
-LM_SRCS = [os.path.join(CSRC, f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logprobs.hip")]
+LM_SRCS = [os.path.join(CSRC, f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logprobs.hip", "lm_w4.hip")]
 LM_OUT = os.path.join(PKG, "libselscan_lm.so")
 UBENCH_SRCS = [os.path.join(CSRC, "ubench.hip")]
 UBENCH_OUT = os.path.join(PKG, "libselscan_ubench.so")

@@ -39,10 +39,10 @@ inline bool any_alias(const Span *in, int nin, const Span *out, int nout) {
 }
 
 template <class P>
-int enqueue(void (*kernel)(P), dim3 grid, dim3 block, const P &p, void *stream) {
+int enqueue(void (*kernel)(P), dim3 grid, dim3 block, const P &p, void *stream, unsigned lds = 0) {
     P copy = p;
     void *args[] = {&copy};
-    const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, args, 0, (hipStream_t)stream);
+    const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, args, lds, (hipStream_t)stream);
     if (e != hipSuccess) {
         record_hip_error(e);
         return SELSCAN_E_HIP;
@@ -61,6 +61,34 @@ __device__ __forceinline__ float4 load_f4(const float *p) {
     };
     const U u = *(const U *)p;
     return make_float4(u.a, u.b, u.c, u.d);
+}
+
+// 8 elements from any address aligned to the element
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_any8(const T *p) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U {
+        uint32_t w[sizeof(T) * 2];
+    };
+    const U u = *(const U *)p;
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 2; ++i) r.w[i] = u.w[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_any8(T *p, const float (&v)[8]) {
+    struct __attribute__((packed, aligned(sizeof(T)))) U {
+        uint32_t w[sizeof(T) * 2];
+    };
+    U u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.w[i] = Io<T>::to2(v[2 * i], v[2 * i + 1]);
+    }
+    *(U *)p = u;
 }
 
 __device__ __forceinline__ float wave_sum(float v) {

@@ -29,34 +29,6 @@ struct LpParams {
     float c, scale;
 };
 
-// 8 elements from any address aligned to the element
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_any8(const T *p) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U {
-        uint32_t w[sizeof(T) * 2];
-    };
-    const U u = *(const U *)p;
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) * 2; ++i) r.w[i] = u.w[i];
-    return r;
-}
-template <typename T>
-__device__ __forceinline__ void store_any8(T *p, const float (&v)[8]) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U {
-        uint32_t w[sizeof(T) * 2];
-    };
-    U u;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u.w[i] = __float_as_uint(v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u.w[i] = Io<T>::to2(v[2 * i], v[2 * i + 1]);
-    }
-    *(U *)p = u;
-}
-
 // elements [at, at + 8) of a row of n; those past its end are -inf
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_logits(const T *row, int at, int n) {

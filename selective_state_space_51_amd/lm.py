@@ -47,6 +47,7 @@ def _load(path=None):
     sig("token_logprobs_fwd", [vp, i64, vp, cf, ci] + [vp] * 5 + [i64, i64, ci, vp, sz, vp])
     sig("token_logprobs_workspace_bytes", [i64, i64, ci], sz)
     sig("token_logprobs_bwd", [vp, i64] + [vp] * 5 + [cf, vp, i64, i64, ci, vp])
+    sig("w4_matvec", [vp, i64] + [vp] * 5 + [i64] * 4 + [ci, vp])
     sig("selscan_lm_abi_version", [])
     sig("selscan_lm_last_hip_error", [], ctypes.c_char_p)
     return lib
@@ -349,3 +350,28 @@ def token_logprobs_bwd(logits, targets, stats, entropy, dlogprob=None, dentropy=
                                    _dtype_code(logits), _stream(stream))
     _check(rc, "token_logprobs_bwd")
     return dx
+
+
+@_on_launch_stream
+def w4_matvec(x, qweight, scales, zeros=None, group=128, bias=None, out=None, stream=None):
+    """x [rows, k] times the transpose of a 4-bit matrix: qweight uint8 [n, k // 2] (q[2i] in the low, q[2i+1] in the
+    high bits of byte i), weight (q - zero) * scale with scales bf16 and zeros uint8 (None: 8), [n, k // group]
+    each; bias fp32 [n].  Returns [rows, n] in x's dtype."""
+    torch = _torch()
+    rows, k = x.shape
+    n = qweight.shape[0]
+    io = x.dtype
+    if group <= 0 or k % group:
+        raise ValueError(f"group {group} does not divide k = {k}")
+    for n_, t_, s_ in (("qweight", qweight, (n, k // 2)), ("scales", scales, (n, k // group)),
+                       ("zeros", zeros, (n, k // group)), ("bias", bias, (n,))):
+        _shape_check(n_, t_, s_)
+    if out is None:
+        out = torch.empty(rows, n, dtype=io, device=x.device)
+    _shape_check("out", out, (rows, n))
+    xp, xs = _rows(x, "x", io)
+    rc = lm_lib.w4_matvec(xp, xs, _typed(qweight, "qweight", torch.uint8), _typed(scales, "scales", torch.bfloat16),
+                          _typed(zeros, "zeros", torch.uint8), _ptr(bias, "bias", f32=True), _ptr(out, "out", io), rows, n,
+                          k, group, _dtype_code(x), _stream(stream))
+    _check(rc, "w4_matvec")
+    return out

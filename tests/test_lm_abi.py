@@ -178,3 +178,17 @@ def test_logprobs_bwd_refusals():
     assert lp_bwd(rows=0) == OK and lp_bwd(vocab=0) == OK
     assert lp_bwd(xs=10) == SHAPE and lp_bwd(scale=0.0) == UNSUPPORTED
     assert lp_bwd(dx=P + 1) == ALIGN and lp_bwd(dx=P) == ALIAS
+
+
+def w4(x=P, xs=256, q=P + MB, s=P + 2 * MB, z=None, b=None, y=P + 4 * MB, rows=2, n=64, k=256, group=64, dt=1):
+    return L.w4_matvec(x, xs, q, s, z, b, y, rows, n, k, group, dt, None)
+
+
+def test_w4_refusals():
+    for kw in ("x", "q", "s", "y"):
+        assert w4(**{kw: None}) == NULL, kw
+    assert w4(rows=-1) == SHAPE and w4(k=0) == SHAPE and w4(k=96) == SHAPE and w4(xs=255) == SHAPE
+    assert w4(rows=0) == OK and w4(n=0) == OK
+    assert w4(group=16) == UNSUPPORTED and w4(dt=5) == UNSUPPORTED
+    assert w4(q=P + MB + 8) == ALIGN and w4(s=P + 2 * MB + 1) == ALIGN and w4(b=P + 3 * MB + 2) == ALIGN
+    assert w4(y=P) == ALIAS and w4(y=P + MB) == ALIAS and w4(z=P + 4 * MB + 16) == ALIAS
