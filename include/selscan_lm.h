@@ -129,6 +129,9 @@ int add_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, cons
  *     dweight[c] = sum_rows dy * xhat
  *   dy             : [rows][width] io_dtype
  *   s              : [rows][width] residual_dtype, the forward's residual_out;  rstd : its rstd
+ *   x              : [rows][width] io_dtype, row stride x_stride, nullable.  Given, the sum is formed anew as
+ *                    x + s, with s the forward's residual instead: for a residual_out rounded to 16 bits, which is
+ *                    not the sum that was normed (its rounding, 2^-9, would go into dweight)
  *   dresidual_out  : [rows][width] residual_dtype, nullable (no gradient through residual_out)
  *   dx             : [rows][width] io_dtype, nullable;  dresidual : [rows][width] residual_dtype,
  *                    nullable (both are ds, each in its type)
@@ -136,9 +139,10 @@ int add_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, cons
  *   workspace      : add_rms_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (per-workgroup
  *                    sums of dweight); required with dweight
  */
-int add_rms_norm_bwd(const void *dy, const void *s, const float *weight, const float *rstd, const void *dresidual_out,
-                     void *dx, void *dresidual, float *dweight, int64_t rows, int64_t width, int io_dtype,
-                     int residual_dtype, void *workspace, size_t workspace_bytes, void *stream);
+int add_rms_norm_bwd(const void *dy, const void *s, const void *x, int64_t x_stride, const float *weight,
+                     const float *rstd, const void *dresidual_out, void *dx, void *dresidual, float *dweight,
+                     int64_t rows, int64_t width, int io_dtype, int residual_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
 size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
 
 /*

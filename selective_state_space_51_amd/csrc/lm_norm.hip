@@ -12,6 +12,7 @@ struct NormParams {
     const float *weight;
     void *y, *residual_out;    // backward: dx, dresidual
     const void *dres;          // backward: gradient of residual_out
+    const void *add;           // backward: x, where the sum is formed anew; row stride x_stride
     float *scale, *rstd;       // backward: rstd is read
     float *partial;            // backward: [slots][width] sums of dweight
     int64_t rows, x_stride;
@@ -195,6 +196,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd(NormParams p) 
             load_piece<T, TPR, VEC>((const T *)p.x + at, v, tr, p.width, g[v]);
             load_piece<R, TPR, VEC>((const R *)p.residual + at, v, tr, p.width, xh[v]);
         }
+        if (p.add) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                float a[8];
+                load_piece<T, TPR, VEC>((const T *)p.add + row * p.x_stride, v, tr, p.width, a);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xh[v][e] += a[e];
+            }
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -338,26 +348,30 @@ size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width) {
     return (size_t)bwd_slots(rows, width) * (size_t)width * sizeof(float);
 }
 
-int add_rms_norm_bwd(const void *dy, const void *s, const float *weight, const float *rstd, const void *dresidual_out,
-                     void *dx, void *dresidual, float *dweight, int64_t rows, int64_t width, int io_dtype,
-                     int residual_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+int add_rms_norm_bwd(const void *dy, const void *s, const void *x, int64_t x_stride, const float *weight,
+                     const float *rstd, const void *dresidual_out, void *dx, void *dresidual, float *dweight,
+                     int64_t rows, int64_t width, int io_dtype, int residual_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream) {
     int rc = norm_sizes(rows, width, io_dtype, residual_dtype);
     if (rc != SELSCAN_OK) return rc;
     if (width == 0 || (rows == 0 && !dweight)) return SELSCAN_OK;
+    if (x && (x_stride < width || mul_size(rows, x_stride) < 0)) return SELSCAN_E_SHAPE;
     if (rows > 0 && (!dy || !s || !weight || !rstd)) return SELSCAN_E_NULL;
     const size_t b = io_bytes(io_dtype), r = io_bytes(residual_dtype);
     const size_t need = dweight ? add_rms_norm_bwd_workspace_bytes(rows, width) : 0;
-    if (!span_aligned(dy, b) || !span_aligned(dx, b) || !span_aligned(s, r) || !span_aligned(dresidual_out, r) ||
+    if (!span_aligned(dy, b) || !span_aligned(x, b) || !span_aligned(dx, b) || !span_aligned(s, r) || !span_aligned(dresidual_out, r) ||
         !span_aligned(dresidual, r) || !span_aligned(weight, 4) || !span_aligned(rstd, 4) || !span_aligned(dweight, 4) ||
         (need && !span_aligned(workspace, 16)))
         return SELSCAN_E_ALIGN;
     if (need && (!workspace || workspace_bytes < need)) return SELSCAN_E_WORKSPACE;
     const size_t n = (size_t)rows * width;
-    const Span in[] = {{dy, n * b}, {s, n * r}, {weight, (size_t)width * 4}, {rstd, (size_t)rows * 4}, {dresidual_out, n * r}};
+    const Span in[] = {{dy, n * b}, {s, n * r}, {weight, (size_t)width * 4}, {rstd, (size_t)rows * 4}, {dresidual_out, n * r},
+                       {x, strided_bytes(rows, width, x_stride, b)}};
     const Span out[] = {{dx, n * b}, {dresidual, n * r}, {dweight, (size_t)width * 4}, {need ? workspace : nullptr, need}};
-    if (any_alias(in, 5, out, 4)) return SELSCAN_E_ALIAS;
+    if (any_alias(in, 6, out, 4)) return SELSCAN_E_ALIAS;
     NormParams p{};
     p.x = dy, p.residual = s, p.weight = weight, p.y = dx, p.residual_out = dresidual, p.dres = dresidual_out;
+    p.add = x, p.x_stride = x_stride;
     p.rstd = (float *)rstd, p.rows = rows, p.width = (int)width, p.inv_width = 1.f / (float)width;
     p.partial = dweight ? (float *)workspace : nullptr;
     p.slots = (int)bwd_slots(rows, width);
@@ -366,7 +380,7 @@ int add_rms_norm_bwd(const void *dy, const void *s, const float *weight, const f
         p.rows_per = (rows + p.slots - 1) / p.slots;
         p.slots = (int)((rows + p.rows_per - 1) / p.rows_per);
         const bool vec = width % 8 == 0 && span_aligned(dy, 16) && span_aligned(s, 16) && span_aligned(weight, 16) &&
-                         span_aligned(dresidual_out, 16) && span_aligned(dx, 16) && span_aligned(dresidual, 16);
+                         span_aligned(dresidual_out, 16) && span_aligned(dx, 16) && span_aligned(dresidual, 16) && (!x || (span_aligned(x, 16) && x_stride * b % 16 == 0));
         rc = launch_types<true>(p, io_dtype, residual_dtype, vec, stream);
         if (rc != SELSCAN_OK || !dweight) return rc;
     }

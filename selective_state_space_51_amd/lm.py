@@ -42,7 +42,7 @@ def _load(path=None):
     sig("selscan_packed_workspace_bytes", [i64] * 5, sz)
     sig("selscan_step", [vp] * 5 + [i64, vp, vp, i64, vp, cu] + [vp] * 3 + [i64] * 4 + [ci, vp])
     sig("add_rms_norm_fwd", [vp, i64, vp, vp, cf, ci] + [vp] * 4 + [i64, i64, ci, ci, vp])
-    sig("add_rms_norm_bwd", [vp] * 8 + [i64, i64, ci, ci, vp, sz, vp])
+    sig("add_rms_norm_bwd", [vp] * 3 + [i64] + [vp] * 6 + [i64, i64, ci, ci, vp, sz, vp])
     sig("add_rms_norm_bwd_workspace_bytes", [i64, i64], sz)
     sig("token_logprobs_fwd", [vp, i64, vp, cf, ci] + [vp] * 5 + [i64, i64, ci, vp, sz, vp])
     sig("token_logprobs_workspace_bytes", [i64, i64, ci], sz)
@@ -249,8 +249,9 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out="io", residual_dtyp
 
     residual: [rows, width], fp32 or x's dtype (None: s = x, kept as residual_dtype, by default x's).
     out: "io" (y in x's dtype), "int8" or "fp8" (e4m3; y stands for scale[:, None] * y).
-    Returns (y, s[, scale][, rstd]): s in the residual's dtype, scale fp32 [rows] for the 8-bit outputs, rstd
-    fp32 [rows] when asked for (add_rms_norm_bwd takes it)."""
+    Returns (y, s[, scale][, saved]): s in the residual's dtype, scale fp32 [rows] for the 8-bit outputs.
+    rstd=True adds what add_rms_norm_bwd needs beside s: rstd fp32 [rows]; where s was rounded to 16 bits, the
+    tuple (rstd, x, residual), since the sum that was normed is theirs and not the rounded one."""
     torch = _torch()
     rows, width = x.shape
     io = x.dtype
@@ -270,7 +271,8 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out="io", residual_dtyp
                                  _OUT_KINDS[out], _ptr(y, "y"), _ptr(s, "s"), _ptr(scale, "scale"), _ptr(rs, "rstd"),
                                  rows, width, _dtype_code(x), _dtype_code(s), _stream(stream))
     _check(rc, "add_rms_norm_fwd")
-    return (y, s) + ((scale,) if scale is not None else ()) + ((rs,) if rstd else ())
+    saved = (rs, x, residual) if residual is not None and rdt != torch.float32 else rs
+    return (y, s) + ((scale,) if scale is not None else ()) + ((saved,) if rstd else ())
 
 
 def add_rms_norm_bwd_workspace_bytes(rows: int, width: int) -> int:
@@ -279,14 +281,20 @@ def add_rms_norm_bwd_workspace_bytes(rows: int, width: int) -> int:
 
 @_on_launch_stream
 def add_rms_norm_bwd(dy, s, weight, rstd, x_dtype=None, dresidual_out=None, workspace=None, stream=None):
-    """Gradients of add_rms_norm_fwd's "io" output: dy [rows, width]; s and rstd from the forward; dresidual_out
-    the gradient that reaches s by the residual path (None: none).  Returns a dict: dx (x_dtype, which is dy's),
+    """Gradients of add_rms_norm_fwd's "io" output: dy [rows, width]; s and rstd (its rstd=True result, as it is)
+    from the forward; dresidual_out the gradient that reaches s by the residual path (None: none).  Returns a dict: dx (x_dtype, which is dy's),
     dresidual (the same numbers in s's dtype; dx itself where the dtypes agree) and dweight (fp32 [width])."""
     torch = _torch()
     rows, width = dy.shape
     io = dy.dtype
     if x_dtype not in (None, io):
         raise TypeError("dy must have x's dtype")
+    base, x = s, None
+    if isinstance(rstd, tuple):
+        rstd, x, base = rstd
+        _shape_check("x", x, (rows, width))
+        _shape_check("residual", base, (rows, width))
+    xp, xs = _rows(x, "x", io)
     for n_, t_, s_ in (("s", s, (rows, width)), ("weight", weight, (width,)), ("rstd", rstd, (rows,)),
                        ("dresidual_out", dresidual_out, (rows, width))):
         _shape_check(n_, t_, s_)
@@ -294,7 +302,7 @@ def add_rms_norm_bwd(dy, s, weight, rstd, x_dtype=None, dresidual_out=None, work
          "dresidual": torch.empty_like(s) if s.dtype != io else None,
          "dweight": torch.empty(width, dtype=torch.float32, device=dy.device)}
     ws, wsb, _keep = _workspace(add_rms_norm_bwd_workspace_bytes(rows, width), workspace, dy.device)
-    rc = lm_lib.add_rms_norm_bwd(_ptr(dy, "dy"), _ptr(s, "s"), _ptr(weight, "weight", f32=True),
+    rc = lm_lib.add_rms_norm_bwd(_ptr(dy, "dy"), _ptr(base, "s", s.dtype), xp, xs, _ptr(weight, "weight", f32=True),
                                  _ptr(rstd, "rstd", f32=True), _ptr(dresidual_out, "dresidual_out", s.dtype),
                                  _ptr(g["dx"], "dx"), _ptr(g["dresidual"], "dresidual"), _ptr(g["dweight"], "dweight"),
                                  rows, width, _dtype_code(dy), _dtype_code(s), ws, wsb, _stream(stream))

@@ -129,15 +129,16 @@ def test_norm_refusals():
     assert norm(ro=P + 16) == ALIAS
 
 
-def norm_bwd(dy=P, s=P + MB, w=P + 2 * MB, rstd=P + 3 * MB, dres=None, dx=P + 4 * MB, dr=P + 5 * MB, dw=P + 6 * MB, rows=8,
+def norm_bwd(dy=P, s=P + MB, x=None, xs=64, w=P + 2 * MB, rstd=P + 3 * MB, dres=None, dx=P + 4 * MB, dr=P + 5 * MB, dw=P + 6 * MB, rows=8,
              width=64, dt=1, rdt=0, ws=P + 7 * MB, wsb=MB):
-    return L.add_rms_norm_bwd(dy, s, w, rstd, dres, dx, dr, dw, rows, width, dt, rdt, ws, wsb, None)
+    return L.add_rms_norm_bwd(dy, s, x, xs, w, rstd, dres, dx, dr, dw, rows, width, dt, rdt, ws, wsb, None)
 
 
 def test_norm_bwd_refusals():
     for kw in ("dy", "s", "w", "rstd"):
         assert norm_bwd(**{kw: None}) == NULL, kw
-    assert norm_bwd(rows=-1) == SHAPE and norm_bwd(dt=9) == UNSUPPORTED
+    assert norm_bwd(rows=-1) == SHAPE and norm_bwd(dt=9) == UNSUPPORTED and norm_bwd(x=P + 9 * MB, xs=63) == SHAPE
+    assert norm_bwd(x=P + 9 * MB + 1) == ALIGN and norm_bwd(x=P + 4 * MB) == ALIAS
     assert norm_bwd(rows=0, dw=None) == OK
     need = S.add_rms_norm_bwd_workspace_bytes(8, 64)
     assert need == 8 * 64 * 4 and S.add_rms_norm_bwd_workspace_bytes(0, 64) == 0
