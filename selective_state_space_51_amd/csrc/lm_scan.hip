@@ -3,6 +3,8 @@
 // causal_conv1d_step, selscan_step of include/selscan_lm.h).  MI355X (gfx950).
 #include "lm_common.h"
 
+#include <type_traits>
+
 namespace selscan_rt {
 thread_local char g_last_hip_error[160] = "no error";
 }  // namespace selscan_rt
@@ -43,11 +45,17 @@ __device__ __forceinline__ int64_t slot_of(const Seqs &q, int s) {
 // from (cu[s] >> shift) + s to the next sequence's first, exclusively.  They are at least
 // ceil(len / 2^shift) and at least one (floor(a + b) + 1 >= ceil(b) + floor(a)), and all of them together at
 // most (tokens >> shift) + nseq, which the host knows; those past a sequence's end have nothing to do.
-// The sequence of a segment: the last one whose first segment is not after it, by a search 64
-// positions wide (one load for up to 64 sequences).  Every lane of the wave takes part.
-__device__ __forceinline__ int seq_of_segment(const Seqs &q, int seg, int shift, int lane) {
+struct Segment {
+    int s, t0, len;  // its sequence
+    int j;           // its number within the sequence (negative: none)
+};
+
+// The sequence of a segment is the last one whose first segment is not after it: a search 64 positions wide,
+// whose last round also brings the offsets themselves (one load in all for up to 64 sequences).  Every lane of
+// the wave takes part.
+__device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, int shift, int lane) {
     int lo = 0, n = q.nseq;
-    while (n > 1) {
+    while (n > 64) {
         const int step = (n + 63) >> 6, i = lane * step;
         const bool at_or_before = i < n && (cu_at(q, lo + i) >> shift) + lo + i <= seg;
         int c = __popcll(__ballot(at_or_before));
@@ -56,7 +64,12 @@ __device__ __forceinline__ int seq_of_segment(const Seqs &q, int seg, int shift,
         n -= (c - 1) * step;
         n = n < step ? n : step;
     }
-    return __builtin_amdgcn_readfirstlane(lo);
+    const int i = lane < n ? lane : n - 1;
+    const int a = cu_at(q, lo + i), b = cu_at(q, lo + i + 1);
+    int c = __popcll(__ballot(lane < n && (a >> shift) + lo + lane <= seg));
+    c = __builtin_amdgcn_readfirstlane(c < 1 ? 0 : c - 1);
+    const int s = lo + c, t0 = __builtin_amdgcn_readlane(a, c), t1 = __builtin_amdgcn_readlane(b, c);
+    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - (t0 >> shift) - s};
 }
 
 // ------------------------------------------------------------------------------------
@@ -136,10 +149,8 @@ template <typename T, int K>
 __global__ __launch_bounds__(256) void conv_packed(ConvParams p) {
     constexpr int R = 1 << kConvShift, B = sizeof(T) == 2 ? 8 : 4;  // B: rows in flight at a time
     const int seg = blockIdx.x;
-    const int s = seq_of_segment(p.q, seg, kConvShift, threadIdx.x & 63);
-    const Range rg = range_of(p.q, s);
-    const int j = seg - (rg.t0 >> kConvShift) - s;
-    const int first = j << kConvShift;
+    const Segment rg = find_segment(p.q, seg, kConvShift, threadIdx.x & 63);
+    const int s = rg.s, j = rg.j, first = j << kConvShift;
     if (j < 0 || (j > 0 && first >= rg.len)) return;
     const int64_t c0 = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
     if (c0 >= p.dim) return;
@@ -282,212 +293,272 @@ struct ScanParams {
     const float *A, *D, *bias;
     void *y;
     float *h;     // cache, or NULL
-    float *seg;   // split: [nsegs][dim][16] end state of a segment from zero, then the state it starts from
+    float *seg;   // split: [nsegs][dim][16] end state of a segment, from zero but for a sequence's first
     float *sdt;   // split: [nsegs][dim] sum of delta over the segment
     Seqs q;
     int64_t dim, bc_stride, z_stride;
     int softplus, shift;
+    int ntiles;    // blocks of 64 channels
+    int joined;    // split: scan_join runs between the launches
     int rows_per;  // step: rows a thread takes one after another
 };
 
-// B and C of one step as raw words, wave-uniform.  Scalar loads bring them to scalar registers (rows on 4-byte
-// boundaries); otherwise lanes 0-31 load one value each and they are read lane by lane.
-template <typename T>
-struct BcRaw {
-    static constexpr int NW = kN * (int)sizeof(T) / 4;
-    uint32_t b[NW], c[NW];
+// a value of another lane of the group of four: lane CTRL & 3, CTRL >> 2 & 3, ... of lanes 0, 1, 2, 3
+template <int CTRL>
+__device__ __forceinline__ float quad(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int I>
+__device__ __forceinline__ float quad_lane(float v) {
+    return quad<I * 0x55>(v);
+}
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;
+
+// The scan, one wave per 16 channels of a sequence or segment: the four lanes of a channel hold four of
+// its 16 states each and walk its tokens in order.
+//
+//  - Per (token, channel, state): mul, exp, mul, fma, fma.  What is done per token and channel (softplus, the
+//    gate, conversions, the store) is shared out: lane q of a channel does it for token q of every four, and
+//    the others read delta and delta x from it with DPP, as an operand of the products that use them.  The
+//    sums over states of four tokens are transposed and added across the four lanes at once.
+//  - B and C are the same for all channels: a block of 16 tokens of them is converted once per wave to fp32
+//    in LDS, and read back as one 16-byte broadcast each per token.  The wave reads only what it wrote itself,
+//    in order: no barrier.
+//  - The next block's x, delta, z, B and C are in flight during a block's arithmetic.
+//
+// Bound by instruction issue (about 31 VALU instructions and 2 LDS reads per token of a wave).  A lane per
+// channel with all 16 states and B and C as scalar operands needs a tenth less issue per element, but a
+// quarter of the waves, each token taking four times as long: measured slower wherever the chip was not full
+// of long sequences of equal length.
+//
+// The four waves of a workgroup take neighbouring channels, 128 bytes of a bf16 row together.
+//
+// Segments of a sequence run side by side in two launches.  The first takes segment 0 from the sequence's true
+// start, y and all, and of the others but the last only the end state from a zero start and the sum of delta, which
+// make the segment a map h -> exp(A sum delta) h + end.  The second takes all but segment 0, each from the
+// state that the maps before it lead to.  Whole sequences are the first launch alone, one segment each.
+constexpr int kBlk = 16;  // tokens per block
+
+struct Piece {
+    int t0, len;          // tokens
+    const float *h_in;    // [dim][16] start state, or NULL: zero
+    float *h_out, *sdt;   // [dim][16], or NULL: not kept; [dim], of a map only
 };
 
-template <typename T, bool SC, bool WITH_C>
-__device__ __forceinline__ BcRaw<T> load_bc(const T *B, const T *C, int64_t off, int lane) {
-    BcRaw<T> r;
-    constexpr int NW = BcRaw<T>::NW;
-    if constexpr (SC) {
-        using W = const __attribute__((address_space(4))) uint32_t;
-        W *b = (W *)(uintptr_t)(B + off), *c = (W *)(uintptr_t)(C + off);
-#pragma unroll
-        for (int i = 0; i < NW; ++i) r.b[i] = b[i];
-        if constexpr (WITH_C) {
-#pragma unroll
-            for (int i = 0; i < NW; ++i) r.c[i] = c[i];
-        }
-    } else {
-        uint32_t v = 0;
-        if (lane < kN || (WITH_C && lane < 2 * kN)) {
-            const T *src = lane < kN ? B + off + lane : C + off + lane - kN;
-            if constexpr (sizeof(T) == 4) v = __float_as_uint(*src);
-            else v = *src;
-        }
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                r.b[i] = __builtin_amdgcn_readlane(v, i);
-                if constexpr (WITH_C) r.c[i] = __builtin_amdgcn_readlane(v, kN + i);
-            } else {
-                r.b[i] = __builtin_amdgcn_readlane(v, 2 * i) | (__builtin_amdgcn_readlane(v, 2 * i + 1) << 16);
-                if constexpr (WITH_C)
-                    r.c[i] = __builtin_amdgcn_readlane(v, kN + 2 * i) | (__builtin_amdgcn_readlane(v, kN + 2 * i + 1) << 16);
-            }
-        }
-    }
-    return r;
-}
-template <typename T>
-__device__ __forceinline__ float bc_f32(const uint32_t *w, int n) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[n]);
-    else return __uint_as_float(n & 1 ? w[n >> 1] & 0xFFFF0000u : w[n >> 1] << 16);
-}
-
-// The scan, one wave per 64 channels of a sequence or segment: a lane walks its channel's tokens in
-// order with the 16 states in registers.
-//
-// Per (token, channel, state) this is mul, exp, mul, fma, fma and nothing else: B and C are the same for every lane
-// and come as scalar operands, x, delta, z and y are one coalesced row piece per token, and no state
-// passes between lanes.  (A scan whose lanes share a channel needs 2.5 more instructions per element for the maps
-// between lanes and the LDS reads of B and C.)  Bound by instruction issue; the price is that only
-// sequences x channels / 64 waves exist, so where those do not fill the chip the sequence is cut
-// into segments (FULL = false is their first pass, see split_shift).
-//
-// FULL: y and the last state.  Else a segment's end state from zero and the sum of its delta: the
-// segment as a map h -> exp(A sum delta) h + end.
-template <typename T, bool ZOH, bool FULL, bool SC>
-__global__ __launch_bounds__(64) void scan_packed(ScanParams p) {
-    constexpr int U = 4;  // tokens whose x, delta and z are loaded ahead
-    const int lane = threadIdx.x;
-    const bool split = p.seg != nullptr;
-    int s = blockIdx.x, t0, len;
-    int64_t slot = -1;
-    if (split) {
-        s = seq_of_segment(p.q, blockIdx.x, p.shift, lane);
-        const Range rg = range_of(p.q, s);
-        const int first = ((int)blockIdx.x - (rg.t0 >> p.shift) - s) << p.shift;
-        if (first < 0 || first >= rg.len) return;
-        t0 = rg.t0 + first;
-        len = rg.len - first < (1 << p.shift) ? rg.len - first : 1 << p.shift;
-    } else {
-        const Range rg = range_of(p.q, s);
-        t0 = rg.t0, len = rg.len;
-        slot = p.h ? slot_of(p.q, s) : -1;
-    }
-    t0 = __builtin_amdgcn_readfirstlane(t0), len = __builtin_amdgcn_readfirstlane(len);
-    const int64_t dim = p.dim, c0 = (int64_t)blockIdx.y * 64;
-    const int lc = (int)(c0 + lane < dim ? lane : dim - 1 - c0);  // lanes past the last channel repeat it
-    const bool live = c0 + lane < dim;
-    const int64_t ch = c0 + lc;
-
-    float a2[kN], h[kN];
-#pragma unroll
-    for (int n = 0; n < kN; n += 4) {
-        const float4 v = load_f4(p.A + ch * kN + n);
-        a2[n] = v.x * kLog2e, a2[n + 1] = v.y * kLog2e, a2[n + 2] = v.z * kLog2e, a2[n + 3] = v.w * kLog2e;
-    }
-    const float *h_in = nullptr;
-    if (FULL && split) h_in = p.seg + ((int64_t)blockIdx.x * dim + ch) * kN;
-    else if (FULL && slot >= 0 && p.q.carry && p.q.carry[s]) h_in = p.h + (slot * dim + ch) * kN;
-#pragma unroll
-    for (int n = 0; n < kN; n += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h_in) v = *(const float4 *)(h_in + n);
-        h[n] = v.x, h[n + 1] = v.y, h[n + 2] = v.z, h[n + 3] = v.w;
-    }
+// FULL: y and the last state.  Else the map.
+template <typename T, bool ZOH, bool FULL, bool GATE>
+__device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, float (*bc)[2 * kN], int64_t c0, int lane,
+                                           const float (&a2)[4], float (&h)[4]) {
+    const int cl = lane >> 2, q = lane & 3;
+    const int64_t dim = p.dim;
+    const bool live = c0 + cl < dim;
+    const int64_t ch = live ? c0 + cl : dim - 1;  // lanes past the last channel repeat it
+    const int len = w.len;
     const float Dd = FULL && p.D ? p.D[ch] : 0.f, bias = p.bias ? p.bias[ch] : 0.f;
-    const T *x = (const T *)p.x + (int64_t)t0 * dim + c0;
-    const T *dl = (const T *)p.delta + (int64_t)t0 * dim + c0;
-    const T *z = FULL && p.z ? (const T *)p.z + (int64_t)t0 * p.z_stride + c0 : nullptr;
-    T *y = (T *)p.y + (int64_t)t0 * dim + c0;
-    const T *B = (const T *)p.B + (int64_t)t0 * p.bc_stride, *C = (const T *)p.C + (int64_t)t0 * p.bc_stride;
-    float sum = 0.f;
+    const T *x = (const T *)p.x + (int64_t)w.t0 * dim + ch;
+    const T *dl = (const T *)p.delta + (int64_t)w.t0 * dim + ch;
+    const T *z = GATE ? (const T *)p.z + (int64_t)w.t0 * p.z_stride + ch : nullptr;
+    T *y = (T *)p.y + (int64_t)w.t0 * dim + ch;
+    // this lane's eighth of a token's B (q < 2) and C
+    const T *src = (q < 2 ? (const T *)p.B + 8 * q : (const T *)p.C + 8 * (q - 2)) + (int64_t)w.t0 * p.bc_stride;
 
-    T xr[U], dr[U], zr[U];
-    auto load_block = [&](int t, T (&xb)[U], T (&db)[U], T (&zb)[U]) {
+    struct Block {
+        uint32_t x[4], d[4], z[4];  // tokens 4 j + q (as 32-bit words: 16-bit pairs would tie two loads together)
+        Raw8<T> bc;                 // token lane / 4
+    };
+    auto raw = [](const T *a) -> uint32_t {
+        if constexpr (sizeof(T) == 4) return __float_as_uint(*a);
+        else return *a;
+    };
+    auto val = [](uint32_t w) { return __uint_as_float(sizeof(T) == 4 ? w : w << 16); };
+    auto load = [&](int t, Block &b) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int tt = t + u < len ? t + u : len - 1;
-            xb[u] = (x + (int64_t)tt * dim)[lc];
-            db[u] = (dl + (int64_t)tt * dim)[lc];
+        for (int j = 0; j < 4; ++j) {
+            const int64_t tt = t + 4 * j + q < len ? t + 4 * j + q : len - 1;
+            b.x[j] = raw(x + tt * dim);
+            b.d[j] = raw(dl + tt * dim);
+            b.z[j] = GATE ? raw(z + tt * p.z_stride) : 0u;
+        }
+        const int64_t tb = t + cl < len ? t + cl : len - 1;
+        if (FULL || q < 2) b.bc = load_any8(src + tb * p.bc_stride);
+    };
+    float sum = 0.f;
+    auto compute = [&](int t, const Block &b) {
+        if (FULL || q < 2) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = raw_f32(b.bc, e);
+            *(float4 *)&bc[cl][8 * q] = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4 *)&bc[cl][8 * q + 4] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        float d[4], dx[4], gate[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = val(b.d[j]) + bias;
+        if (p.softplus) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = softplus(d[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            d[j] = t + 4 * j + q < len ? d[j] : 0.f;  // past the end: the identity step
+            dx[j] = t + 4 * j + q < len ? d[j] * val(b.x[j]) : 0.f;
+            gate[j] = GATE ? silu(val(b.z[j])) : 1.f;
+            sum += d[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (t + 4 * j >= len) break;
+            float yt[4];
+            auto token = [&](auto ic) {
+                constexpr int I = decltype(ic)::value;
+                const float4 Bv = *(const float4 *)&bc[4 * j + I][4 * q];
+                float4 Cv;
+                if constexpr (FULL) Cv = *(const float4 *)&bc[4 * j + I][kN + 4 * q];
+                const float bv[4] = {Bv.x, Bv.y, Bv.z, Bv.w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float arg = quad_lane<I>(d[j]) * a2[n], e = __builtin_amdgcn_exp2f(arg);
+                    float u = quad_lane<I>(dx[j]) * bv[n];
+                    if constexpr (ZOH) u *= zoh_phi(e, arg);
+                    h[n] = fmaf(e, h[n], u);
+                }
+                if constexpr (FULL) yt[I] = fmaf(Cv.x, h[0], Cv.y * h[1]) + fmaf(Cv.z, h[2], Cv.w * h[3]);
+            };
+            token(std::integral_constant<int, 0>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 3>{});
             if constexpr (FULL) {
-                if (z) zb[u] = (z + (int64_t)tt * p.z_stride)[lc];
+                // lane q gets the sum of yt[q] over the four lanes
+                const bool b0 = q & 1, b1 = q & 2;
+                const float r0 = (b0 ? yt[1] : yt[0]) + quad<kQuadXor1>(b0 ? yt[0] : yt[1]);
+                const float r1 = (b0 ? yt[3] : yt[2]) + quad<kQuadXor1>(b0 ? yt[2] : yt[3]);
+                const float r = (b1 ? r1 : r0) + quad<kQuadXor2>(b1 ? r0 : r1);
+                const float v = fmaf(Dd, val(b.x[j]), r) * gate[j];
+                const int64_t tt = t + 4 * j + q;
+                if (live && tt < len) y[tt * dim] = Io<T>::to(v);
             }
         }
     };
-    BcRaw<T> bc;
-    if (len > 0) {
-        load_block(0, xr, dr, zr);
-        bc = load_bc<T, SC, FULL>(B, C, 0, lane);
-    }
-    for (int t = 0; t < len; t += U) {
-        T xn[U], dn[U], zn[U];
-        load_block(t + U, xn, dn, zn);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= len) break;
-            // the next token's B and C, in flight during this one's arithmetic
-            const int tn = t + u + 1 < len ? t + u + 1 : len - 1;
-            const BcRaw<T> next = load_bc<T, SC, FULL>(B, C, (int64_t)tn * p.bc_stride, lane);
-            float d = Io<T>::f32(dr[u]) + bias;
-            if (p.softplus) d = softplus(d);
-            const float xv = Io<T>::f32(xr[u]), dx = d * xv;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                const float arg = d * a2[n], e = __builtin_amdgcn_exp2f(arg);
-                float g = dx;
-                if constexpr (ZOH) g = dx * zoh_phi(e, arg);
-                h[n] = fmaf(e, h[n], g * bc_f32<T>(bc.b, n));
-                if constexpr (FULL) acc[n & 3] = fmaf(bc_f32<T>(bc.c, n), h[n], acc[n & 3]);
-            }
-            if constexpr (FULL) {
-                float v = fmaf(Dd, xv, (acc[0] + acc[1]) + (acc[2] + acc[3]));
-                if (z) v *= silu(Io<T>::f32(zr[u]));
-                if (live) (y + (int64_t)(t + u) * dim)[lane] = Io<T>::to(v);
-            } else {
-                sum += d;
-            }
-            bc = next;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) xr[u] = xn[u], dr[u] = dn[u], zr[u] = zn[u];
+    // two buffers named in turn: copying one to the other would wait for every load and store in flight
+    Block even, odd;
+    if (len > 0) load(0, even);
+    // (a block past the end loads the last token again: where a load depended on a condition, the wait before
+    // the next use would be for all of them)
+    for (int t = 0; t < len; t += 2 * kBlk) {
+        load(t + kBlk, odd);
+        compute(t, even);
+        if (t + kBlk >= len) break;
+        load(t + 2 * kBlk, even);
+        compute(t + kBlk, odd);
     }
     if (!live) return;
-    float *h_out = nullptr;
-    if (!FULL) h_out = p.seg + ((int64_t)blockIdx.x * dim + ch) * kN;
-    else if (slot >= 0) h_out = p.h + (slot * dim + ch) * kN;
-    if (h_out) {
-#pragma unroll
-        for (int n = 0; n < kN; n += 4) *(float4 *)(h_out + n) = make_float4(h[n], h[n + 1], h[n + 2], h[n + 3]);
+    if (w.h_out) *(float4 *)(w.h_out + ch * kN + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
+    if constexpr (!FULL) {
+        sum += quad<kQuadXor1>(sum);
+        sum += quad<kQuadXor2>(sum);
+        if (q == 0) w.sdt[ch] = sum;
     }
-    if (!FULL) p.sdt[(int64_t)blockIdx.x * dim + ch] = sum;
 }
 
-// Joins the segments of a sequence: one thread per (sequence, channel, state) walks its segments in
-// order, replaces each end state from zero by the state the segment starts from, and leaves the last in the cache.
+// LAUNCH 0, 1: the first and the second launch above.
+template <typename T, bool ZOH, bool GATE, int LAUNCH>
+__global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
+    __shared__ __attribute__((aligned(16))) float bc_lds[4][kBlk][2 * kN];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
+    // channel blocks of a segment follow one another: they go to different XCDs, so that a long
+    // sequence does not load one of them
+    const int seg = blockIdx.x / p.ntiles, tile = blockIdx.x - seg * p.ntiles;
+    const int64_t dim = p.dim, c0 = (int64_t)tile * 64 + wave * 16;
+    if (c0 >= dim) return;
+    const int64_t ch = c0 + (lane >> 2) < dim ? c0 + (lane >> 2) : dim - 1;
+    const float4 av = load_f4(p.A + ch * kN + 4 * q);
+    const bool split = p.seg != nullptr;
+    Segment g{seg, 0, 0, 0};
+    if (split) {
+        g = find_segment(p.q, seg, p.shift, lane);
+    } else {
+        const Range r = range_of(p.q, seg);
+        g.t0 = __builtin_amdgcn_readfirstlane(r.t0), g.len = __builtin_amdgcn_readfirstlane(r.len);
+    }
+    const int first = split ? g.j << p.shift : 0, size = split ? 1 << p.shift : g.len;
+    if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
+    const bool last = g.len - first <= size;
+    if (LAUNCH == 0 && g.j > 0 && last) return;
+    const int64_t slot = p.h ? slot_of(p.q, g.s) : -1, st = dim * kN;
+    float *cache = slot >= 0 ? p.h + slot * st : nullptr;
+    Piece w{g.t0 + first, last ? g.len - first : size, nullptr, nullptr, nullptr};
+    if (last) w.h_out = cache;
+    else if (LAUNCH == 0) w.h_out = p.seg + seg * st;
+    if (LAUNCH == 0) w.sdt = split ? p.sdt + seg * dim : nullptr;
+
+    const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
+    float h[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (LAUNCH == 0) {
+        if (g.j == 0 && cache && p.q.carry && p.q.carry[g.s]) {
+            const float4 v = *(const float4 *)(cache + ch * kN + 4 * q);
+            h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+        }
+        if (g.j == 0) scan_piece<T, ZOH, true, GATE>(p, w, bc_lds[wave], c0, lane, a2, h);
+        else scan_piece<T, ZOH, false, false>(p, w, bc_lds[wave], c0, lane, a2, h);
+    } else {
+        // the state this segment starts from: the maps of those before it, in order, or what scan_join left
+        const float *e = p.seg + (int64_t)(seg - g.j) * st + ch * kN + 4 * q;
+        const float *d = p.sdt + (int64_t)(seg - g.j) * dim + ch;
+        const int n = p.joined ? 1 : g.j;
+        if (p.joined) e += (g.j - 1) * st;
+        constexpr int U = 4;  // maps loaded ahead
+        for (int i0 = 0; i0 < n; i0 += U) {
+            float4 ev[U];
+            float dv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u < n ? i0 + u : n - 1;
+                ev[u] = *(const float4 *)(e + i * st);
+                dv[u] = i > 0 ? d[i * dim] : 0.f;  // (segment 0 is a state, not a map)
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u >= n) break;
+                h[0] = fmaf(__builtin_amdgcn_exp2f(a2[0] * dv[u]), h[0], ev[u].x);
+                h[1] = fmaf(__builtin_amdgcn_exp2f(a2[1] * dv[u]), h[1], ev[u].y);
+                h[2] = fmaf(__builtin_amdgcn_exp2f(a2[2] * dv[u]), h[2], ev[u].z);
+                h[3] = fmaf(__builtin_amdgcn_exp2f(a2[3] * dv[u]), h[3], ev[u].w);
+            }
+        }
+        scan_piece<T, ZOH, true, GATE>(p, w, bc_lds[wave], c0, lane, a2, h);
+    }
+}
+
+// Joins the segments of long sequences between the launches: one thread per (sequence, channel, state) walks the
+// maps in order and leaves the state at the end of each segment in its place.
 __global__ __launch_bounds__(256) void scan_join(ScanParams p) {
     const int s = blockIdx.x;
     const Range rg = range_of(p.q, s);
-    const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x, ch = i / kN;
+    const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x, ch = i / kN, st = p.dim * kN;
     if (ch >= p.dim) return;
-    const int64_t slot = p.h ? slot_of(p.q, s) : -1;
     const float a2 = p.A[i] * kLog2e;
-    const int first = (rg.t0 >> p.shift) + s, n = (rg.len + (1 << p.shift) - 1) >> p.shift;
-    float h = 0.f;
-    if (slot >= 0 && p.q.carry && p.q.carry[s]) h = p.h[slot * p.dim * kN + i];
+    const int first = (rg.t0 >> p.shift) + s, n = ((rg.len + (1 << p.shift) - 1) >> p.shift) - 1;  // all but the last
+    if (n < 2) return;
+    float *e = p.seg + (int64_t)first * st + i;
+    const float *d = p.sdt + (int64_t)first * p.dim + ch;
+    float h = e[0];
     constexpr int U = 8;  // segments loaded ahead
-    for (int j0 = 0; j0 < n; j0 += U) {
-        float e[U], d[U];
+    for (int j0 = 1; j0 < n; j0 += U) {
+        float ev[U], dv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t j = first + (j0 + u < n ? j0 + u : n - 1);
-            e[u] = p.seg[j * p.dim * kN + i];
-            d[u] = p.sdt[j * p.dim + ch];
+            const int64_t j = j0 + u < n ? j0 + u : n - 1;
+            ev[u] = e[j * st];
+            dv[u] = d[j * p.dim];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j0 + u >= n) break;
-            p.seg[(int64_t)(first + j0 + u) * p.dim * kN + i] = h;
-            h = fmaf(__builtin_amdgcn_exp2f(a2 * d[u]), h, e[u]);
+            h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
+            e[(j0 + u) * st] = h;
         }
     }
-    if (slot >= 0) p.h[slot * p.dim * kN + i] = h;
 }
 
 // One token per sequence.  Four lanes per channel hold four states each, so that a wave moves 16 channels' states as
@@ -535,20 +606,35 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
     }
 }
 
-// Tokens per segment as a power of two, or 0: whole sequences.  A sequence walks alone at the rate of
-// its longest, so whole sequences take max(longest, tokens x tiles / SIMDs) token times; segments cost the
-// first pass on top (mul, exp, mul, fma of the five: 1.55 times the work) and the join.
+// Tokens per segment as a power of two, or 0: whole sequences.  In clocks of a SIMD, a wave's token
+// takes 245 alone and 150 beside others (measured); a segment's map takes 115.  Whole sequences: the longest alone,
+// or all evenly plus a quarter for lengths that do not even out.  Segments: both passes, and 25,000 for the second
+// launch and the join.
 constexpr int kSimds = 1024;  // MI355X: 256 compute units of 4
+#ifndef KWALK
+#define KWALK 16
+#endif
+constexpr int kWalk = KWALK;     // segments up to which the second launch walks the maps itself
 
 int split_shift(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim) {
-    const int64_t tiles = (dim + 63) / 64;
+    const int64_t tiles = (dim + 15) / 16;
     const int64_t longest = max_seqlen < tokens ? max_seqlen : tokens;
     const int64_t share = (tokens * tiles + kSimds - 1) / kSimds;  // token times of a SIMD if all is even
-    const int64_t whole = longest > share ? longest : share;
-    if (whole <= share + share / 2 + 64) return 0;
-    // two waves per SIMD, segments of 32 to 4096 tokens
-    int shift = 5;
-    while (shift < 12 && (tokens >> shift) * tiles > 2 * kSimds) ++shift;
+    const int64_t whole = longest * 245 > share * 188 ? longest * 245 : share * 188;
+#ifdef NOSPLIT
+    return 0;
+#endif
+#ifndef FORCESPLIT
+    if (whole <= share * 265 + 25000) return 0;
+#endif
+#ifndef SEGW
+#define SEGW 4
+#endif
+#ifndef MINSH
+#define MINSH 5
+#endif
+    int shift = MINSH;
+    while (shift < 12 && (tokens >> shift) * tiles > SEGW * kSimds) ++shift;
     if ((INT64_C(2) << shift) > longest) return 0;
     (void)nseq;
     return shift;
@@ -633,24 +719,20 @@ ScanParams scan_params(const ScanArgs &a) {
     return p;
 }
 
-template <typename T, bool ZOH, bool SC>
+template <typename T, bool ZOH, bool GATE>
 int launch_scan(const ScanParams &p, int64_t blocks, void *stream) {
-    const dim3 grid((unsigned)blocks, (unsigned)((p.dim + 63) / 64));
-    if (p.seg) {
-        int rc = enqueue(scan_packed<T, ZOH, false, SC>, grid, dim3(64), p, stream);
-        if (rc == SELSCAN_OK)
-            rc = enqueue(scan_join, dim3((unsigned)p.q.nseq, (unsigned)((p.dim * kN + 255) / 256)), dim3(256), p, stream);
-        if (rc != SELSCAN_OK) return rc;
-    }
-    return enqueue(scan_packed<T, ZOH, true, SC>, grid, dim3(64), p, stream);
+    const dim3 grid((unsigned)blocks);
+    int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, grid, dim3(256), p, stream);
+    if (rc == SELSCAN_OK && p.joined)
+        rc = enqueue(scan_join, dim3((unsigned)p.q.nseq, (unsigned)((p.dim * kN + 255) / 256)), dim3(256), p, stream);
+    if (rc == SELSCAN_OK && p.seg) rc = enqueue(scan_packed<T, ZOH, GATE, 1>, grid, dim3(256), p, stream);
+    return rc;
 }
 
 template <typename T>
 int launch_scan_io(const ScanParams &p, int64_t blocks, bool zoh, void *stream) {
-    // scalar loads of B and C need their rows on 4-byte boundaries
-    const bool sc = sizeof(T) == 4 || (p.bc_stride % 2 == 0 && aligned(p.B, 4) && aligned(p.C, 4));
-    if (zoh) return sc ? launch_scan<T, true, true>(p, blocks, stream) : launch_scan<T, true, false>(p, blocks, stream);
-    return sc ? launch_scan<T, false, true>(p, blocks, stream) : launch_scan<T, false, false>(p, blocks, stream);
+    if (zoh) return p.z ? launch_scan<T, true, true>(p, blocks, stream) : launch_scan<T, true, false>(p, blocks, stream);
+    return p.z ? launch_scan<T, false, true>(p, blocks, stream) : launch_scan<T, false, false>(p, blocks, stream);
 }
 
 // rows that a thread of a step kernel takes one after another: one while the launch has fewer than
@@ -733,17 +815,20 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
     const int rc = scan_check(a, &nothing);
     if (rc != SELSCAN_OK || nothing) return rc;
     ScanParams p = scan_params(a);
-    int64_t blocks = nseq;
+    p.ntiles = (int)((dim + 63) / 64);
+    int64_t pieces = nseq;
     if (need) {
         p.shift = split_shift(tokens, nseq, max_seqlen, dim);
-        blocks = segments(tokens, nseq, p.shift);
+        pieces = segments(tokens, nseq, p.shift);
         p.seg = (float *)workspace;
-        p.sdt = p.seg + blocks * dim * kN;
+        p.sdt = p.seg + pieces * dim * kN;
+        p.joined = (max_seqlen >> p.shift) > kWalk ? 1 : 0;
     }
-    if ((dim * kN + 255) / 256 > kGridY) return SELSCAN_E_UNSUPPORTED;
+    // (the join's grid: 16 channels per workgroup)
+    if (pieces * p.ntiles > INT32_MAX || (dim * kN + 255) / 256 > kGridY) return SELSCAN_E_UNSUPPORTED;
     const bool zoh = (flags & SELSCAN_FLAG_ZOH) != 0;
-    return io_dtype == SELSCAN_BF16 ? launch_scan_io<uint16_t>(p, blocks, zoh, stream)
-                                    : launch_scan_io<float>(p, blocks, zoh, stream);
+    return io_dtype == SELSCAN_BF16 ? launch_scan_io<uint16_t>(p, pieces * p.ntiles, zoh, stream)
+                                    : launch_scan_io<float>(p, pieces * p.ntiles, zoh, stream);
 }
 
 int selscan_step(const void *x, const void *delta, const float *A, const void *B, const void *C, int64_t bc_stride,
