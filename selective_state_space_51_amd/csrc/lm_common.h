@@ -91,15 +91,27 @@ __device__ __forceinline__ void store_any8(T *p, const float (&v)[8]) {
     *(U *)p = u;
 }
 
+// Sum and maximum over the 64 lanes, the same in every lane.  DPP moves along rows of 16 and then across them
+// (lane 63 ends with all), without LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or(float other, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, float identity, F f) {
+    v = f(v, dpp_or<0x111, 0xF>(identity, v));  // row_shr 1, 2, 4, 8
+    v = f(v, dpp_or<0x112, 0xF>(identity, v));
+    v = f(v, dpp_or<0x114, 0xF>(identity, v));
+    v = f(v, dpp_or<0x118, 0xF>(identity, v));
+    v = f(v, dpp_or<0x142, 0xA>(identity, v));  // row_bcast 15 into rows 1 and 3, 31 into rows 2 and 3
+    v = f(v, dpp_or<0x143, 0xC>(identity, v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return wave_reduce(v, 0.f, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace

@@ -9,10 +9,13 @@
 // slices' (m, s, t) and their best alternatives are joined by a second, small kernel.  HBM bound.
 #include "lm_common.h"
 
+#include <float.h>
+
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTop = 32;
+constexpr int kMaxVocab = 1 << 21;
 constexpr int kCand = 512;  // candidates a slice ranks directly
 
 struct LpParams {
@@ -76,10 +79,14 @@ __device__ __forceinline__ float kth_of_wave(float v, int k) {
 
 // One workgroup: PIECES x 256 x 8 logits of one row, in registers.
 //
+// a = c x - fl(c m) takes one fma per logit instead of c (x - m)'s two operations; the rounding of c m is the same
+// for all logits and so a factor of s and t, which the join takes out again (from the exact residue of c m).  Where
+// c m overflows (a row of the type's lowest value), the subtraction comes first.
+//
 // Alternatives: the `top`-th largest of a wave's 64 per-lane maxima is no larger than the slice's `top`-th
 // largest logit, so every logit of the slice that can be among the best is at or above the largest of the four
-// waves' bounds.  Those few (some hundred for top = 32) are gathered in LDS and ranked by counting.  If equal
-// values make them too many, the best are taken out one after another instead.
+// waves' bounds.  Those few (some hundred for top = 32) are found by the maxima of pieces of 8, gathered in LDS
+// and ranked by counting.  If equal values make them too many, the best are taken out one after another.
 template <typename T, int PIECES>
 __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     __shared__ float red[4];
@@ -88,20 +95,22 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     __shared__ unsigned long long cand[kCand], pick[4];
     __shared__ int ncand;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int64_t blk = blockIdx.x, row = blk / p.nsl;
-    const int base = (int)(blk - row * p.nsl) * (PIECES * kThreads * 8);
+    const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;
+    const int base = sl * (PIECES * kThreads * 8);
     const T *x = (const T *)p.x + row * p.stride;
     Raw8<T> r[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) r[i] = load_logits(x, base + (i * kThreads + tid) * 8, p.vocab);
     if (tid == 0) ncand = 0;
-    float m = -INFINITY;
+    float pm[PIECES], mine = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
+    for (int i = 0; i < PIECES; ++i) {
+        pm[i] = raw_f32(r[i], 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, raw_f32(r[i], e));
-    const float mine = m;
-    m = wave_max(m);
+        for (int e = 1; e < 8; ++e) pm[i] = fmaxf(pm[i], raw_f32(r[i], e));
+        mine = fmaxf(mine, pm[i]);
+    }
+    float m = wave_max(mine);
     if (lane == 0) red[wave] = m;
     if (p.top) {
         const float b = kth_of_wave<T>(mine, p.top);
@@ -109,41 +118,55 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     }
     lds_barrier();
     m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mm = m == -INFINITY ? 0.f : m;
+    const float mc = m * p.c;  // (-inf: nothing but -inf)
     float s = 0.f, t = 0.f;
+    if (fabsf(mc) < INFINITY) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
+        for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = (raw_f32(r[i], e) - mm) * p.c, w = __builtin_amdgcn_exp2f(a);
-            s += w;
-            t = fmaf(w, fmaxf(a, -200.f), t);  // 2^-200 is 0: no 0 * inf for a logit of -inf
-        }
+            for (int e = 0; e < 8; ++e) {
+                const float a = fmaf(raw_f32(r[i], e), p.c, -mc), w = __builtin_amdgcn_exp2f(a);
+                s += w;
+                t = fmaf(w, fmaxf(a, -200.f), t);  // 2^-200 is 0: no 0 * inf for a logit of -inf
+            }
+    } else {
+        const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = (raw_f32(r[i], e) - mm) * p.c, w = __builtin_amdgcn_exp2f(a);
+                s += w;
+                t = fmaf(w, fmaxf(a, -200.f), t);
+            }
+    }
     s = wave_sum(s), t = wave_sum(t);
     if (lane == 0) red2[wave][0] = s, red2[wave][1] = t;
     if (p.top) {
-        const float b = fmaxf(fmaxf(bound[0], bound[1]), fmaxf(bound[2], bound[3]));
-        if (mine >= b && mine > -INFINITY) {
+        float b = fmaxf(fmaxf(bound[0], bound[1]), fmaxf(bound[2], bound[3]));
+        b = fmaxf(b, -FLT_MAX);  // a logit of -inf is no alternative
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i)
+        for (int i = 0; i < PIECES; ++i) {
+            if (pm[i] >= b) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float v = raw_f32(r[i], e);
-                    if (v >= b && v > -INFINITY) {
+                    if (v >= b) {
                         const int at = atomicAdd(&ncand, 1);
                         if (at < kCand) cand[at] = entry(v, base + (i * kThreads + tid) * 8 + e);
                     }
                 }
+            }
         }
     }
     lds_barrier();
     if (tid == 0) {
         s = (red2[0][0] + red2[1][0]) + (red2[2][0] + red2[3][0]);
         t = (red2[0][1] + red2[1][1]) + (red2[2][1] + red2[3][1]);
-        p.part[blk] = make_float4(m, s, t, 0.f);
+        p.part[blockIdx.x] = make_float4(m, s, t, 0.f);
     }
     if (!p.top) return;
-    unsigned long long *out = p.cand + blk * p.top;
+    unsigned long long *out = p.cand + (int64_t)blockIdx.x * p.top;
     const int n = ncand;
     if (n <= kCand) {
         for (int i = tid; i < n; i += kThreads) {
@@ -158,14 +181,17 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     unsigned long long last = ~0ull;
     for (int k = 0; k < p.top; ++k) {
         unsigned long long best = 0;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+            // (from memory again: this rare loop then costs the kernel no registers)
+            const Raw8<T> q8 = load_logits(x, base + (i * kThreads + tid) * 8, p.vocab);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = raw_f32(r[i], e);
+                const float v = raw_f32(q8, e);
                 const unsigned long long q = entry(v, base + (i * kThreads + tid) * 8 + e);
                 if (v > -INFINITY && q < last && q > best) best = q;
             }
+        }
 #pragma unroll
         for (int o = 32; o; o >>= 1) {
             const unsigned long long q = __shfl_xor(best, o);
@@ -181,69 +207,117 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     }
 }
 
-// One wave per row: joins the slices.  An alternative's rank is the number of better ones in all slices, each
-// of which is sorted: the count walks a slice's list only as far as it is better.
+// c m as a slice took it off: its rounding where that is finite, else nothing (the subtraction came first)
+struct Base {
+    float mc, rest;  // c m = mc + rest
+};
+__device__ __forceinline__ Base base_of(float m, float c) {
+    const float mc = m * c;
+    if (fabsf(mc) < INFINITY) return {mc, fmaf(m, c, -mc)};
+    return {mc, 0.f};
+}
+
+// One workgroup per row: joins the slices.  Alternatives: with `low` the worst over the slices of their place-th entries,
+// place = ceil(top / slices), at least top entries are at or above it, so only those can be among the
+// best.  They are gathered in LDS and ranked by counting.
 template <typename T>
-__global__ __launch_bounds__(64) void logprobs_join(LpParams p) {
-    const int64_t row = blockIdx.x;
-    const int lane = threadIdx.x;
-    const float4 *part = p.part + row * p.nsl;
+__global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
+    __shared__ unsigned long long list[kCand], lows[4];
+    __shared__ int count;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const float4 *part = p.part + (int64_t)row * p.nsl;
+    const unsigned long long *cand = p.cand + (int64_t)row * p.nsl * p.top;
+    const int n = p.nsl * p.top;
+    const unsigned long long first = p.top && tid < n ? cand[tid] : 0;  // (all of them, mostly)
+    unsigned long long low = ~0ull;
+    if (p.top) {
+        const int place = (p.top + p.nsl - 1) / p.nsl - 1;
+        for (int i = tid; i < p.nsl; i += blockDim.x) {
+            const unsigned long long k = cand[i * p.top + place];
+            low = k < low ? k : low;
+        }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) {
+            const unsigned long long k = __shfl_xor(low, o);
+            low = k < low ? k : low;
+        }
+        if (lane == 0) lows[tid >> 6] = low;
+        if (tid == 0) count = 0;
+    }
     float M = -INFINITY;
     for (int i = lane; i < p.nsl; i += 64) M = fmaxf(M, part[i].x);
     M = wave_max(M);
+    const Base B = base_of(M, p.c);
+    const bool finite = fabsf(B.mc) < INFINITY;
     float s = 0.f, t = 0.f;
     for (int i = lane; i < p.nsl; i += 64) {
         const float4 q = part[i];
         // a slice of nothing but -inf has s = t = 0, or NaN where it holds one: taken as it is
         const bool none = q.x == -INFINITY;
-        const float d = none ? 0.f : (q.x - M) * p.c, f = none ? 1.f : __builtin_amdgcn_exp2f(d);
+        const Base b = base_of(q.x, p.c);
+        // how far the slice's base lies below the row's, as both were taken off
+        const float d = none ? 0.f : finite && fabsf(b.mc) < INFINITY ? b.mc - B.mc : (q.x - M) * p.c;
+        const float f = none ? 1.f : __builtin_amdgcn_exp2f(d);
         s = fmaf(q.y, f, s);
         t = fmaf(f, fmaf(q.y, fmaxf(d, -200.f), q.z), t);
     }
     s = wave_sum(s), t = wave_sum(t);
     const bool empty = s == 0.f;
-    const float ls = __builtin_amdgcn_logf(s);
-    if (lane == 0) {
+    const float ls = __builtin_amdgcn_logf(s) - B.rest;  // log2 of sum 2^(c (x - M))
+    // (c (x - M) exactly as far as x - M is)
+    auto logp = [&](float x) { return fmaf(x - M, p.c, -ls) * kLn2; };
+    if (tid == 0) {
         p.stats[2 * row] = M;
         p.stats[2 * row + 1] = ls * kLn2;
-        p.entropy[row] = empty ? 0.f : (ls - t / s) * kLn2;
+        p.entropy[row] = empty ? 0.f : (__builtin_amdgcn_logf(s) - t / s) * kLn2;
         const int64_t y = p.targets[row];
         float lp = 0.f;
-        if (y >= 0 && y < p.vocab) {
-            const float v = Io<T>::f32(((const T *)p.x)[row * p.stride + y]);
-            lp = empty ? -INFINITY : fmaf(v - M, p.c, -ls) * kLn2;
-        }
+        if (y >= 0 && y < p.vocab) lp = empty ? -INFINITY : logp(Io<T>::f32(((const T *)p.x)[row * p.stride + y]));
         p.logprob[row] = lp;
     }
     if (!p.top) return;
-    const unsigned long long *cand = p.cand + row * p.nsl * p.top;
-    const int n = p.nsl * p.top;
-    float *val = p.top_logprob + row * p.top;
-    int64_t *idx = p.top_index + row * p.top;
-    const bool nan = s != s;
-    int have = 0;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        const int i = i0 + lane;
-        const unsigned long long k = i < n ? cand[i] : 0;
-        have += __popcll(__ballot(k != 0));
-        if (k == 0 || nan) continue;
-        int rank = i % p.top;  // the better ones of its own slice come before it
-        const int own = i / p.top;
-        for (int q = 0; q < p.nsl && rank < p.top; ++q) {
-            if (q == own) continue;
-            for (int j = 0; j < p.top && rank < p.top && cand[q * p.top + j] > k; ++j) ++rank;
-        }
-        if (rank < p.top) {
-            const float v = value_of((uint32_t)(k >> 32));
-            val[rank] = fmaf(v - M, p.c, -ls) * kLn2;
-            idx[rank] = (int64_t)(uint32_t)~(uint32_t)k;
+    float *val = p.top_logprob + (int64_t)row * p.top;
+    int64_t *idx = p.top_index + (int64_t)row * p.top;
+    if (s != s) {
+        for (int i = tid; i < p.top; i += blockDim.x) val[i] = NAN, idx[i] = -1;
+        return;
+    }
+    __syncthreads();
+    low = lows[0];
+    for (int i = 1; i < (int)(blockDim.x >> 6); ++i) low = lows[i] < low ? lows[i] : low;
+    low = low == 0 ? 1 : low;  // a slice with fewer: every entry there is
+    for (int i = tid; i < n; i += blockDim.x) {
+        const unsigned long long k = i < (int)blockDim.x ? first : cand[i];
+        if (k >= low) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kCand) list[at] = k;
         }
     }
-    // fewer logits with a probability than alternatives asked for; or none of a row with a NaN
-    for (int i = (nan ? 0 : have) + lane; i < p.top; i += 64) {
-        val[i] = nan ? NAN : -INFINITY;
-        idx[i] = -1;
+    __syncthreads();
+    const int have = count;
+    auto put = [&](unsigned long long k, int rank) {
+        if (rank >= p.top) return;
+        val[rank] = logp(value_of((uint32_t)(k >> 32)));
+        idx[rank] = (int64_t)(uint32_t)~(uint32_t)k;
+    };
+    if (have <= kCand) {
+        for (int i = tid; i < have; i += blockDim.x) {
+            const unsigned long long k = list[i];
+            int rank = 0;
+            for (int j = 0; j < have; ++j) rank += list[j] > k ? 1 : 0;
+            put(k, rank);
+        }
+    } else {
+        // the best sit together in a few of very many slices
+        for (int i = tid; i < n; i += blockDim.x) {
+            const unsigned long long k = cand[i];
+            int rank = k >= low ? 0 : p.top;
+            for (int j = 0; j < n && rank < p.top; ++j) rank += cand[j] > k ? 1 : 0;
+            put(k, rank);
+        }
     }
+    // fewer logits with a probability than alternatives asked for
+    for (int i = have + tid; i < p.top; i += blockDim.x) val[i] = -INFINITY, idx[i] = -1;
 }
 
 constexpr int kBwdPieces = 4;
@@ -251,10 +325,10 @@ constexpr int kBwdPieces = 4;
 // gradient: reads a logit, writes its gradient; HBM bound
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
-    const int64_t blk = blockIdx.x, row = blk / p.nsl;
-    const int base = (int)(blk - row * p.nsl) * (kBwdPieces * kThreads * 8);
+    const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;
+    const int base = sl * (kBwdPieces * kThreads * 8);
     const T *x = (const T *)p.x + row * p.stride;
-    T *dx = (T *)p.dx + row * p.vocab;
+    T *dx = (T *)p.dx + (int64_t)row * p.vocab;
     const int64_t y = p.targets[row];
     const bool valid = y >= 0 && y < p.vocab;
     const float gl = p.dlogprob && valid ? p.dlogprob[row] * p.scale : 0.f;
@@ -291,11 +365,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     }
 }
 
-// 8-logit pieces per thread of a slice: 8 (16,384 logits), or 2 where slices that long would leave the chip's
-// compute units without four workgroups each
+// 8-logit pieces per thread of a slice: 4 (8,192 logits; 8 pieces measured 52 us where 4 take 49, 2,048 x 50,280 bf16), or 2
+// where slices that long would leave the chip's compute units without four workgroups each
 int pieces_for(int64_t rows, int64_t vocab) {
-    const int64_t big = 8 * kThreads * 8;
-    return rows * ((vocab + big - 1) / big) >= 1024 ? 8 : 2;
+    const int64_t big = 4 * kThreads * 8;
+    return rows * ((vocab + big - 1) / big) >= 1024 || vocab > kMaxVocab / 2 ? 4 : 2;
 }
 int64_t slices_for(int64_t rows, int64_t vocab) {
     const int64_t n = (int64_t)pieces_for(rows, vocab) * kThreads * 8;
@@ -304,7 +378,7 @@ int64_t slices_for(int64_t rows, int64_t vocab) {
 
 int lp_check(const void *logits, int64_t stride, const int64_t *targets, float scale, int64_t rows, int64_t vocab, int dtype) {
     if (rows < 0 || vocab < 0) return SELSCAN_E_SHAPE;
-    if (!io_known(dtype) || !(scale > 0.f) || !(scale < INFINITY) || vocab > (1 << 30)) return SELSCAN_E_UNSUPPORTED;
+    if (!io_known(dtype) || !(scale > 0.f) || !(scale < INFINITY) || vocab > kMaxVocab) return SELSCAN_E_UNSUPPORTED;
     if (rows == 0 || vocab == 0) return SELSCAN_OK;
     if (stride < vocab || mul_size(rows, stride) < 0) return SELSCAN_E_SHAPE;
     if (!logits || !targets) return SELSCAN_E_NULL;
@@ -317,7 +391,7 @@ int lp_check(const void *logits, int64_t stride, const int64_t *targets, float s
 extern "C" {
 
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
-    if (rows <= 0 || vocab <= 0 || vocab > (1 << 30) || top < 0 || top > kMaxTop) return 0;
+    if (rows <= 0 || vocab <= 0 || vocab > kMaxVocab || top < 0 || top > kMaxTop) return 0;
     const size_t n = (size_t)rows * (size_t)slices_for(rows, vocab);
     return n * (sizeof(float4) + (size_t)top * 8);
 }
@@ -356,11 +430,12 @@ int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t 
     p.part = (float4 *)workspace;
     p.cand = (unsigned long long *)(p.part + blocks);
     const bool bf = io_dtype == SELSCAN_BF16;
-    void (*k)(LpParams) = pieces == 8 ? (bf ? logprobs_slice<uint16_t, 8> : logprobs_slice<float, 8>)
+    void (*k)(LpParams) = pieces == 4 ? (bf ? logprobs_slice<uint16_t, 4> : logprobs_slice<float, 4>)
                                       : (bf ? logprobs_slice<uint16_t, 2> : logprobs_slice<float, 2>);
     rc = enqueue(k, dim3((unsigned)blocks), dim3(kThreads), p, stream);
     if (rc != SELSCAN_OK) return rc;
-    return enqueue(bf ? logprobs_join<uint16_t> : logprobs_join<float>, dim3((unsigned)rows), dim3(64), p, stream);
+    return enqueue(bf ? logprobs_join<uint16_t> : logprobs_join<float>, dim3((unsigned)rows),
+                   dim3(top && p.nsl * top > 64 ? kThreads : 64), p, stream);
 }
 
 int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t *targets, const float *stats,

@@ -611,39 +611,26 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
 // or all evenly plus a quarter for lengths that do not even out.  Segments: both passes, and 25,000 for the second
 // launch and the join.
 constexpr int kSimds = 1024;  // MI355X: 256 compute units of 4
-#ifndef KWALK
-#define KWALK 16
-#endif
-constexpr int kWalk = KWALK;     // segments up to which the second launch walks the maps itself
+constexpr int kWalk = 16;     // segments up to which the second launch walks the maps itself
 
-int split_shift(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim) {
+int split_shift(int64_t tokens, int64_t max_seqlen, int64_t dim) {
     const int64_t tiles = (dim + 15) / 16;
     const int64_t longest = max_seqlen < tokens ? max_seqlen : tokens;
     const int64_t share = (tokens * tiles + kSimds - 1) / kSimds;  // token times of a SIMD if all is even
     const int64_t whole = longest * 245 > share * 188 ? longest * 245 : share * 188;
-#ifdef NOSPLIT
-    return 0;
-#endif
-#ifndef FORCESPLIT
     if (whole <= share * 265 + 25000) return 0;
-#endif
-#ifndef SEGW
-#define SEGW 4
-#endif
-#ifndef MINSH
-#define MINSH 5
-#endif
-    int shift = MINSH;
-    while (shift < 12 && (tokens >> shift) * tiles > SEGW * kSimds) ++shift;
-    if ((INT64_C(2) << shift) > longest) return 0;
-    (void)nseq;
-    return shift;
+    // from 32 tokens up to what still leaves some four waves per SIMD: measured, 4,097 tokens x 96 tiles take 75 us at
+    // 128 tokens, 77 at 64, 90 at 256 and 434 whole; 505 tokens in 8 sequences x 96 tiles 20 us at 32, 23 at
+    // 64 and 34 whole
+    int shift = 5;
+    while (shift < 12 && (tokens >> shift) * tiles > 4 * kSimds) ++shift;
+    return (INT64_C(2) << shift) > longest ? 0 : shift;
 }
 
 int64_t segments(int64_t tokens, int64_t nseq, int shift) { return (tokens >> shift) + nseq; }
 
 size_t packed_workspace(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim) {
-    const int shift = split_shift(tokens, nseq, max_seqlen, dim);
+    const int shift = split_shift(tokens, max_seqlen, dim);
     return shift ? (size_t)segments(tokens, nseq, shift) * (size_t)dim * (kN + 1) * sizeof(float) : 0;
 }
 
@@ -818,7 +805,7 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
     p.ntiles = (int)((dim + 63) / 64);
     int64_t pieces = nseq;
     if (need) {
-        p.shift = split_shift(tokens, nseq, max_seqlen, dim);
+        p.shift = split_shift(tokens, max_seqlen, dim);
         pieces = segments(tokens, nseq, p.shift);
         p.seg = (float *)workspace;
         p.sdt = p.seg + pieces * dim * kN;
