@@ -4,14 +4,11 @@
 // y[r][j] = sum over groups of  scale * (sum_k q x - zero * sum_k x).  The inner sums run on the matrix
 // cores (16 rows of x by 16 rows of the matrix by 32 k), with the 4-bit values as bf16 numbers 16 + q: a
 // nibble put into the top of the mantissa of 16.0 is that number exactly, one shift and one and-or for two
-// weights.  The 16 leaves with the zero point, both times sum_k x, which one more product with ones gives
-// in the same register layout.  (128 + q would save nothing and cost 8 times the cancellation.)
+// weights.  The 16 leaves together with the zero point, by a second product with the constant -(16 + zero).
+// (128 + q would save nothing and cost 8 times the cancellation.)
 //
-// HBM bound: each weight is read once per 32 rows.
+// Each weight is read once per 32 rows of x.
 #include "lm_common.h"
-#ifndef RTV
-#define RTV 4
-#endif
 
 namespace {
 
@@ -72,6 +69,11 @@ __device__ __forceinline__ Split<T> split_x(const Raw8<T> &r) {
     return s;
 }
 
+template <int V>
+struct IntC {
+    static constexpr int value = V;
+};
+
 // N values of consecutive groups, from any address aligned to one
 template <typename V, int N>
 struct __attribute__((packed, aligned(sizeof(V)))) Group {
@@ -82,181 +84,303 @@ struct __attribute__((packed, aligned(2))) Raw16 {
     uint32_t w[4];
 };
 
-// The LDS of one wave, staged anew for every unit of 128 k.  Pieces of 16 bytes of a row are stored at their number
-// xor a function of the row, so that the 16 rows of a product's operand lie in different banks.
-template <typename T, int RT, int TM, int NG>
-struct Stage {
+// Every load takes whole pieces of rows: the matrix products want each lane to hold another row, but loads in that form
+// touch a cache line per lane, and the address unit, at a line a clock, then bounds the kernel (47 us for 24 x 2,048 x
+// 50,280).  The pieces go through LDS and come back in operand form.  A piece of 16 bytes is stored at its number
+// xor a function of its row, so that the 16 rows of an operand lie in different banks.
+//
+// Loads ahead are never under a condition (past the end they read what is there again), so that the wait for one does
+// not become a wait for all.
+
+// the matrix: 16 rows x 4 pieces of a unit
+__device__ __forceinline__ int w_at(int row, int piece) { return row * 4 + (piece ^ (row >> 2)); }
+
+// what a wave needs of 16 rows of the matrix
+template <int GM>
+struct MatrixRows {
+    static constexpr int NG = 4 / GM;  // groups of a unit
+    const uint8_t *wb, *zb;
+    const uint16_t *sb;
+    uint32_t wo, so;  // offsets: 4 lanes to a row
+    int groups, lane;
+    bool zeros;
+    Group<uint16_t, NG> sv;
+    Group<uint8_t, NG> zv;
+
+    __device__ __forceinline__ MatrixRows(const W4Params &p, int64_t row0, int lane_) : lane(lane_) {
+        // rows past the last repeat it: their products are not stored
+        const int64_t rowc = row0 < p.n ? row0 : p.n - 1;
+        const int most = (int)(p.n - rowc < 16 ? p.n - rowc : 16) - 1;
+        const uint32_t r = (lane >> 2) < most ? lane >> 2 : most;
+        groups = p.groups;
+        zeros = p.zeros != nullptr;
+        wb = p.q + rowc * (p.k >> 1);
+        sb = p.scales + rowc * p.groups;
+        zb = zeros ? p.zeros + rowc * p.groups : (const uint8_t *)sb;  // (read and not used without zeros)
+        wo = r * (uint32_t)(p.k >> 1) + 16 * (lane & 3);
+        so = r * (uint32_t)p.groups;
+    }
+    __device__ __forceinline__ uint4 load(int u) const { return *(const uint4 *)(wb + (int64_t)u * 64 + wo); }
+    // scales and zero points of units u .. u + 3, one unit to a lane (of a unit past the last: some that exist)
+    __device__ __forceinline__ void load_scales(int u) {
+        int at = (u + (lane & 3)) * NG;
+        at = at + NG <= groups ? at : groups - NG;
+        sv = *(const Group<uint16_t, NG> *)(sb + so + at);
+        zv = *(const Group<uint8_t, NG> *)(zb + so + at);
+    }
+    // of unit u alone, which may end early
+    __device__ __forceinline__ void load_scales_of_last(int u) {
+#pragma unroll
+        for (int a = 0; a < NG; ++a) {
+            const int at = u * NG + a < groups ? u * NG + a : groups - 1;
+            sv.v[a] = sb[so + at];
+            zv.v[a] = zb[so + at];
+        }
+    }
+    // [16 rows][4 units][NG]: scale (bf16) above, zero point below
+    __device__ __forceinline__ void store_scales(uint32_t *sz) const {
+#pragma unroll
+        for (int a = 0; a < NG; ++a) sz[lane * NG + a] = (uint32_t)sv.v[a] << 16 | (zeros ? zv.v[a] & 15 : 8);
+    }
+};
+
+// acc += the products of one unit: x as fragments from `fx(t, e, j)`, the matrix from w, scales from sz.  The 16 and the
+// zero point leave by a second product, of x with -(16 + zero) for every k of the group.
+template <int GM, int TM, int NS, class F>
+__device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32_t *sz, int q, int i, int g, f32x4 (&acc)[TM]) {
+    constexpr int NG = 4 / GM;
+    const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
+    f32x4 part[TM];
+    float s;
+    Frag zf;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j % GM == 0) {
+            const uint32_t v = sz[(i * 4 + q) * NG + j / GM];
+            s = __uint_as_float(v & 0xFFFF0000u);
+            // -(16 + zero) as bf16, exact, twice
+            const uint32_t z = 0xC1800000u | (v & 15) << 19;
+            zf.w[0] = zf.w[1] = zf.w[2] = zf.w[3] = z | z >> 16;
+        }
+        const Frag wf = dequant(((const uint32_t *)&w[w_at(i, j)])[g]);
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int e = 0; e < NS; ++e) {
+                const bf16x8 x = frag(fx(t, e, j));
+                part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(wf), j % GM == 0 && e == 0 ? nil : part[t], 0, 0, 0);
+                part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(zf), part[t], 0, 0, 0);
+            }
+        if (j % GM == GM - 1) {
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[t][c] = fmaf(s, part[t][c], acc[t][c]);
+        }
+    }
+}
+
+// Many rows of the matrix: the four waves of a workgroup take 16 rows each and the whole of k together, so that x is
+// staged, split and reordered once for all of them, and no sums are left to join.  x has two buffers: one barrier
+// per unit.  The matrix is loaded two units ahead, x one.
+template <typename T, int GM, int TM>
+__global__ __launch_bounds__(256, 4) void w4_rows(W4Params p) {
+    constexpr int NS = Split<T>::NS, NG = 4 / GM;
+    __shared__ uint4 xl[2][NS][16 * TM * 16];  // bf16 pieces of 8 k, 16 a row
+    __shared__ uint4 wl[4][64];
+    __shared__ uint32_t szl[4][64 * NG];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, g = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * 64 + wave * 16, tok0 = (int64_t)blockIdx.y * (16 * TM);
+    MatrixRows<GM> m(p, row0, lane);
+    // x: this thread brings piece tid & 15 (8 k) of row tid / 16, and of row 16 + tid / 16 where TM = 2
+    const int most = (int)(p.rows - tok0) - 1;
+    uint32_t xo[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        const int r = 16 * t + (tid >> 4);
+        xo[t] = (uint32_t)(r < most ? r : most) * (uint32_t)p.x_stride + 8 * (tid & 15);
+    }
+    const T *xb = (const T *)p.x + tok0 * p.x_stride;
+    f32x4 acc[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    Raw8<T> xv[TM];
+    auto load_x = [&](int u) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) xv[t] = load_any8(xb + (int64_t)u * 128 + xo[t]);
+    };
+    const int whole = p.k >> 7;
+    // unit u, q = u % 4; more: loads ahead
+    auto step = [&](int u, uint4 &wv, auto qc, auto more) {
+        constexpr int q = decltype(qc)::value, buf = q & 1;
+        if (q == 0 || !decltype(more)::value) {
+            m.store_scales(szl[wave]);
+            if constexpr (decltype(more)::value) m.load_scales(u + 4);
+        }
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            const Split<T> sx = split_x<T>(xv[t]);
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+                xl[buf][e][(16 * t + (tid >> 4)) * 16 + ((tid & 15) ^ (tid >> 4))] =
+                    make_uint4(sx.f[e].w[0], sx.f[e].w[1], sx.f[e].w[2], sx.f[e].w[3]);
+        }
+        wl[wave][w_at(lane >> 2, lane & 3)] = wv;
+        lds_barrier();
+        if constexpr (decltype(more)::value) {
+            load_x(u + 1 < whole ? u + 1 : u);
+            wv = m.load(u + 2 < whole ? u + 2 : u);
+        }
+        auto fx = [&](int t, int e, int j) {
+            const uint4 v = xl[buf][e][(16 * t + i) * 16 + ((4 * j + g) ^ i)];
+            return Frag{{v.x, v.y, v.z, v.w}};
+        };
+        unit_products<GM, TM, NS>(fx, wl[wave], szl[wave], q, i, g, acc);
+    };
+    uint4 wa, wc;  // the matrix: units of even and of odd number
+    if (whole > 0) {
+        m.load_scales(0);
+        load_x(0);
+        wa = m.load(0);
+        wc = m.load(whole > 1 ? 1 : 0);
+        for (int u = 0; u < whole; u += 4) {
+            step(u, wa, IntC<0>{}, BoolC<true>{});
+            if (u + 1 >= whole) break;
+            step(u + 1, wc, IntC<1>{}, BoolC<true>{});
+            if (u + 2 >= whole) break;
+            step(u + 2, wa, IntC<2>{}, BoolC<true>{});
+            if (u + 3 >= whole) break;
+            step(u + 3, wc, IntC<3>{}, BoolC<true>{});
+        }
+    }
+    // what k leaves past the whole units: pieces that exist, the others with x and q of zero
+    const int left = p.k - whole * 128;
+    if (left) {
+        m.load_scales_of_last(whole);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            xv[t] = Raw8<T>{};
+            if (8 * (tid & 15) < left) xv[t] = load_any8(xb + (int64_t)whole * 128 + xo[t]);
+        }
+        wa = make_uint4(0, 0, 0, 0);
+        if (32 * (lane & 3) < left) wa = m.load(whole);
+        lds_barrier();  // (the buffer of q = 0 may still be read)
+        step(whole, wa, IntC<0>{}, BoolC<false>{});
+    }
+    const int64_t row = row0 + i;
+    if (row >= p.n) return;
+    const float b = p.bias ? p.bias[row] : 0.f;
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int64_t tok = tok0 + 16 * t + 4 * g + c;
+            if (tok < p.rows) ((T *)p.y)[tok * p.n + row] = Io<T>::to(acc[t][c] + b);
+        }
+}
+
+// Few rows of the matrix: a workgroup takes 16 of them and its waves share out k, upw units each, and add their sums in
+// LDS.  A wave stages its own units of x and waits for no other until the end.
+template <typename T, int TM, int NG>
+struct WaveLds {
     static constexpr int XP = 8 * (int)sizeof(T);  // 16-byte pieces of a row of x
     static constexpr int XL = TM * XP / 4;         // loads of 64 pieces
     uint4 x[16 * TM * XP];
-    uint4 w[16 * RT * 4];
-    uint32_t sz[16 * RT * 4 * NG];  // scale (bf16) above, zero point below; 4 units' groups of a row together
-    __device__ static int xat(int row, int piece) { return row * XP + (piece ^ (row & 15)); }
-    __device__ static int wat(int row, int piece) { return row * 4 + (piece ^ ((row >> 2) & 3)); }
+    uint4 w[64];
+    uint32_t sz[64 * NG];
 };
 
-// One workgroup: 16 RT rows of the matrix for 16 TM rows of x; its waves share out k, upw units of 128 each,
-// and add their sums in LDS.  GM: products per group (group / 32).
-//
-// The matrix products want each lane to hold another row; loads in that form touch a cache line per lane, and the
-// address unit, at one line a clock, bounds the kernel (47 us for 24 x 2,048 x 50,280, of which 512 cycles a unit were
-// that).  So every load takes whole pieces of rows, 4 (matrix) or 16 (x) lanes to a row, goes through the
-// wave's own LDS, and comes back in operand form without bank conflicts; scales and zero points come for 4
-// units at a time, one row to 4 / RT lanes.
-template <typename T, int GM, int RT, int TM>
-__global__ __launch_bounds__(512) void w4_kernel(W4Params p) {
+template <typename T, int GM, int TM>
+__global__ __launch_bounds__(512) void w4_split(W4Params p) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-    constexpr int NS = Split<T>::NS, NG = 4 / GM;
-    using S = Stage<T, RT, TM, NG>;
+    constexpr int NS = Split<T>::NS, NG = 4 / GM, H = (int)sizeof(T) / 2;
+    using S = WaveLds<T, TM, NG>;
+    constexpr int XP = S::XP, XL = S::XL;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, g = lane >> 4;
     S &st = ((S *)lds)[wave];
-    const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
-    const int64_t tok0 = (int64_t)blockIdx.y * (16 * TM);
-    // Addresses: a base that is the same for the wave and advances with k, and a 32-bit offset per lane.  Rows of x
-    // or of the matrix past the last repeat it: their products fall where nothing is stored.
-    const int rows_left = (int)(p.rows - tok0) - 1;
-    const int n_left = (int)(p.n - row0 < 16 * RT ? p.n - row0 : 16 * RT) - 1;
-    auto clamp = [](int r, int most) { return (uint32_t)(r < most ? r : most); };
-    // load l of x: pieces 64 l + lane; of the matrix: rows 16 l .. 16 l + 15, 4 lanes each
-    uint32_t xo[S::XL], wo[RT];
+    const int64_t row0 = (int64_t)blockIdx.x * 16, tok0 = (int64_t)blockIdx.y * (16 * TM);
+    MatrixRows<GM> m(p, row0, lane);
+    const int most = (int)(p.rows - tok0) - 1;
+    uint32_t xo[XL];
 #pragma unroll
-    for (int l = 0; l < S::XL; ++l)
-        xo[l] = clamp((64 * l + lane) / S::XP, rows_left) * (uint32_t)p.x_stride + (lane % S::XP) * (16 / sizeof(T));
-#pragma unroll
-    for (int l = 0; l < RT; ++l) wo[l] = clamp(16 * l + (lane >> 2), n_left) * (uint32_t)(p.k >> 1) + 16 * (lane & 3);
+    for (int l = 0; l < XL; ++l) {
+        const int r = (64 * l + lane) / XP;
+        xo[l] = (uint32_t)(r < most ? r : most) * (uint32_t)p.x_stride + (lane % XP) * (16 / sizeof(T));
+    }
     const T *xb = (const T *)p.x + tok0 * p.x_stride;
-    const uint8_t *wb = p.q + row0 * (p.k >> 1);
-    // scales and zero points of 4 units: NG RT adjacent ones of row lane / (4 / RT)
-    constexpr int NP = NG * RT, LP = 4 / RT;
-    const uint32_t so = clamp(lane / LP, n_left) * (uint32_t)p.groups + (lane % LP) * NP;
-    const int sg = (lane % LP) * NP;  // its first group among the 4 NG
-    const uint16_t *sb = p.scales + row0 * p.groups;
-    const bool zeros = p.zeros != nullptr;
-    const uint8_t *zb = zeros ? p.zeros + row0 * p.groups : (const uint8_t *)sb;  // (read and not used without zeros)
-
-    f32x4 acc[RT][TM];
+    f32x4 acc[TM];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < TM; ++t) acc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    const Frag ones = {{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
-    const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
-
-    uint4 xv[S::XL], wv[RT];
-    Group<uint16_t, NP> sv;
-    Group<uint8_t, NP> zv;
-    auto load_unit = [&](int u) {
-        const T *xu = xb + (int64_t)u * 128;
-        const uint8_t *wu = wb + (int64_t)u * 64;
-#pragma unroll
-        for (int l = 0; l < S::XL; ++l) {
-            const Raw16 r = *(const Raw16 *)(xu + xo[l]);
-            xv[l] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-        }
-#pragma unroll
-        for (int l = 0; l < RT; ++l) wv[l] = *(const uint4 *)(wu + wo[l]);
+    for (int t = 0; t < TM; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    uint4 xv[XL], wv;
+    auto load_piece = [&](int u, int l) {
+        const Raw16 r = *(const Raw16 *)(xb + (int64_t)u * 128 + xo[l]);
+        return make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     };
-    // of units u .. u + 3; where the row ends before them, its last group again
-    auto load_scales = [&](int u) {
-        const int g0 = u * NG;
-        if (g0 + 4 * NG <= p.groups) {
-            sv = *(const Group<uint16_t, NP> *)(sb + g0 + so);
-            zv = *(const Group<uint8_t, NP> *)(zb + g0 + so);
-        } else {
+    auto load_unit = [&](int u) {
+        wv = m.load(u);
 #pragma unroll
-            for (int a = 0; a < NP; ++a) {
-                const int over = g0 + sg + a - (p.groups - 1);
-                sv.v[a] = sb[g0 + so + a - (over > 0 ? over : 0)];
-                zv.v[a] = zb[g0 + so + a - (over > 0 ? over : 0)];
-            }
-        }
+        for (int l = 0; l < XL; ++l) xv[l] = load_piece(u, l);
     };
     auto store_unit = [&]() {
 #pragma unroll
-        for (int l = 0; l < S::XL; ++l) st.x[S::xat((64 * l + lane) / S::XP, lane % S::XP)] = xv[l];
-#pragma unroll
-        for (int l = 0; l < RT; ++l) st.w[S::wat(16 * l + (lane >> 2), lane & 3)] = wv[l];
+        for (int l = 0; l < XL; ++l) {
+            const int r = (64 * l + lane) / XP;
+            st.x[r * XP + ((lane % XP) ^ (r & 15))] = xv[l];
+        }
+        st.w[w_at(lane >> 2, lane & 3)] = wv;
     };
-    auto store_scales = [&]() {
-#pragma unroll
-        for (int a = 0; a < NP; ++a) st.sz[lane * NP + a] = (uint32_t)sv.v[a] << 16 | (zeros ? zv.v[a] & 15 : 8);
-    };
-    // q: the unit's number among the 4 whose scales are staged
     auto compute = [&](int q) {
-        f32x4 part[RT][TM], xs[TM];
+        Split<T> sx[TM][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            Split<T> sx[TM];
+        for (int t = 0; t < TM; ++t)
 #pragma unroll
-            for (int t = 0; t < TM; ++t) {
+            for (int j = 0; j < 4; ++j) {
                 Raw8<T> r;
 #pragma unroll
-                for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-                    const uint4 v = st.x[S::xat(16 * t + i, (4 * j + g) * ((int)sizeof(T) / 2) + h)];
+                for (int h = 0; h < H; ++h) {
+                    const uint4 v = st.x[(16 * t + i) * XP + (((4 * j + g) * H + h) ^ i)];
                     r.w[4 * h] = v.x, r.w[4 * h + 1] = v.y, r.w[4 * h + 2] = v.z, r.w[4 * h + 3] = v.w;
                 }
-                sx[t] = split_x<T>(r);
-#pragma unroll
-                for (int e = 0; e < NS; ++e)
-                    xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sx[t].f[e]), frag(ones),
-                                                                   j % GM == 0 && e == 0 ? nil : xs[t], 0, 0, 0);
+                sx[t][j] = split_x<T>(r);
             }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const Frag w = dequant(((const uint32_t *)&st.w[S::wat(16 * r + i, j)])[g]);
-#pragma unroll
-                for (int t = 0; t < TM; ++t)
-#pragma unroll
-                    for (int e = 0; e < NS; ++e)
-                        part[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sx[t].f[e]), frag(w),
-                                                                            j % GM == 0 && e == 0 ? nil : part[r][t], 0, 0, 0);
-            }
-            if (j % GM == GM - 1) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const uint32_t v = st.sz[(16 * r + i) * 4 * NG + q * NG + j / GM];
-                    const float s = __uint_as_float(v & 0xFFFF0000u), z = -16.f - (float)(v & 255);
-#pragma unroll
-                    for (int t = 0; t < TM; ++t)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[r][t][c] = fmaf(s, fmaf(z, xs[t][c], part[r][t][c]), acc[r][t][c]);
-                }
-            }
-        }
+        unit_products<GM, TM, NS>([&](int t, int e, int j) { return sx[t][j].f[e]; }, st.w, st.sz, q, i, g, acc);
     };
-    // this wave's whole units, the next one (and the next four's scales) in flight during each
     const int whole = p.k >> 7;
     const int u0 = wave * p.upw, u1 = u0 + p.upw < whole ? u0 + p.upw : whole;
     if (u0 < u1) {
-        load_scales(u0);
+        m.load_scales(u0);
         load_unit(u0);
+        auto step = [&](int u, auto qc) {
+            constexpr int q = decltype(qc)::value;
+            if constexpr (q == 0) {
+                m.store_scales(st.sz);
+                m.load_scales(u + 4);
+            }
+            store_unit();
+            load_unit(u + 1 < u1 ? u + 1 : u);
+            compute(q);
+        };
+        for (int u = u0; u < u1; u += 4) {
+            step(u, IntC<0>{});
+            if (u + 1 >= u1) break;
+            step(u + 1, IntC<1>{});
+            if (u + 2 >= u1) break;
+            step(u + 2, IntC<2>{});
+            if (u + 3 >= u1) break;
+            step(u + 3, IntC<3>{});
+        }
     }
-    for (int u = u0; u < u1; ++u) {
-        const int q = (u - u0) & 3;
-        if (q == 0) {
-            store_scales();
-            load_scales(u + 4 < u1 ? u + 4 : u);
-        }
-        store_unit();
-        load_unit(u + 1 < u1 ? u + 1 : u);
-        compute(q);
-    }
-    // what k leaves past the whole units: pieces that exist, the others with x and q of zero
-    if ((p.k & 127) && wave == (int)(blockDim.x >> 6) - 1) {
-        load_scales(whole);
-        const int left = p.k - whole * 128;
+    const int left = p.k - whole * 128;
+    if (left && wave == (int)(blockDim.x >> 6) - 1) {
+        m.load_scales_of_last(whole);
 #pragma unroll
-        for (int l = 0; l < S::XL; ++l) {
-            Raw16 r{};
-            if ((lane % S::XP) * (int)(16 / sizeof(T)) < left) r = *(const Raw16 *)(xb + (int64_t)whole * 128 + xo[l]);
-            xv[l] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        for (int l = 0; l < XL; ++l) {
+            xv[l] = make_uint4(0, 0, 0, 0);
+            if ((lane % XP) * (int)(16 / sizeof(T)) < left) xv[l] = load_piece(whole, l);
         }
-#pragma unroll
-        for (int l = 0; l < RT; ++l) {
-            wv[l] = make_uint4(0, 0, 0, 0);
-            if (32 * (lane & 3) < left) wv[l] = *(const uint4 *)(wb + (int64_t)whole * 64 + wo[l]);
-        }
-        store_scales();
+        wv = make_uint4(0, 0, 0, 0);
+        if (32 * (lane & 3) < left) wv = m.load(whole);
+        m.store_scales(st.sz);
         store_unit();
         compute(0);
     }
@@ -265,48 +389,42 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Params p) {
     float *red = (float *)lds;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int t = 0; t < TM; ++t)
 #pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) red[((wave * RT + r) * TM + t) * 256 + c * 64 + lane] = acc[r][t][c];
+        for (int c = 0; c < 4; ++c) red[(wave * TM + t) * 256 + c * 64 + lane] = acc[t][c];
     __syncthreads();
-    for (int o = tid; o < RT * TM * 256; o += blockDim.x) {
-        const int l = o & 63, c = (o >> 6) & 3, t = (o >> 8) % TM, r = (o >> 8) / TM;
-        const int64_t tok = tok0 + 16 * t + 4 * (l >> 4) + c;
-        const int64_t row = row0 + 16 * r + (l & 15);
+    for (int o = tid; o < TM * 256; o += blockDim.x) {
+        const int l = o & 63, c = (o >> 6) & 3, t = o >> 8;
+        const int64_t tok = tok0 + 16 * t + 4 * (l >> 4) + c, row = row0 + (l & 15);
         if (tok >= p.rows || row >= p.n) continue;
         float v = 0.f;
-        for (int w = 0; w < nw; ++w) v += red[w * RT * TM * 256 + o];
+        for (int w = 0; w < nw; ++w) v += red[w * TM * 256 + o];
         if (p.bias) v += p.bias[row];
         ((T *)p.y)[tok * p.n + row] = Io<T>::to(v);
     }
 }
 
-template <typename T, int GM, int RT, int TM>
-int launch_w4(const W4Params &p, int waves, void *stream) {
-    using S = Stage<T, RT, TM, 4 / GM>;
-    const dim3 grid((unsigned)((p.n + 16 * RT - 1) / (16 * RT)), (unsigned)((p.rows + 16 * TM - 1) / (16 * TM)));
-    const int sums = RT * TM * 1024, per = (int)sizeof(S) > sums ? (int)sizeof(S) : sums;
-    while (waves > 1 && waves * per > 65536) waves >>= 1;  // (64 KB: what a launch gets without asking for more)
-    W4Params c = p;
-    const int units = p.k >> 7 > 0 ? p.k >> 7 : 1;
+template <typename T, int GM, int TM>
+int launch_w4(const W4Params &p, void *stream) {
+    const int64_t tiles = (p.n + 15) / 16, blocks_y = (p.rows + 16 * TM - 1) / (16 * TM);
+    // shared x where that leaves two workgroups per compute unit
+    if (tiles >= 4 * 2 * 256)
+        return enqueue(w4_rows<T, GM, TM>, dim3((unsigned)((tiles + 3) / 4), (unsigned)blocks_y), dim3(256), p, stream);
+    // waves over k: four, or eight where there are few workgroups; at most one per unit
+    const int units = p.k >> 7 > 0 ? p.k >> 7 : 1, per = (int)sizeof(WaveLds<T, TM, 4 / GM>);
+    static_assert(sizeof(WaveLds<T, TM, 4 / GM>) >= TM * 1024, "the sums reuse the stages");
+    int waves = tiles >= 512 ? 4 : 8;
+    while (waves * per > 65536) waves >>= 1;  // (64 KB: what a launch gets without asking for more)
     if (waves > units) waves = units;
+    W4Params c = p;
     c.upw = (units + waves - 1) / waves;
-    return enqueue(w4_kernel<T, GM, RT, TM>, grid, dim3(64 * waves), c, stream, (unsigned)(waves * per));
+    return enqueue(w4_split<T, GM, TM>, dim3((unsigned)tiles, (unsigned)blocks_y), dim3(64 * waves), c, stream,
+                   (unsigned)(waves * per));
 }
 
 template <typename T, int GM>
 int launch_rt(const W4Params &p, int tm, void *stream) {
-    // rows of the matrix per wave: x is staged once for them, so 64 (fp32 x, whose three fragments take
-    // more registers: 32) where that still leaves three workgroups per compute unit, else 16
-    constexpr int RT = sizeof(T) == 2 ? RTV : 2;
-    const int64_t tiles = (p.n + 15) / 16;
-    const bool big = tiles >= RT * 768;
-    // waves over k: four, or eight where there are few workgroups
-    const int waves = (big ? tiles / RT : tiles) >= 512 ? 4 : 8;
-    if (big) return tm == 1 ? launch_w4<T, GM, RT, 1>(p, waves, stream) : launch_w4<T, GM, RT, 2>(p, waves, stream);
-    return tm == 1 ? launch_w4<T, GM, 1, 1>(p, waves, stream) : launch_w4<T, GM, 1, 2>(p, waves, stream);
+    return tm == 1 ? launch_w4<T, GM, 1>(p, stream) : launch_w4<T, GM, 2>(p, stream);
 }
 
 template <typename T>
