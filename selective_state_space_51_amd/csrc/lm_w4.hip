@@ -184,7 +184,7 @@ __device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32
 // staged, split and reordered once for all of them, and no sums are left to join.  x has two buffers: one barrier
 // per unit.  The matrix is loaded two units ahead, x one.
 template <typename T, int GM, int TM>
-__global__ __launch_bounds__(256, 4) void w4_rows(W4Params p) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void w4_rows(W4Params p) {
     constexpr int NS = Split<T>::NS, NG = 4 / GM;
     __shared__ uint4 xl[2][NS][16 * TM * 16];  // bf16 pieces of 8 k, 16 a row
     __shared__ uint4 wl[4][64];
@@ -311,23 +311,22 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
     f32x4 acc[TM];
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    uint4 xv[XL], wv;
+    uint4 xv[XL], wv[4];  // the matrix: four units ahead
     auto load_piece = [&](int u, int l) {
         const Raw16 r = *(const Raw16 *)(xb + (int64_t)u * 128 + xo[l]);
         return make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     };
-    auto load_unit = [&](int u) {
-        wv = m.load(u);
+    auto load_x = [&](int u) {
 #pragma unroll
         for (int l = 0; l < XL; ++l) xv[l] = load_piece(u, l);
     };
-    auto store_unit = [&]() {
+    auto store_unit = [&](const uint4 &w) {
 #pragma unroll
         for (int l = 0; l < XL; ++l) {
             const int r = (64 * l + lane) / XP;
             st.x[r * XP + ((lane % XP) ^ (r & 15))] = xv[l];
         }
-        st.w[w_at(lane >> 2, lane & 3)] = wv;
+        st.w[w_at(lane >> 2, lane & 3)] = w;
     };
     auto compute = [&](int q) {
         Split<T> sx[TM][4];
@@ -348,16 +347,19 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
     const int whole = p.k >> 7;
     const int u0 = wave * p.upw, u1 = u0 + p.upw < whole ? u0 + p.upw : whole;
     if (u0 < u1) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) wv[h] = m.load(u0 + h < u1 ? u0 + h : u0);
         m.load_scales(u0);
-        load_unit(u0);
+        load_x(u0);
         auto step = [&](int u, auto qc) {
             constexpr int q = decltype(qc)::value;
             if constexpr (q == 0) {
                 m.store_scales(st.sz);
                 m.load_scales(u + 4);
             }
-            store_unit();
-            load_unit(u + 1 < u1 ? u + 1 : u);
+            store_unit(wv[q]);
+            load_x(u + 1 < u1 ? u + 1 : u);
+            wv[q] = m.load(u + 4 < u1 ? u + 4 : u);
             compute(q);
         };
         for (int u = u0; u < u1; u += 4) {
@@ -378,10 +380,10 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
             xv[l] = make_uint4(0, 0, 0, 0);
             if ((lane % XP) * (int)(16 / sizeof(T)) < left) xv[l] = load_piece(whole, l);
         }
-        wv = make_uint4(0, 0, 0, 0);
-        if (32 * (lane & 3) < left) wv = m.load(whole);
+        wv[0] = make_uint4(0, 0, 0, 0);
+        if (32 * (lane & 3) < left) wv[0] = m.load(whole);
         m.store_scales(st.sz);
-        store_unit();
+        store_unit(wv[0]);
         compute(0);
     }
     // the waves' sums, in order; element c of lane (i, g): row i of the matrix, row 4 g + c of x
@@ -407,10 +409,12 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
 template <typename T, int GM, int TM>
 int launch_w4(const W4Params &p, void *stream) {
     const int64_t tiles = (p.n + 15) / 16, blocks_y = (p.rows + 16 * TM - 1) / (16 * TM);
-    // shared x where that leaves two workgroups per compute unit
-    if (tiles >= 4 * 2 * 256)
+    // shared x where that leaves two workgroups per compute unit (measured at 1 and 32 rows, k 2,048 / n 16,384: 13.1 and
+    // 18.0 us with it, 8.2 and 13.3 without; n 50,280: 18.8 and 27, without 20.3 and 35)
+        if (tiles >= 4 * 2 * 256)
         return enqueue(w4_rows<T, GM, TM>, dim3((unsigned)((tiles + 3) / 4), (unsigned)blocks_y), dim3(256), p, stream);
-    // waves over k: four, or eight where there are few workgroups; at most one per unit
+    // waves over k: four, or eight where there are few workgroups (n 8,192, k 2,048, one row: 5.6 us with four, 6.3 with
+    // eight; n 16,384: 8.2 and 10.8); at most one per unit
     const int units = p.k >> 7 > 0 ? p.k >> 7 : 1, per = (int)sizeof(WaveLds<T, TM, 4 / GM>);
     static_assert(sizeof(WaveLds<T, TM, 4 / GM>) >= TM * 1024, "the sums reuse the stages");
     int waves = tiles >= 512 ? 4 : 8;
