@@ -48,11 +48,15 @@ __device__ __forceinline__ int64_t slot_of(const Seqs &q, int s) {
 struct Segment {
     int s, t0, len;  // its sequence
     int j;           // its number within the sequence (negative: none)
+    int slot;        // the sequence's cache entry, or negative
+    bool carry;
 };
+// entries past 2^31 are none: slots are int32
+__device__ __forceinline__ int slot_in(const Seqs &q, int v) { return v >= 0 && v < q.nslots ? v : -1; }
 
 // The sequence of a segment is the last one whose first segment is not after it: a search 64 positions wide,
-// whose last round also brings the offsets themselves (one load in all for up to 64 sequences).  Every lane of
-// the wave takes part.
+// whose last round also brings the offsets, slots and carries (one trip to memory in all for up to 64 sequences).
+// Every lane of the wave takes part.
 __device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, int shift, int lane) {
     int lo = 0, n = q.nseq;
     while (n > 64) {
@@ -64,12 +68,21 @@ __device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, int shif
         n -= (c - 1) * step;
         n = n < step ? n : step;
     }
-    const int i = lane < n ? lane : n - 1;
-    const int a = cu_at(q, lo + i), b = cu_at(q, lo + i + 1);
+    const int i = lo + (lane < n ? lane : n - 1);
+    const int a = cu_at(q, i), b = cu_at(q, i + 1);
+    const int sl = q.slots ? q.slots[i] : i, ca = q.carry ? q.carry[i] : 0;
     int c = __popcll(__ballot(lane < n && (a >> shift) + lo + lane <= seg));
     c = __builtin_amdgcn_readfirstlane(c < 1 ? 0 : c - 1);
     const int s = lo + c, t0 = __builtin_amdgcn_readlane(a, c), t1 = __builtin_amdgcn_readlane(b, c);
-    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - (t0 >> shift) - s};
+    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - (t0 >> shift) - s,
+            slot_in(q, __builtin_amdgcn_readlane(sl, c)), __builtin_amdgcn_readlane(ca, c) != 0};
+}
+// a sequence as one segment
+__device__ __forceinline__ Segment whole_sequence(const Seqs &q, int s) {
+    const Range r = range_of(q, s);
+    const int sl = q.slots ? q.slots[s] : s, ca = q.carry ? q.carry[s] : 0;
+    return {s, __builtin_amdgcn_readfirstlane(r.t0), __builtin_amdgcn_readfirstlane(r.len), 0,
+            slot_in(q, __builtin_amdgcn_readfirstlane(sl)), __builtin_amdgcn_readfirstlane(ca) != 0};
 }
 
 // ------------------------------------------------------------------------------------
@@ -138,43 +151,54 @@ __device__ __forceinline__ void store_raw8(T *p, int n, bool vec, const Raw8<T> 
     }
 }
 
-constexpr int kConvShift = 4;  // a thread takes 16 tokens of 8 channels
+// A thread takes 2^SHIFT tokens of 8 channels: 16, or 4 where runs of 16 would leave most of the chip without a
+// wave (a thread's run of 16 is 1,400 instructions).
+constexpr int kConvLong = 4, kConvShort = 2;
 
-// One workgroup: a segment of 16 tokens of one sequence, a block of 8 channels per thread.  Every
-// row of the segment and the width-1 rows before it are read once by the thread (its neighbours in
+// One workgroup: a segment of one sequence, 8 channels per thread.  HBM bound on
+// long batches (28,838 tokens x 4,096 channels bf16: 95 us, 5.0 TB/s); on short ones the chain of loads counts, so the
+// first rows come before the cache's.  Every row of the segment and the width-1 rows before it are read once by the thread (its neighbours in
 // time read those again, from L2).  A sequence's first segment holds at least its first width-1 tokens,
 // so its threads alone need the cached rows: they read them, and then write the sequence's last
 // rows to the cache, in program order on the same addresses.
-template <typename T, int K>
+template <typename T, int K, int SHIFT>
 __global__ __launch_bounds__(256) void conv_packed(ConvParams p) {
-    constexpr int R = 1 << kConvShift, B = sizeof(T) == 2 ? 8 : 4;  // B: rows in flight at a time
+    constexpr int R = 1 << SHIFT, B = sizeof(T) == 2 && R > 4 ? 8 : 4;  // B: rows in flight at a time
+    static_assert(R >= K - 1, "a sequence's first segment holds its first width - 1 tokens");
     const int seg = blockIdx.x;
-    const Segment rg = find_segment(p.q, seg, kConvShift, threadIdx.x & 63);
-    const int s = rg.s, j = rg.j, first = j << kConvShift;
-    if (j < 0 || (j > 0 && first >= rg.len)) return;
     const int64_t c0 = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
-    if (c0 >= p.dim) return;
-    const int nv = (int)(p.dim - c0 < 8 ? p.dim - c0 : 8);
+    const bool live = c0 < p.dim;
+    const int nv = !live ? 0 : (int)(p.dim - c0 < 8 ? p.dim - c0 : 8);
     const bool vec = p.vec != 0;
-    const T *x = (const T *)p.x + (int64_t)rg.t0 * p.x_stride + c0;
-    T *out = (T *)p.out + (int64_t)rg.t0 * p.dim + c0;
+    const Segment g = find_segment(p.q, seg, SHIFT, threadIdx.x & 63);
+    const int first = g.j << SHIFT;
+    if (!live || g.j < 0 || (g.j > 0 && first >= g.len)) return;
+    const T *x = (const T *)p.x + (int64_t)g.t0 * p.x_stride + c0;
+    T *out = (T *)p.out + (int64_t)g.t0 * p.dim + c0;
+    T *st = K > 1 && p.state && g.slot >= 0 ? (T *)p.state + (int64_t)g.slot * (K - 1) * p.dim + c0 : nullptr;
+    const int n = g.len - first < R ? g.len - first : R;
     Raw8<T> win[B + K - 1];  // the rows before the current block, then the block
+    auto load_block = [&](int u0) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            const int t = first + u0 + u < g.len ? first + u0 + u : g.len - 1;
+            win[K - 1 + u] = load_raw8(x + (int64_t)t * p.x_stride, nv, vec);
+        }
+    };
+    if (n > 0) load_block(0);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         win[i] = Raw8<T>{};
         if (first > 0) win[i] = load_raw8(x + (int64_t)(first - (K - 1) + i) * p.x_stride, nv, vec);
+        else if (st && g.carry) win[i] = load_raw8(st + i * p.dim, nv, vec);
     }
+    float f[K][8], b[8];
+    load_filters<K>(p, c0, nv, f, b);
     if constexpr (K > 1) {
-        const int64_t slot = p.state ? slot_of(p.q, s) : -1;
-        if (first == 0 && slot >= 0) {
-            T *st = (T *)p.state + slot * (K - 1) * p.dim + c0;
-            if (p.q.carry && p.q.carry[s]) {
-#pragma unroll
-                for (int i = 0; i < K - 1; ++i) win[i] = load_raw8(st + i * p.dim, nv, vec);
-            }
+        if (first == 0 && st) {
 #pragma unroll
             for (int i = 0; i < K - 1; ++i) {
-                const int at = rg.len - (K - 1) + i;  // row of the sequence, or a cached one where negative
+                const int at = g.len - (K - 1) + i;  // row of the sequence, or a cached one where negative
                 Raw8<T> r{};
                 if (at >= 0) r = load_raw8(x + (int64_t)at * p.x_stride, nv, vec);
 #pragma unroll
@@ -184,17 +208,10 @@ __global__ __launch_bounds__(256) void conv_packed(ConvParams p) {
             }
         }
     }
-    const int n = rg.len - first < R ? rg.len - first : R;
-    float f[K][8], b[8];
-    load_filters<K>(p, c0, nv, f, b);
 #pragma unroll
     for (int u0 = 0; u0 < R; u0 += B) {
         if (u0 >= n) break;
-#pragma unroll
-        for (int u = 0; u < B; ++u) {
-            const int t = first + u0 + u < rg.len ? first + u0 + u : rg.len - 1;
-            win[K - 1 + u] = load_raw8(x + (int64_t)t * p.x_stride, nv, vec);
-        }
+        if (u0 > 0) load_block(u0);
 #pragma unroll
         for (int u = 0; u < B; ++u) {
             if (u0 + u < n) {
@@ -409,25 +426,39 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
         for (int j = 0; j < 4; ++j) {
             if (t + 4 * j >= len) break;
             float yt[4];
-            auto token = [&](auto ic) {
+            // what does not wait for the state first, for four tokens: e = exp(delta A) and u = delta B x
+            float4 Bq[4], Cq[4];
+            float e[4][4], u[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Bq[i] = *(const float4 *)&bc[4 * j + i][4 * q];
+                if constexpr (FULL) Cq[i] = *(const float4 *)&bc[4 * j + i][kN + 4 * q];
+            }
+            auto coef = [&](auto ic) {
                 constexpr int I = decltype(ic)::value;
-                const float4 Bv = *(const float4 *)&bc[4 * j + I][4 * q];
-                float4 Cv;
-                if constexpr (FULL) Cv = *(const float4 *)&bc[4 * j + I][kN + 4 * q];
-                const float bv[4] = {Bv.x, Bv.y, Bv.z, Bv.w};
+                const float bv[4] = {Bq[I].x, Bq[I].y, Bq[I].z, Bq[I].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) e[I][n] = quad_lane<I>(d[j]) * a2[n];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) u[I][n] = quad_lane<I>(dx[j]) * bv[n];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float arg = quad_lane<I>(d[j]) * a2[n], e = __builtin_amdgcn_exp2f(arg);
-                    float u = quad_lane<I>(dx[j]) * bv[n];
-                    if constexpr (ZOH) u *= zoh_phi(e, arg);
-                    h[n] = fmaf(e, h[n], u);
+                    const float arg = e[I][n];
+                    e[I][n] = __builtin_amdgcn_exp2f(arg);
+                    if constexpr (ZOH) u[I][n] *= zoh_phi(e[I][n], arg);
                 }
-                if constexpr (FULL) yt[I] = fmaf(Cv.x, h[0], Cv.y * h[1]) + fmaf(Cv.z, h[2], Cv.w * h[3]);
             };
-            token(std::integral_constant<int, 0>{});
-            token(std::integral_constant<int, 1>{});
-            token(std::integral_constant<int, 2>{});
-            token(std::integral_constant<int, 3>{});
+            coef(std::integral_constant<int, 0>{});
+            coef(std::integral_constant<int, 1>{});
+            coef(std::integral_constant<int, 2>{});
+            coef(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) h[n] = fmaf(e[i][n], h[n], u[i][n]);
+                if constexpr (FULL) yt[i] = fmaf(Cq[i].x, h[0], Cq[i].y * h[1]) + fmaf(Cq[i].z, h[2], Cq[i].w * h[3]);
+            }
             if constexpr (FULL) {
                 // lane q gets the sum of yt[q] over the four lanes
                 const bool b0 = q & 1, b1 = q & 2;
@@ -474,19 +505,13 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     const int64_t ch = c0 + (lane >> 2) < dim ? c0 + (lane >> 2) : dim - 1;
     const float4 av = load_f4(p.A + ch * kN + 4 * q);
     const bool split = p.seg != nullptr;
-    Segment g{seg, 0, 0, 0};
-    if (split) {
-        g = find_segment(p.q, seg, p.shift, lane);
-    } else {
-        const Range r = range_of(p.q, seg);
-        g.t0 = __builtin_amdgcn_readfirstlane(r.t0), g.len = __builtin_amdgcn_readfirstlane(r.len);
-    }
+    const Segment g = split ? find_segment(p.q, seg, p.shift, lane) : whole_sequence(p.q, seg);
     const int first = split ? g.j << p.shift : 0, size = split ? 1 << p.shift : g.len;
     if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
     const bool last = g.len - first <= size;
     if (LAUNCH == 0 && g.j > 0 && last) return;
-    const int64_t slot = p.h ? slot_of(p.q, g.s) : -1, st = dim * kN;
-    float *cache = slot >= 0 ? p.h + slot * st : nullptr;
+    const int64_t st = dim * kN;
+    float *cache = p.h && g.slot >= 0 ? p.h + g.slot * st : nullptr;
     Piece w{g.t0 + first, last ? g.len - first : size, nullptr, nullptr, nullptr};
     if (last) w.h_out = cache;
     else if (LAUNCH == 0) w.h_out = p.seg + seg * st;
@@ -495,7 +520,7 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
     float h[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (LAUNCH == 0) {
-        if (g.j == 0 && cache && p.q.carry && p.q.carry[g.s]) {
+        if (g.j == 0 && cache && g.carry) {
             const float4 v = *(const float4 *)(cache + ch * kN + 4 * q);
             h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
         }
@@ -752,11 +777,16 @@ int causal_conv1d_packed_fwd(const void *x, int64_t x_stride, const float *weigh
     // threads per workgroup: the channel groups of a row, at most 256, in whole waves
     const int64_t groups = (dim + 7) / 8;
     const unsigned block = groups >= 256 ? 256 : (unsigned)((groups + 63) / 64 * 64);
-    const dim3 grid((unsigned)segments(tokens, nseq, kConvShift), (unsigned)((groups + block - 1) / block));
+    // (4,097 tokens x 1,536 channels fp32, 771 waves of runs of 16: 15.7 us with them, 19.6 with runs of 4; 505 tokens in 8
+    // sequences, 117 waves: 9.4 and 5.8)
+    const int shift = segments(tokens, nseq, kConvLong) * ((groups + 63) / 64) >= kSimds / 2 ? kConvLong : kConvShort;
+    const dim3 grid((unsigned)segments(tokens, nseq, shift), (unsigned)((groups + block - 1) / block));
     if (grid.y > kGridY) return SELSCAN_E_UNSUPPORTED;
     void (*k)(ConvParams) = nullptr;
-#define PICK(T) (width == 1 ? conv_packed<T, 1> : width == 2 ? conv_packed<T, 2> : width == 3 ? conv_packed<T, 3> : conv_packed<T, 4>)
-    k = io_dtype == SELSCAN_BF16 ? PICK(uint16_t) : PICK(float);
+#define PICK(T, S) (width == 1 ? conv_packed<T, 1, S> : width == 2 ? conv_packed<T, 2, S> : width == 3 ? conv_packed<T, 3, S> : conv_packed<T, 4, S>)
+#define PICK_T(S) (io_dtype == SELSCAN_BF16 ? PICK(uint16_t, S) : PICK(float, S))
+    k = shift == kConvLong ? PICK_T(kConvLong) : PICK_T(kConvShort);
+#undef PICK_T
 #undef PICK
     return enqueue(k, grid, dim3(block), p, stream);
 }
