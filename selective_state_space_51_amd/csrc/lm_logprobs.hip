@@ -77,25 +77,71 @@ __device__ __forceinline__ float kth_of_wave(float v, int k) {
     return value_of(sizeof(T) == 2 ? (best << 16) | (best & 0x8000u ? 0u : 0xFFFFu) : best);
 }
 
-// One workgroup: PIECES x 256 x 8 logits of one row, in registers.
+// c m as it was taken off the logits: its rounding where that is finite, else nothing (the subtraction came first)
+struct Base {
+    float mc, rest;  // c m = mc + rest
+};
+__device__ __forceinline__ Base base_of(float m, float c) {
+    const float mc = m * c;
+    if (fabsf(mc) < INFINITY) return {mc, fmaf(m, c, -mc)};
+    return {mc, 0.f};
+}
+
+// what a row comes to: from its largest logit m and s, t as they were taken with base_of(m)
+template <typename T, bool WRITE>
+struct RowEnd {
+    float m, c, ls;  // ls: log2 of sum 2^(c (x - m))
+    bool empty, nan;
+
+    // (lead: one thread of those that call this writes)
+    __device__ __forceinline__ RowEnd(const LpParams &p, int row, float m_, float s, float t, bool lead) : m(m_), c(p.c) {
+        const float l = __builtin_amdgcn_logf(s);
+        ls = l - base_of(m, c).rest;
+        empty = s == 0.f, nan = s != s;
+        if (!WRITE || !lead) return;
+        p.stats[2 * (int64_t)row] = m;
+        p.stats[2 * (int64_t)row + 1] = ls * kLn2;
+        p.entropy[row] = empty ? 0.f : (l - t / s) * kLn2;
+        const int64_t y = p.targets[row];
+        float lp = 0.f;
+        if (y >= 0 && y < p.vocab) lp = empty ? -INFINITY : logp(Io<T>::f32(((const T *)p.x)[row * p.stride + y]));
+        p.logprob[row] = lp;
+    }
+    // (c (x - m) exactly as far as x - m is)
+    __device__ __forceinline__ float logp(float x) const { return fmaf(x - m, c, -ls) * kLn2; }
+    __device__ __forceinline__ void put(const LpParams &p, int row, unsigned long long k, int rank) const {
+        if (rank >= p.top) return;
+        p.top_logprob[(int64_t)row * p.top + rank] = logp(value_of((uint32_t)(k >> 32)));
+        p.top_index[(int64_t)row * p.top + rank] = (int64_t)(uint32_t)~(uint32_t)k;
+    }
+    // places from `have` on: fewer logits with a probability than asked for, or (NaN) no order at all
+    __device__ __forceinline__ void pad(const LpParams &p, int row, int have, int tid, int threads) const {
+        for (int i = (nan ? 0 : have) + tid; i < p.top; i += threads) {
+            p.top_logprob[(int64_t)row * p.top + i] = nan ? NAN : -INFINITY;
+            p.top_index[(int64_t)row * p.top + i] = -1;
+        }
+    }
+};
+
+// One workgroup: PIECES x 256 x 8 logits of one row, in registers.  WHOLE: that is all of the row, and the
+// workgroup finishes it; else a slice for logprobs_join.
 //
 // a = c x - fl(c m) takes one fma per logit instead of c (x - m)'s two operations; the rounding of c m is the same
 // for all logits and so a factor of s and t, which the join takes out again (from the exact residue of c m).  Where
 // c m overflows (a row of the type's lowest value), the subtraction comes first.
 //
 // Alternatives: the `top`-th largest of a wave's 64 per-lane maxima is no larger than the slice's `top`-th
-// largest logit, so every logit of the slice that can be among the best is at or above the largest of the four
+// largest logit, so every logit of the slice that can be among the best is at or above the largest of the
 // waves' bounds.  Those few (some hundred for top = 32) are found by the maxima of pieces of 8, gathered in LDS
 // and ranked by counting.  If equal values make them too many, the best are taken out one after another.
-template <typename T, int PIECES>
+template <typename T, int PIECES, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
-    __shared__ float red[4];
-    __shared__ float red2[4][2];
-    __shared__ float bound[4];
-    __shared__ unsigned long long cand[kCand], pick[4];
+    constexpr int NW = kThreads / 64;
+    __shared__ float red[NW], red2[NW][2], bound[NW];
+    __shared__ unsigned long long cand[kCand], pick[NW];
     __shared__ int ncand;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;
+    const int row = WHOLE ? blockIdx.x : blockIdx.x / p.nsl, sl = WHOLE ? 0 : blockIdx.x - row * p.nsl;
     const int base = sl * (PIECES * kThreads * 8);
     const T *x = (const T *)p.x + row * p.stride;
     Raw8<T> r[PIECES];
@@ -117,7 +163,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
         if (lane == 0) bound[wave] = b;
     }
     lds_barrier();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    m = red[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) m = fmaxf(m, red[i]);
     const float mc = m * p.c;  // (-inf: nothing but -inf)
     float s = 0.f, t = 0.f;
     if (fabsf(mc) < INFINITY) {
@@ -143,8 +191,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     s = wave_sum(s), t = wave_sum(t);
     if (lane == 0) red2[wave][0] = s, red2[wave][1] = t;
     if (p.top) {
-        float b = fmaxf(fmaxf(bound[0], bound[1]), fmaxf(bound[2], bound[3]));
-        b = fmaxf(b, -FLT_MAX);  // a logit of -inf is no alternative
+        float b = -FLT_MAX;  // a logit of -inf is no alternative
+#pragma unroll
+        for (int i = 0; i < NW; ++i) b = fmaxf(b, bound[i]);
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             if (pm[i] >= b) {
@@ -160,22 +209,36 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
         }
     }
     lds_barrier();
-    if (tid == 0) {
-        s = (red2[0][0] + red2[1][0]) + (red2[2][0] + red2[3][0]);
-        t = (red2[0][1] + red2[1][1]) + (red2[2][1] + red2[3][1]);
-        p.part[blockIdx.x] = make_float4(m, s, t, 0.f);
+    s = red2[0][0], t = red2[0][1];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) s += red2[i][0], t += red2[i][1];
+    unsigned long long *out = p.cand + (int64_t)blockIdx.x * p.top;  // (a slice's)
+    if constexpr (!WHOLE) {
+        if (tid == 0) p.part[blockIdx.x] = make_float4(m, s, t, 0.f);
     }
+    const RowEnd<T, WHOLE> end(p, row, m, s, t, tid == 0);
     if (!p.top) return;
-    unsigned long long *out = p.cand + (int64_t)blockIdx.x * p.top;
+    if (WHOLE && end.nan) {
+        end.pad(p, row, 0, tid, kThreads);
+        return;
+    }
+    auto put = [&](unsigned long long k, int rank) {
+        if constexpr (WHOLE) end.put(p, row, k, rank);
+        else if (rank < p.top) out[rank] = k;
+    };
     const int n = ncand;
     if (n <= kCand) {
         for (int i = tid; i < n; i += kThreads) {
             const unsigned long long k = cand[i];
             int rank = 0;
             for (int j = 0; j < n; ++j) rank += cand[j] > k ? 1 : 0;
-            if (rank < p.top) out[rank] = k;
+            put(k, rank);
         }
-        for (int i = n + tid; i < p.top; i += kThreads) out[i] = 0;
+        if constexpr (WHOLE) {
+            end.pad(p, row, n, tid, kThreads);
+        } else {
+            for (int i = n + tid; i < p.top; i += kThreads) out[i] = 0;
+        }
         return;
     }
     unsigned long long last = ~0ull;
@@ -200,21 +263,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
         if (lane == 0) pick[wave] = best;
         lds_barrier();
         best = pick[0];
-        for (int i = 1; i < 4; ++i) best = pick[i] > best ? pick[i] : best;
-        if (tid == 0) out[k] = best;
+        for (int i = 1; i < NW; ++i) best = pick[i] > best ? pick[i] : best;
+        if (tid == 0) put(best, k);  // (more than kCand candidates: every round finds one)
         last = best;
         lds_barrier();  // every wave has read the picks before the next round writes them
     }
-}
-
-// c m as a slice took it off: its rounding where that is finite, else nothing (the subtraction came first)
-struct Base {
-    float mc, rest;  // c m = mc + rest
-};
-__device__ __forceinline__ Base base_of(float m, float c) {
-    const float mc = m * c;
-    if (fabsf(mc) < INFINITY) return {mc, fmaf(m, c, -mc)};
-    return {mc, 0.f};
 }
 
 // One workgroup per row: joins the slices.  Alternatives: with `low` the worst over the slices of their place-th entries,
@@ -262,24 +315,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
         t = fmaf(f, fmaf(q.y, fmaxf(d, -200.f), q.z), t);
     }
     s = wave_sum(s), t = wave_sum(t);
-    const bool empty = s == 0.f;
-    const float ls = __builtin_amdgcn_logf(s) - B.rest;  // log2 of sum 2^(c (x - M))
-    // (c (x - M) exactly as far as x - M is)
-    auto logp = [&](float x) { return fmaf(x - M, p.c, -ls) * kLn2; };
-    if (tid == 0) {
-        p.stats[2 * row] = M;
-        p.stats[2 * row + 1] = ls * kLn2;
-        p.entropy[row] = empty ? 0.f : (__builtin_amdgcn_logf(s) - t / s) * kLn2;
-        const int64_t y = p.targets[row];
-        float lp = 0.f;
-        if (y >= 0 && y < p.vocab) lp = empty ? -INFINITY : logp(Io<T>::f32(((const T *)p.x)[row * p.stride + y]));
-        p.logprob[row] = lp;
-    }
+    const RowEnd<T, true> end(p, row, M, s, t, tid == 0);
     if (!p.top) return;
-    float *val = p.top_logprob + (int64_t)row * p.top;
-    int64_t *idx = p.top_index + (int64_t)row * p.top;
-    if (s != s) {
-        for (int i = tid; i < p.top; i += blockDim.x) val[i] = NAN, idx[i] = -1;
+    if (end.nan) {
+        end.pad(p, row, 0, tid, blockDim.x);
         return;
     }
     __syncthreads();
@@ -295,17 +334,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
     }
     __syncthreads();
     const int have = count;
-    auto put = [&](unsigned long long k, int rank) {
-        if (rank >= p.top) return;
-        val[rank] = logp(value_of((uint32_t)(k >> 32)));
-        idx[rank] = (int64_t)(uint32_t)~(uint32_t)k;
-    };
     if (have <= kCand) {
         for (int i = tid; i < have; i += blockDim.x) {
             const unsigned long long k = list[i];
             int rank = 0;
             for (int j = 0; j < have; ++j) rank += list[j] > k ? 1 : 0;
-            put(k, rank);
+            end.put(p, row, k, rank);
         }
     } else {
         // the best sit together in a few of very many slices
@@ -313,11 +347,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
             const unsigned long long k = cand[i];
             int rank = k >= low ? 0 : p.top;
             for (int j = 0; j < n && rank < p.top; ++j) rank += cand[j] > k ? 1 : 0;
-            put(k, rank);
+            end.put(p, row, k, rank);
         }
     }
-    // fewer logits with a probability than alternatives asked for
-    for (int i = have + tid; i < p.top; i += blockDim.x) val[i] = -INFINITY, idx[i] = -1;
+    end.pad(p, row, have, tid, blockDim.x);
 }
 
 constexpr int kBwdPieces = 4;
@@ -371,6 +404,9 @@ int pieces_for(int64_t rows, int64_t vocab) {
     const int64_t big = 4 * kThreads * 8;
     return rows * ((vocab + big - 1) / big) >= 1024 || vocab > kMaxVocab / 2 ? 4 : 2;
 }
+// rows of a slice's length need no join.  (Longer ones by a workgroup of 16 waves measured slower than slices and a join: 7 x
+// 50,280 bf16 with eight alternatives 11.0 us against 9.3.)
+bool whole_row(int64_t vocab) { return vocab <= 4 * kThreads * 8; }
 int64_t slices_for(int64_t rows, int64_t vocab) {
     const int64_t n = (int64_t)pieces_for(rows, vocab) * kThreads * 8;
     return (vocab + n - 1) / n;
@@ -392,6 +428,7 @@ extern "C" {
 
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
     if (rows <= 0 || vocab <= 0 || vocab > kMaxVocab || top < 0 || top > kMaxTop) return 0;
+    if (whole_row(vocab)) return 0;
     const size_t n = (size_t)rows * (size_t)slices_for(rows, vocab);
     return n * (sizeof(float4) + (size_t)top * 8);
 }
@@ -404,34 +441,39 @@ int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t 
     if (top < 0 || top > kMaxTop) return SELSCAN_E_UNSUPPORTED;
     if (rows == 0) return SELSCAN_OK;
     if (vocab == 0 || top > vocab) return SELSCAN_E_SHAPE;
+    const size_t need = token_logprobs_workspace_bytes(rows, vocab, top);
     if (!logprob || !entropy || !stats || (top && (!top_logprob || !top_index))) return SELSCAN_E_NULL;
     if (!span_aligned(logprob, 4) || !span_aligned(entropy, 4) || !span_aligned(stats, 4) ||
-        (top && (!span_aligned(top_logprob, 4) || !span_aligned(top_index, 8))) || !span_aligned(workspace, 16))
+        (top && (!span_aligned(top_logprob, 4) || !span_aligned(top_index, 8))) || (need && !span_aligned(workspace, 16)))
         return SELSCAN_E_ALIGN;
-    const size_t need = token_logprobs_workspace_bytes(rows, vocab, top);
-    if (!workspace || workspace_bytes < need) return SELSCAN_E_WORKSPACE;
+    if (need && (!workspace || workspace_bytes < need)) return SELSCAN_E_WORKSPACE;
     const Span in[] = {{logits, strided_bytes(rows, vocab, logits_stride, io_bytes(io_dtype))}, {targets, (size_t)rows * 8}};
     const Span out[] = {{logprob, (size_t)rows * 4},
                         {entropy, (size_t)rows * 4},
                         {stats, (size_t)rows * 8},
                         {top ? top_logprob : nullptr, (size_t)rows * top * 4},
                         {top ? top_index : nullptr, (size_t)rows * top * 8},
-                        {workspace, need}};
+                        {need ? workspace : nullptr, need}};
     if (any_alias(in, 2, out, 6)) return SELSCAN_E_ALIAS;
     LpParams p{};
     p.x = logits, p.targets = targets, p.logprob = logprob, p.entropy = entropy, p.stats = stats;
     p.top_logprob = top_logprob, p.top_index = top_index;
     p.rows = rows, p.stride = logits_stride, p.vocab = (int)vocab, p.top = top;
     p.scale = scale, p.c = scale * kLog2e;
+    const bool bf = io_dtype == SELSCAN_BF16;
+    if (whole_row(vocab)) {
+        if (rows > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+        return enqueue(bf ? logprobs_slice<uint16_t, 4, true> : logprobs_slice<float, 4, true>, dim3((unsigned)rows), dim3(kThreads), p,
+                       stream);
+    }
     const int pieces = pieces_for(rows, vocab);
     p.nsl = (int)slices_for(rows, vocab);
     const int64_t blocks = rows * p.nsl;
     if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     p.part = (float4 *)workspace;
     p.cand = (unsigned long long *)(p.part + blocks);
-    const bool bf = io_dtype == SELSCAN_BF16;
-    void (*k)(LpParams) = pieces == 4 ? (bf ? logprobs_slice<uint16_t, 4> : logprobs_slice<float, 4>)
-                                      : (bf ? logprobs_slice<uint16_t, 2> : logprobs_slice<float, 2>);
+    void (*k)(LpParams) = pieces == 4 ? (bf ? logprobs_slice<uint16_t, 4, false> : logprobs_slice<float, 4, false>)
+                                      : (bf ? logprobs_slice<uint16_t, 2, false> : logprobs_slice<float, 2, false>);
     rc = enqueue(k, dim3((unsigned)blocks), dim3(kThreads), p, stream);
     if (rc != SELSCAN_OK) return rc;
     return enqueue(bf ? logprobs_join<uint16_t> : logprobs_join<float>, dim3((unsigned)rows),

@@ -41,10 +41,10 @@ __device__ __forceinline__ int64_t slot_of(const Seqs &q, int s) {
     return v >= 0 && v < q.nslots ? v : -1;
 }
 
-// Segments of 2^shift tokens, without a pass over the lengths: sequence s owns the segment numbers
-// from (cu[s] >> shift) + s to the next sequence's first, exclusively.  They are at least
-// ceil(len / 2^shift) and at least one (floor(a + b) + 1 >= ceil(b) + floor(a)), and all of them together at
-// most (tokens >> shift) + nseq, which the host knows; those past a sequence's end have nothing to do.
+// Segments of z tokens, without a pass over the lengths: sequence s owns the segment numbers
+// from floor(cu[s] / z) + s to the next sequence's first, exclusively.  They are at least
+// ceil(len / z) and at least one (floor(a + b) + 1 >= ceil(b) + floor(a)), and all of them together at
+// most floor(tokens / z) + nseq, which the host knows; those past a sequence's end have nothing to do.
 struct Segment {
     int s, t0, len;  // its sequence
     int j;           // its number within the sequence (negative: none)
@@ -56,12 +56,13 @@ __device__ __forceinline__ int slot_in(const Seqs &q, int v) { return v >= 0 && 
 
 // The sequence of a segment is the last one whose first segment is not after it: a search 64 positions wide,
 // whose last round also brings the offsets, slots and carries (one trip to memory in all for up to 64 sequences).
-// Every lane of the wave takes part.
-__device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, int shift, int lane) {
+// Every lane of the wave takes part.  div_z: division by z.
+template <class F>
+__device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, F div_z, int lane) {
     int lo = 0, n = q.nseq;
     while (n > 64) {
         const int step = (n + 63) >> 6, i = lane * step;
-        const bool at_or_before = i < n && (cu_at(q, lo + i) >> shift) + lo + i <= seg;
+        const bool at_or_before = i < n && div_z(cu_at(q, lo + i)) + lo + i <= seg;
         int c = __popcll(__ballot(at_or_before));
         c = c < 1 ? 1 : c;
         lo += (c - 1) * step;
@@ -71,10 +72,10 @@ __device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, int shif
     const int i = lo + (lane < n ? lane : n - 1);
     const int a = cu_at(q, i), b = cu_at(q, i + 1);
     const int sl = q.slots ? q.slots[i] : i, ca = q.carry ? q.carry[i] : 0;
-    int c = __popcll(__ballot(lane < n && (a >> shift) + lo + lane <= seg));
+    int c = __popcll(__ballot(lane < n && div_z(a) + lo + lane <= seg));
     c = __builtin_amdgcn_readfirstlane(c < 1 ? 0 : c - 1);
     const int s = lo + c, t0 = __builtin_amdgcn_readlane(a, c), t1 = __builtin_amdgcn_readlane(b, c);
-    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - (t0 >> shift) - s,
+    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - __builtin_amdgcn_readfirstlane(div_z(t0)) - s,
             slot_in(q, __builtin_amdgcn_readlane(sl, c)), __builtin_amdgcn_readlane(ca, c) != 0};
 }
 // a sequence as one segment
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(256) void conv_packed(ConvParams p) {
     const bool live = c0 < p.dim;
     const int nv = !live ? 0 : (int)(p.dim - c0 < 8 ? p.dim - c0 : 8);
     const bool vec = p.vec != 0;
-    const Segment g = find_segment(p.q, seg, SHIFT, threadIdx.x & 63);
+    const Segment g = find_segment(p.q, seg, [](int v) { return v >> SHIFT; }, threadIdx.x & 63);
     const int first = g.j << SHIFT;
     if (!live || g.j < 0 || (g.j > 0 && first >= g.len)) return;
     const T *x = (const T *)p.x + (int64_t)g.t0 * p.x_stride + c0;
@@ -314,7 +315,9 @@ struct ScanParams {
     float *sdt;   // split: [nsegs][dim] sum of delta over the segment
     Seqs q;
     int64_t dim, bc_stride, z_stride;
-    int softplus, shift;
+    int softplus;
+    int size;      // split: tokens of a segment, and division by it
+    FastDiv dsize;
     int ntiles;    // blocks of 64 channels
     int joined;    // split: scan_join runs between the launches
     int rows_per;  // step: rows a thread takes one after another
@@ -505,8 +508,9 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     const int64_t ch = c0 + (lane >> 2) < dim ? c0 + (lane >> 2) : dim - 1;
     const float4 av = load_f4(p.A + ch * kN + 4 * q);
     const bool split = p.seg != nullptr;
-    const Segment g = split ? find_segment(p.q, seg, p.shift, lane) : whole_sequence(p.q, seg);
-    const int first = split ? g.j << p.shift : 0, size = split ? 1 << p.shift : g.len;
+    const Segment g = split ? find_segment(p.q, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane)
+                            : whole_sequence(p.q, seg);
+    const int first = split ? g.j * p.size : 0, size = split ? p.size : g.len;
     if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
     const bool last = g.len - first <= size;
     if (LAUNCH == 0 && g.j > 0 && last) return;
@@ -563,7 +567,8 @@ __global__ __launch_bounds__(256) void scan_join(ScanParams p) {
     const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x, ch = i / kN, st = p.dim * kN;
     if (ch >= p.dim) return;
     const float a2 = p.A[i] * kLog2e;
-    const int first = (rg.t0 >> p.shift) + s, n = ((rg.len + (1 << p.shift) - 1) >> p.shift) - 1;  // all but the last
+    const int first = (int)fdiv((uint32_t)rg.t0, p.dsize) + s;
+    const int n = (int)fdiv((uint32_t)(rg.len + p.size - 1), p.dsize) - 1;  // all but the last
     if (n < 2) return;
     float *e = p.seg + (int64_t)first * st + i;
     const float *d = p.sdt + (int64_t)first * p.dim + ch;
@@ -631,32 +636,33 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
     }
 }
 
-// Tokens per segment as a power of two, or 0: whole sequences.  In clocks of a SIMD, a wave's token
-// takes 245 alone and 150 beside others (measured); a segment's map takes 115.  Whole sequences: the longest alone,
-// or all evenly plus a quarter for lengths that do not even out.  Segments: both passes, and 25,000 for the second
-// launch and the join.
-constexpr int kSimds = 1024;  // MI355X: 256 compute units of 4
-constexpr int kWalk = 16;     // segments up to which the second launch walks the maps itself
+// Tokens per segment, or 0: whole sequences.
+//  - In clocks of a SIMD a wave's token takes 245 alone and 150 beside others (measured), a map's 115.  Whole sequences take
+//    the longest alone, or all evenly plus a quarter for lengths that do not even out; segments take both passes, and 25,000
+//    for the second launch and the join.
+//  - Segments of multiples of 16 (a block) that give each compute unit four workgroups: measured, 4,097 tokens x 1,536
+//    channels fp32 72 us at 96 tokens (4.0 workgroups per unit), 74 at 64, 79 at 112, 90 at 176 and 434 whole; 505 tokens in 8
+//    sequences x 1,536 bf16 18 us at 16, 20 at 32, 22 at 64 and 34 whole; 28,838 tokens in 24 sequences x 4,096 734 us at
+//    256, and 650 whole.
+constexpr int kSimds = 1024, kUnits = 256;  // MI355X: 256 compute units of 4
+constexpr int kWalk = 16;                   // segments up to which the second launch walks the maps itself
 
-int split_shift(int64_t tokens, int64_t max_seqlen, int64_t dim) {
-    const int64_t tiles = (dim + 15) / 16;
+int64_t segments(int64_t tokens, int64_t nseq, int64_t size) { return tokens / size + nseq; }
+
+int split_size(int64_t tokens, int64_t max_seqlen, int64_t dim) {
+    const int64_t tiles = (dim + 15) / 16, blocks = (dim + 63) / 64;
     const int64_t longest = max_seqlen < tokens ? max_seqlen : tokens;
     const int64_t share = (tokens * tiles + kSimds - 1) / kSimds;  // token times of a SIMD if all is even
     const int64_t whole = longest * 245 > share * 188 ? longest * 245 : share * 188;
     if (whole <= share * 265 + 25000) return 0;
-    // from 32 tokens up to what still leaves some four waves per SIMD: measured, 4,097 tokens x 96 tiles take 75 us at
-    // 128 tokens, 77 at 64, 90 at 256 and 434 whole; 505 tokens in 8 sequences x 96 tiles 20 us at 32, 23 at
-    // 64 and 34 whole
-    int shift = 5;
-    while (shift < 12 && (tokens >> shift) * tiles > 4 * kSimds) ++shift;
-    return (INT64_C(2) << shift) > longest ? 0 : shift;
+    const int64_t even = (tokens * blocks / (4 * kUnits) + 8) / 16 * 16;
+    const int size = (int)(even < 16 ? 16 : even > 4096 ? 4096 : even);
+    return 2 * size <= longest ? size : 0;
 }
 
-int64_t segments(int64_t tokens, int64_t nseq, int shift) { return (tokens >> shift) + nseq; }
-
 size_t packed_workspace(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim) {
-    const int shift = split_shift(tokens, max_seqlen, dim);
-    return shift ? (size_t)segments(tokens, nseq, shift) * (size_t)dim * (kN + 1) * sizeof(float) : 0;
+    const int size = split_size(tokens, max_seqlen, dim);
+    return size ? (size_t)segments(tokens, nseq, size) * (size_t)dim * (kN + 1) * sizeof(float) : 0;
 }
 
 struct ScanArgs {
@@ -779,8 +785,8 @@ int causal_conv1d_packed_fwd(const void *x, int64_t x_stride, const float *weigh
     const unsigned block = groups >= 256 ? 256 : (unsigned)((groups + 63) / 64 * 64);
     // (4,097 tokens x 1,536 channels fp32, 771 waves of runs of 16: 15.7 us with them, 19.6 with runs of 4; 505 tokens in 8
     // sequences, 117 waves: 9.4 and 5.8)
-    const int shift = segments(tokens, nseq, kConvLong) * ((groups + 63) / 64) >= kSimds / 2 ? kConvLong : kConvShort;
-    const dim3 grid((unsigned)segments(tokens, nseq, shift), (unsigned)((groups + block - 1) / block));
+    const int shift = segments(tokens, nseq, 1 << kConvLong) * ((groups + 63) / 64) >= kSimds / 2 ? kConvLong : kConvShort;
+    const dim3 grid((unsigned)segments(tokens, nseq, 1 << shift), (unsigned)((groups + block - 1) / block));
     if (grid.y > kGridY) return SELSCAN_E_UNSUPPORTED;
     void (*k)(ConvParams) = nullptr;
 #define PICK(T, S) (width == 1 ? conv_packed<T, 1, S> : width == 2 ? conv_packed<T, 2, S> : width == 3 ? conv_packed<T, 3, S> : conv_packed<T, 4, S>)
@@ -835,11 +841,12 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
     p.ntiles = (int)((dim + 63) / 64);
     int64_t pieces = nseq;
     if (need) {
-        p.shift = split_shift(tokens, max_seqlen, dim);
-        pieces = segments(tokens, nseq, p.shift);
+        p.size = split_size(tokens, max_seqlen, dim);
+        p.dsize = make_div((uint32_t)p.size);
+        pieces = segments(tokens, nseq, p.size);
         p.seg = (float *)workspace;
         p.sdt = p.seg + pieces * dim * kN;
-        p.joined = (max_seqlen >> p.shift) > kWalk ? 1 : 0;
+        p.joined = max_seqlen / p.size > kWalk ? 1 : 0;
     }
     // (the join's grid: 16 channels per workgroup)
     if (pieces * p.ntiles > INT32_MAX || (dim * kN + 255) / 256 > kGridY) return SELSCAN_E_UNSUPPORTED;

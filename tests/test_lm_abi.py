@@ -162,10 +162,13 @@ def test_logprobs_refusals():
     assert lp_fwd(top=33) == UNSUPPORTED and lp_fwd(top=-1) == UNSUPPORTED and lp_fwd(dt=4) == UNSUPPORTED
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert lp_fwd(scale=s) == UNSUPPORTED
-    assert lp_fwd(t=P + MB + 4) == ALIGN and lp_fwd(ws=P + 5 * MB + 8) == ALIGN and lp_fwd(x=P + 1) == ALIGN
-    need = S.token_logprobs_workspace_bytes(4, 100, 0)
-    assert need > 0 and lp_fwd(wsb=need - 1) == WORKSPACE and lp_fwd(ws=None) == WORKSPACE
-    assert lp_fwd(lp=P + 8) == ALIAS and lp_fwd(ent=P + 2 * MB) == ALIAS and lp_fwd(ws=P + 4 * MB) == ALIAS
+    assert lp_fwd(t=P + MB + 4) == ALIGN and lp_fwd(x=P + 1) == ALIGN
+    assert S.token_logprobs_workspace_bytes(4, 100, 0) == 0  # one workgroup takes a whole row
+    big = dict(vocab=90_000, xs=90_000, x=P + 100 * MB)
+    need = S.token_logprobs_workspace_bytes(4, 90_000, 0)
+    assert need > 0 and lp_fwd(**big, wsb=need - 1) == WORKSPACE and lp_fwd(**big, ws=None) == WORKSPACE
+    assert lp_fwd(**big, ws=P + 5 * MB + 8) == ALIGN and lp_fwd(**big, ws=P + 4 * MB) == ALIAS
+    assert lp_fwd(lp=P + 8) == ALIAS and lp_fwd(ent=P + 2 * MB) == ALIAS
 
 
 def lp_bwd(x=P, xs=100, t=P + MB, st=P + 2 * MB, ent=P + 3 * MB, dl=P + 4 * MB, dh=None, scale=1.0, dx=P + 5 * MB, rows=4,
