@@ -86,6 +86,26 @@ __device__ __forceinline__ Segment whole_sequence(const Seqs &q, int s) {
             slot_in(q, __builtin_amdgcn_readfirstlane(sl)), __builtin_amdgcn_readfirstlane(ca) != 0};
 }
 
+// The sequence that stands at place `place` when whole sequences are dealt to the chip (up to 64 of them): longest first, and
+// every second round of `round` sequences (those whose workgroups fill the compute units once) in rising order, so that the
+// units that got a round's longest get the next one's shortest. Twenty-four prompts of 1 to 4,096 tokens, 27,591 in all, x 4,096
+// channels: 636 us against 675 as they come, and 532 to 566 against 600 to 708 in four other orders of the same prompts.
+__device__ __forceinline__ Segment dealt_sequence(const Seqs &q, int place, int round, int lane) {
+    const int n = q.nseq, i = lane < n ? lane : n - 1;
+    const int a = cu_at(q, i), b = cu_at(q, i + 1), len = b > a ? b - a : 0;
+    const int sl = q.slots ? q.slots[i] : i, ca = q.carry ? q.carry[i] : 0;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane) ? 1 : 0;
+    }
+    const int k = place / round, first = k * round, m = n - first < round ? n - first : round;
+    const int want = k & 1 ? first + m - 1 - (place - first) : place;
+    const int s = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(lane < n && rank == want)));
+    return {s, __builtin_amdgcn_readlane(a, s), __builtin_amdgcn_readlane(len, s), 0,
+            slot_in(q, __builtin_amdgcn_readlane(sl, s)), __builtin_amdgcn_readlane(ca, s) != 0};
+}
+
 // ------------------------------------------------------------------------------------
 // convolution
 // ------------------------------------------------------------------------------------
@@ -157,7 +177,7 @@ __device__ __forceinline__ void store_raw8(T *p, int n, bool vec, const Raw8<T> 
 constexpr int kConvLong = 4, kConvShort = 2;
 
 // One workgroup: a segment of one sequence, 8 channels per thread.  HBM bound on
-// long batches (28,838 tokens x 4,096 channels bf16: 95 us, 5.0 TB/s); on short ones the chain of loads counts, so the
+// long batches (27,591 tokens x 4,096 channels bf16: 95 us, 5.0 TB/s); on short ones the chain of loads counts, so the
 // first rows come before the cache's.  Every row of the segment and the width-1 rows before it are read once by the thread (its neighbours in
 // time read those again, from L2).  A sequence's first segment holds at least its first width-1 tokens,
 // so its threads alone need the cached rows: they read them, and then write the sequence's last
@@ -319,6 +339,7 @@ struct ScanParams {
     int size;      // split: tokens of a segment, and division by it
     FastDiv dsize;
     int ntiles;    // blocks of 64 channels
+    int round;     // whole sequences: how many fill the compute units once (0: taken as they come)
     int joined;    // split: scan_join runs between the launches
     int rows_per;  // step: rows a thread takes one after another
 };
@@ -509,7 +530,8 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     const float4 av = load_f4(p.A + ch * kN + 4 * q);
     const bool split = p.seg != nullptr;
     const Segment g = split ? find_segment(p.q, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane)
-                            : whole_sequence(p.q, seg);
+                      : p.round ? dealt_sequence(p.q, seg, p.round, lane)
+                                : whole_sequence(p.q, seg);
     const int first = split ? g.j * p.size : 0, size = split ? p.size : g.len;
     if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
     const bool last = g.len - first <= size;
@@ -642,7 +664,7 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
 //    for the second launch and the join.
 //  - Segments of multiples of 16 (a block) that give each compute unit four workgroups: measured, 4,097 tokens x 1,536
 //    channels fp32 72 us at 96 tokens (4.0 workgroups per unit), 74 at 64, 79 at 112, 90 at 176 and 434 whole; 505 tokens in 8
-//    sequences x 1,536 bf16 18 us at 16, 20 at 32, 22 at 64 and 34 whole; 28,838 tokens in 24 sequences x 4,096 734 us at
+//    sequences x 1,536 bf16 18 us at 16, 20 at 32, 22 at 64 and 34 whole; 27,591 tokens in 24 sequences x 4,096 734 us at
 //    256, and 650 whole.
 constexpr int kSimds = 1024, kUnits = 256;  // MI355X: 256 compute units of 4
 constexpr int kWalk = 16;                   // segments up to which the second launch walks the maps itself
@@ -840,7 +862,10 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
     ScanParams p = scan_params(a);
     p.ntiles = (int)((dim + 63) / 64);
     int64_t pieces = nseq;
-    if (need) {
+    if (!need) {
+        const int round = p.ntiles < kUnits ? kUnits / p.ntiles : 1;
+        p.round = nseq <= 64 && nseq > round ? round : 0;
+    } else {
         p.size = split_size(tokens, max_seqlen, dim);
         p.dsize = make_div((uint32_t)p.size);
         pieces = segments(tokens, nseq, p.size);
