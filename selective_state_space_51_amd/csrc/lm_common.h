@@ -110,6 +110,24 @@ __device__ __forceinline__ float wave_reduce(float v, float identity, F f) {
 __device__ __forceinline__ float wave_sum(float v) {
     return wave_reduce(v, 0.f, [](float a, float b) { return a + b; });
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+    const int64_t b = __double_as_longlong(v);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((int64_t)hi << 32 | (uint32_t)lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v += dpp_or_zero<0x111, 0xF>(v);
+    v += dpp_or_zero<0x112, 0xF>(v);
+    v += dpp_or_zero<0x114, 0xF>(v);
+    v += dpp_or_zero<0x118, 0xF>(v);
+    v += dpp_or_zero<0x142, 0xA>(v);
+    v += dpp_or_zero<0x143, 0xC>(v);
+    const int64_t b = __double_as_longlong(v);
+    const int lo = __builtin_amdgcn_readlane((int)b, 63), hi = __builtin_amdgcn_readlane((int)(b >> 32), 63);
+    return __longlong_as_double((int64_t)hi << 32 | (uint32_t)lo);
+}
 __device__ __forceinline__ float wave_max(float v) {
     return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }

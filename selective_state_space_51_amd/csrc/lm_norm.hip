@@ -18,7 +18,8 @@ struct NormParams {
     int64_t rows, x_stride;
     int width, kind, slots;
     int64_t rows_per;          // backward: consecutive rows of a slot
-    float eps, inv_width;
+    float eps, inv_width;      // (inv_width: backward; inv_width64: forward)
+    double inv_width64;
 };
 
 // element e of piece v of a thread: 8 adjacent ones (rows that move as 16-byte vectors), or elements TPR
@@ -58,19 +59,23 @@ __device__ __forceinline__ void store_piece(T *row, int v, int tr, int width, co
     }
 }
 
-// the sum (or maximum) over the TPR threads of a row; sh: one float per wave of the workgroup, two buffers
+// the sum (or maximum) over the TPR threads of a row; sh: one value per wave of the workgroup, two buffers
 // used in turn (buf), so that one barrier per reduction is enough
-template <int TPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float *sh, int buf) {
-    v = MAX ? wave_max(v) : wave_sum(v);
+template <int TPR, bool MAX, typename V>
+__device__ __forceinline__ V row_reduce(V v, V *sh, int buf) {
+    if constexpr (MAX) v = wave_max(v);
+    else v = wave_sum(v);
     if constexpr (TPR > 64) {
         constexpr int NW = TPR / 64;
-        float *s = sh + buf * NW;
+        V *s = sh + buf * NW;
         if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
         lds_barrier();
         v = s[0];
 #pragma unroll
-        for (int i = 1; i < NW; ++i) v = MAX ? fmaxf(v, s[i]) : v + s[i];
+        for (int i = 1; i < NW; ++i) {
+            if constexpr (MAX) v = fmaxf(v, s[i]);
+            else v += s[i];
+        }
     }
     return v;
 }
@@ -94,16 +99,20 @@ __device__ __forceinline__ uint2 pack8(const float (&q)[8]) {
     return make_uint2(w[0], w[1]);
 }
 
+// Forward.  The squares are added in 64 bits, which hides behind the row's loads: rstd is then the rounded exact one whatever
+// the split over threads, and a value between two steps of an 8-bit output does not move with the width's thread count.
 template <typename T, typename R, int TPR, int NV, bool VEC>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) {
     constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-    __shared__ float sh[2 * (BLOCK / 64)];
+    __shared__ double sums[BLOCK / 64];
+    __shared__ float sh[BLOCK / 64];
     const int tr = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
     if (row >= p.rows) return;  // with more than one row per workgroup, rows do not share barriers
     const T *x = (const T *)p.x + row * p.x_stride;
     const R *res = p.residual ? (const R *)p.residual + row * p.width : nullptr;
-    float s[NV][8], ss = 0.f;
+    float s[NV][8];
+    double ss = 0.;
 #pragma unroll
     for (int v = 0; v < NV; ++v) load_piece<T, TPR, VEC>(x, v, tr, p.width, s[v]);
     if (res) {
@@ -118,14 +127,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(s[v][e], s[v][e], ss);
+        for (int e = 0; e < 8; ++e) ss = fma((double)s[v][e], (double)s[v][e], ss);
     if (p.residual_out) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             store_piece<R, TPR, VEC>((R *)p.residual_out + row * p.width, v, tr, p.width, s[v]);
     }
-    ss = row_reduce<TPR, false>(ss, sh, 0);
-    const float rstd = 1.f / sqrtf(fmaf(ss, p.inv_width, p.eps));
+    const float mean = (float)(row_reduce<TPR, false>(ss, sums, 0) * p.inv_width64);
+    const float rstd = 1.f / sqrtf(mean + p.eps);
     if (p.rstd && tr == 0) p.rstd[row] = rstd;
     float amax = 0.f;
 #pragma unroll
@@ -143,12 +152,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
         for (int v = 0; v < NV; ++v) store_piece<T, TPR, VEC>((T *)p.y + row * p.width, v, tr, p.width, s[v]);
         return;
     }
-    amax = row_reduce<TPR, true>(amax, sh, 1);
+    amax = row_reduce<TPR, true>(amax, sh, 0);
     const float top = p.kind == SELSCAN_LM_OUT_INT8 ? 127.f : 448.f;
-    // fmaxf drops a NaN: a row that holds one (or whose sum of squares overflows) is marked by its scale
-    const bool bad = !(ss < INFINITY), zero = bad || amax < 1e-32f;
-    const float inv = zero ? 0.f : top / amax;
-    if (tr == 0) p.scale[row] = bad ? NAN : zero ? 0.f : amax / top;
+    // fmaxf drops a NaN: a row that holds one (or whose mean square overflows) is marked by its scale
+    const bool bad = !(mean < INFINITY), zero = bad || amax < 1e-32f;
+    const float inv = zero ? 0.f : top * (1.f / amax);
+    if (tr == 0) p.scale[row] = bad ? NAN : zero ? 0.f : amax * (1.f / top);
     uint8_t *y = (uint8_t *)p.y + row * p.width;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -337,7 +346,7 @@ int add_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, cons
     NormParams p{};
     p.x = x, p.residual = residual, p.weight = weight, p.y = y, p.residual_out = residual_out;
     p.scale = scale, p.rstd = rstd, p.rows = rows, p.x_stride = x_stride;
-    p.width = (int)width, p.kind = out_kind, p.eps = eps, p.inv_width = 1.f / (float)width;
+    p.width = (int)width, p.kind = out_kind, p.eps = eps, p.inv_width64 = 1. / (double)width;
     const bool vec = width % 8 == 0 && x_stride * s % 16 == 0 && span_aligned(x, 16) && span_aligned(residual, 16) &&
                      span_aligned(residual_out, 16) && span_aligned(y, q8 ? 8 : 16) && span_aligned(weight, 16);
     return launch_types<false>(p, io_dtype, residual_dtype, vec, stream);

@@ -1,7 +1,7 @@
 """GPU tests of add_rms_norm_fwd and add_rms_norm_bwd against the same formulas in 64 bits.
 
-Bars, from the arithmetic.  u = 2^-24.  A row's sum of squares adds positive terms in chains of at most 32
-fused steps, then 6 + 16 across lanes and waves: relative error at most 54 u, half of it in rstd; y adds three
+Bars, from the arithmetic.  u = 2^-24.  A row's sum of squares, added in 32 bits in chains of at most 32
+fused steps, then 6 + 16 across lanes and waves, would be off by at most 54 u, half of it in rstd (it is added in 64 bits); y adds three
 roundings, so |y - exact| <= 32 u |y| (2e-6) in fp32, plus half an ulp (2^-8 |y|, bf16 having 8 significant bits) where it is rounded to bf16.
 8-bit outputs add half a step of their grid.  ds = rstd (g - xhat mean(g xhat)): the mean carries 54 u of
 mean|g xhat|, every other factor a few u.  dweight adds rows_per + 64 terms in order: that many u of the sum of
@@ -236,3 +236,22 @@ def test_empty_in_place_stream_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cap, eager))
+
+
+@pytest.mark.parametrize("width", [5, 520, 1536, 5000, 20000, 32768])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rstd_is_rounded_four_times(width, dtype):
+    """The squares are added in 64 bits, so rstd carries the roundings of mean, + eps, square root and reciprocal
+    alone: (1/2 + 1/2 + 1 + 1) u, u^2 terms aside, at every width.  And the grid of an 8-bit output is its row's largest
+    magnitude over 127 or 448: that element is the grid's last."""
+    torch = _torch()
+    import selective_state_space_51_amd as S
+    _say("rstd", width, dtype)
+    i = make(130, width, dtype, "f32", seed=11)
+    s = (i["x"].float() + i["r"]).double()
+    want = 1 / torch.sqrt((s * s).mean(1) + 1e-5)
+    for out, top in (("int8", 127), ("fp8", 448)):
+        y, _, scale, rstd = S.add_rms_norm_fwd(i["x"], i["w"], residual=i["r"], out=out, rstd=True)
+        torch.cuda.synchronize()
+        assert float(((rstd.double() - want) / want).abs().max()) <= 3.01 * U
+        assert (y.float().abs().amax(1) == top).all()
