@@ -30,10 +30,23 @@ struct Frag {
 };
 __device__ __forceinline__ bf16x8 frag(const Frag &f) { return __builtin_bit_cast(bf16x8, f); }
 
+// 16.0 twice, in a vector register: and-or is one instruction if only one of its operands is scalar
+__device__ __forceinline__ uint32_t two_16s() {
+    uint32_t v = 0x41804180u;
+    asm("" : "+v"(v));
+    return v;
+}
 // 8 nibbles as 16 + q, in the order 0 4 1 5 2 6 3 7
-__device__ __forceinline__ Frag dequant(uint32_t d) {
-    constexpr uint32_t mask = 0x00780078u, one = 0x41804180u;  // 16.0 twice
-    return {{((d << 3) & mask) | one, ((d >> 1) & mask) | one, ((d >> 5) & mask) | one, ((d >> 9) & mask) | one}};
+__device__ __forceinline__ Frag dequant(uint32_t d, uint32_t base) {
+    constexpr uint32_t mask = 0x00780078u;
+    return {{((d << 3) & mask) | base, ((d >> 1) & mask) | base, ((d >> 5) & mask) | base, ((d >> 9) & mask) | base}};
+}
+
+// The operand of -(16 + zero), exact in bf16, eight times, for each zero point: a 16-byte read in place of forming it.
+__device__ __forceinline__ void fill_zero_table(uint4 *zt, int lane) {
+    if (lane >= 16) return;
+    const uint32_t z = 0xC180u | (uint32_t)lane << 3, v = z << 16 | z;
+    zt[lane] = make_uint4(v, v, v, v);
 }
 
 // 8 values of x as NS bf16 fragments in that order whose sum is x: x itself for bf16; for fp32 its upper,
@@ -137,17 +150,19 @@ struct MatrixRows {
             zv.v[a] = zb[so + at];
         }
     }
-    // [16 rows][4 units][NG]: scale (bf16) above, zero point below
+    // [4 units][NG][16 rows]: scale (bf16) above, the zero point's byte offset in its table below
     __device__ __forceinline__ void store_scales(uint32_t *sz) const {
 #pragma unroll
-        for (int a = 0; a < NG; ++a) sz[lane * NG + a] = (uint32_t)sv.v[a] << 16 | (zeros ? zv.v[a] & 15 : 8);
+        for (int a = 0; a < NG; ++a)
+            sz[((lane & 3) * NG + a) * 16 + (lane >> 2)] = (uint32_t)sv.v[a] << 16 | (zeros ? zv.v[a] & 15 : 8) << 4;
     }
 };
 
 // acc += the products of one unit: x as fragments from `fx(t, e, j)`, the matrix from w, scales from sz.  The 16 and the
 // zero point leave by a second product, of x with -(16 + zero) for every k of the group.
 template <int GM, int TM, int NS, class F>
-__device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32_t *sz, int q, int i, int g, f32x4 (&acc)[TM]) {
+__device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32_t *sz, const uint4 *zt, uint32_t base, int q, int i,
+                                              int g, f32x4 (&acc)[TM]) {
     constexpr int NG = 4 / GM;
     const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
     f32x4 part[TM];
@@ -156,13 +171,12 @@ __device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (j % GM == 0) {
-            const uint32_t v = sz[(i * 4 + q) * NG + j / GM];
+            const uint32_t v = sz[(q * NG + j / GM) * 16 + i];
             s = __uint_as_float(v & 0xFFFF0000u);
-            // -(16 + zero) as bf16, exact, twice
-            const uint32_t z = 0xC1800000u | (v & 15) << 19;
-            zf.w[0] = zf.w[1] = zf.w[2] = zf.w[3] = z | z >> 16;
+            const uint4 z = *(const uint4 *)((const char *)zt + (v & 0xFFFFu));
+            zf = {{z.x, z.y, z.z, z.w}};
         }
-        const Frag wf = dequant(((const uint32_t *)&w[w_at(i, j)])[g]);
+        const Frag wf = dequant(((const uint32_t *)&w[w_at(i, j)])[g], base);
 #pragma unroll
         for (int t = 0; t < TM; ++t)
 #pragma unroll
@@ -189,9 +203,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void w4_rows(W4Params 
     __shared__ uint4 xl[2][NS][16 * TM * 16];  // bf16 pieces of 8 k, 16 a row
     __shared__ uint4 wl[4][64];
     __shared__ uint32_t szl[4][64 * NG];
+    __shared__ uint4 zt[16];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, g = lane >> 4;
     const int64_t row0 = (int64_t)blockIdx.x * 64 + wave * 16, tok0 = (int64_t)blockIdx.y * (16 * TM);
     MatrixRows<GM> m(p, row0, lane);
+    const uint32_t base = two_16s();
+    fill_zero_table(zt, tid);  // (the first unit's barrier comes before it is read)
     // x: this thread brings piece tid & 15 (8 k) of row tid / 16, and of row 16 + tid / 16 where TM = 2
     const int most = (int)(p.rows - tok0) - 1;
     uint32_t xo[TM];
@@ -235,7 +252,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void w4_rows(W4Params 
             const uint4 v = xl[buf][e][(16 * t + i) * 16 + ((4 * j + g) ^ i)];
             return Frag{{v.x, v.y, v.z, v.w}};
         };
-        unit_products<GM, TM, NS>(fx, wl[wave], szl[wave], q, i, g, acc);
+        unit_products<GM, TM, NS>(fx, wl[wave], szl[wave], zt, base, q, i, g, acc);
     };
     uint4 wa, wc;  // the matrix: units of even and of odd number
     if (whole > 0) {
@@ -287,6 +304,7 @@ struct WaveLds {
     static constexpr int XL = TM * XP / 4;         // loads of 64 pieces
     uint4 x[16 * TM * XP];
     uint4 w[64];
+    uint4 zt[16];
     uint32_t sz[64 * NG];
 };
 
@@ -300,6 +318,8 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
     S &st = ((S *)lds)[wave];
     const int64_t row0 = (int64_t)blockIdx.x * 16, tok0 = (int64_t)blockIdx.y * (16 * TM);
     MatrixRows<GM> m(p, row0, lane);
+    const uint32_t base = two_16s();
+    fill_zero_table(st.zt, lane);
     const int most = (int)(p.rows - tok0) - 1;
     uint32_t xo[XL];
 #pragma unroll
@@ -342,7 +362,7 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
                 }
                 sx[t][j] = split_x<T>(r);
             }
-        unit_products<GM, TM, NS>([&](int t, int e, int j) { return sx[t][j].f[e]; }, st.w, st.sz, q, i, g, acc);
+        unit_products<GM, TM, NS>([&](int t, int e, int j) { return sx[t][j].f[e]; }, st.w, st.sz, st.zt, base, q, i, g, acc);
     };
     const int whole = p.k >> 7;
     const int u0 = wave * p.upw, u1 = u0 + p.upw < whole ? u0 + p.upw : whole;
@@ -411,7 +431,7 @@ int launch_w4(const W4Params &p, void *stream) {
     const int64_t tiles = (p.n + 15) / 16, blocks_y = (p.rows + 16 * TM - 1) / (16 * TM);
     // shared x where that leaves two workgroups per compute unit (measured at 1 and 32 rows, k 2,048 / n 16,384: 13.1 and
     // 18.0 us with it, 8.2 and 13.3 without; n 50,280: 18.8 and 27, without 20.3 and 35)
-        if (tiles >= 4 * 2 * 256)
+    if (tiles >= 4 * 2 * 256)
         return enqueue(w4_rows<T, GM, TM>, dim3((unsigned)((tiles + 3) / 4), (unsigned)blocks_y), dim3(256), p, stream);
     // waves over k: four, or eight where there are few workgroups (n 8,192, k 2,048, one row: 5.6 us with four, 6.3 with
     // eight; n 16,384: 8.2 and 10.8); at most one per unit
