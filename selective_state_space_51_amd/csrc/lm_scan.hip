@@ -262,13 +262,13 @@ __global__ __launch_bounds__(64) void conv_step(ConvParams p) {
         if (r >= p.q.tokens) break;
         const int64_t slot = slot_of(p.q, r);
         Raw8<T> win[K];
+        win[K - 1] = load_raw8((const T *)p.x + r * p.x_stride + c0, nv, vec);
         T *st = K > 1 ? (T *)p.state + (slot < 0 ? 0 : slot) * (K - 1) * p.dim + c0 : nullptr;
 #pragma unroll
         for (int t = 0; t < K - 1; ++t) {
             win[t] = Raw8<T>{};
             if (slot >= 0) win[t] = load_raw8(st + t * p.dim, nv, vec);
         }
-        win[K - 1] = load_raw8((const T *)p.x + r * p.x_stride + c0, nv, vec);
         float v[8];
         conv_row<T, K>(f, b, win, p.silu, v);
         store8((T *)p.out + r * p.dim + c0, nv, vec, v);
@@ -583,10 +583,10 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
 
 // Joins the segments of long sequences between the launches: one thread per (sequence, channel, state) walks the
 // maps in order and leaves the state at the end of each segment in its place.
-__global__ __launch_bounds__(256) void scan_join(ScanParams p) {
+__global__ __launch_bounds__(64) void scan_join(ScanParams p) {
     const int s = blockIdx.x;
     const Range rg = range_of(p.q, s);
-    const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x, ch = i / kN, st = p.dim * kN;
+    const int64_t i = (int64_t)blockIdx.y * 64 + threadIdx.x, ch = i / kN, st = p.dim * kN;
     if (ch >= p.dim) return;
     const float a2 = p.A[i] * kLog2e;
     const int first = (int)fdiv((uint32_t)rg.t0, p.dsize) + s;
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(256) void scan_join(ScanParams p) {
     float *e = p.seg + (int64_t)first * st + i;
     const float *d = p.sdt + (int64_t)first * p.dim + ch;
     float h = e[0];
-    constexpr int U = 8;  // segments loaded ahead
+    constexpr int U = 16;  // segments loaded ahead
     for (int j0 = 1; j0 < n; j0 += U) {
         float ev[U], dv[U];
 #pragma unroll
@@ -764,7 +764,7 @@ int launch_scan(const ScanParams &p, int64_t blocks, void *stream) {
     const dim3 grid((unsigned)blocks);
     int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, grid, dim3(256), p, stream);
     if (rc == SELSCAN_OK && p.joined)
-        rc = enqueue(scan_join, dim3((unsigned)p.q.nseq, (unsigned)((p.dim * kN + 255) / 256)), dim3(256), p, stream);
+        rc = enqueue(scan_join, dim3((unsigned)p.q.nseq, (unsigned)((p.dim * kN + 63) / 64)), dim3(64), p, stream);
     if (rc == SELSCAN_OK && p.seg) rc = enqueue(scan_packed<T, ZOH, GATE, 1>, grid, dim3(256), p, stream);
     return rc;
 }

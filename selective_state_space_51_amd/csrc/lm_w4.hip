@@ -430,7 +430,7 @@ template <typename T, int GM, int TM>
 int launch_w4(const W4Params &p, void *stream) {
     const int64_t tiles = (p.n + 15) / 16, blocks_y = (p.rows + 16 * TM - 1) / (16 * TM);
     // shared x where that leaves two workgroups per compute unit (measured at 1 and 32 rows, k 2,048 / n 16,384: 13.1 and
-    // 18.0 us with it, 8.2 and 13.3 without; n 50,280: 18.8 and 27, without 20.3 and 35)
+    // 18.0 us with it, 8.2 and 13.3 without; n 50,280: 18.0 and 25, without 20.3 and 35)
     if (tiles >= 4 * 2 * 256)
         return enqueue(w4_rows<T, GM, TM>, dim3((unsigned)((tiles + 3) / 4), (unsigned)blocks_y), dim3(256), p, stream);
     // waves over k: four, or eight where there are few workgroups (n 8,192, k 2,048, one row: 5.6 us with four, 6.3 with
