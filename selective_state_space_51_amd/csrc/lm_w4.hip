@@ -7,7 +7,9 @@
 // weights.  The 16 leaves together with the zero point, by a second product with the constant -(16 + zero).
 // (128 + q would save nothing and cost 8 times the cancellation.)
 //
-// Each weight is read once per 32 rows of x.
+// Each weight is read once per 32 rows of x.  One row (n 50,280, k 2,048, groups of 64): 18 us, of which 14 are the matrix at
+// the rate that reads alone reach (4.05 TB/s).  24 rows: 25 us; two tiles of x double the matrix products and the reads of x
+// from LDS, and each compute unit's fourth workgroup (3.07 on average) adds 5 us to its first three.
 #include "lm_common.h"
 
 namespace {
