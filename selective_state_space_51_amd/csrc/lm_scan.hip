@@ -586,40 +586,51 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
 // Joins the segments of long sequences between the launches: one thread per (sequence, channel, state) walks the
 // maps in order and leaves the state at the end of each segment in its place.
 __global__ __launch_bounds__(64) void scan_join(ScanParams p) {
-    const int s = blockIdx.x;
-    const Range rg = range_of(p.q, s);
-    const int64_t i = (int64_t)blockIdx.y * 64 + threadIdx.x, ch = i / kN, st = p.dim * kN;
+    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x, ch = i / kN, st = p.dim * kN;
     if (ch >= p.dim) return;
     const float a2 = p.A[i] * kLog2e;
-    const int first = (int)fdiv((uint32_t)rg.t0, p.dsize) + s;
-    const int n = (int)fdiv((uint32_t)(rg.len + p.size - 1), p.dsize) - 1;  // all but the last
-    if (n < 2) return;
-    float *e = p.seg + (int64_t)first * st + i;
-    const float *d = p.sdt + (int64_t)first * p.dim + ch;
-    float h = e[0];
-    constexpr int U = 16;  // segments loaded ahead
-    for (int j0 = 1; j0 < n; j0 += U) {
-        float ev[U], dv[U];
+    for (int s = blockIdx.y; s < p.q.nseq; s += gridDim.y) {
+        const Range rg = range_of(p.q, s);
+        const int first = (int)fdiv((uint32_t)rg.t0, p.dsize) + s;
+        const int n = (int)fdiv((uint32_t)(rg.len + p.size - 1), p.dsize) - 1;  // all but the last
+        if (n < 2) continue;
+        float *e = p.seg + (int64_t)first * st + i;
+        const float *d = p.sdt + (int64_t)first * p.dim + ch;
+        float h = e[0];
+        constexpr int U = 16;  // segments loaded ahead
+        for (int j0 = 1; j0 < n; j0 += U) {
+            float ev[U], dv[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t j = j0 + u < n ? j0 + u : n - 1;
-            ev[u] = e[j * st];
-            dv[u] = d[j * p.dim];
-        }
+            for (int u = 0; u < U; ++u) {
+                const int64_t j = j0 + u < n ? j0 + u : n - 1;
+                ev[u] = e[j * st];
+                dv[u] = d[j * p.dim];
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (j0 + u >= n) break;
-            h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
-            e[(j0 + u) * st] = h;
+            for (int u = 0; u < U; ++u) {
+                if (j0 + u >= n) break;
+                h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
+                e[(j0 + u) * st] = h;
+            }
         }
     }
 }
+
+// 4 values from any address aligned to one
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Four {
+    T v[4];
+};
 
 // One token per sequence.  Four lanes per channel hold four states each, so that a wave moves 16 channels' states as
 // 1 KB of adjacent memory in and out; y is summed over the four lanes.  HBM bound by the states (128
 // bytes per row and channel of fp32 state in and out) where there are many rows: 256 rows x 4,096 channels bf16 26 us, 5.5
 // TB/s; one row x 1,536 3.4 us.  A, D and bias are held
 // over the rows_per rows that a thread takes.
+//
+// The next row's loads are in flight during a row's arithmetic, none of them under a condition (that would make the wait
+// for one a wait for all): a row without an entry of the cache reads A in its place, which has an entry's layout, and
+// takes zero.
 template <typename T, bool ZOH>
 __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, ch = i >> 2;
@@ -628,36 +639,54 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
     const float4 a = load_f4(p.A + ch * kN + n0);
     const float a2[4] = {a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e};
     const float Dd = p.D ? p.D[ch] : 0.f, bias = p.bias ? p.bias[ch] : 0.f;
-    const int r0 = blockIdx.y * p.rows_per;
-    for (int k = 0; k < p.rows_per; ++k) {
-        const int r = r0 + k;
-        if (r >= p.q.tokens) break;
-        const int64_t slot = slot_of(p.q, r);
-        float *hp = p.h + ((slot < 0 ? 0 : slot) * p.dim + ch) * kN + n0;
-        float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (slot >= 0) hv = *(const float4 *)hp;
-        float h[4] = {hv.x, hv.y, hv.z, hv.w};
-        const T *B = (const T *)p.B + r * p.bc_stride + n0, *C = (const T *)p.C + r * p.bc_stride + n0;
-        float d = Io<T>::f32(((const T *)p.delta)[r * p.dim + ch]) + bias;
+    struct Row {
+        int64_t slot;
+        float4 h;
+        Four<T> B, C;
+        T d, x, z;
+    };
+    auto fetch = [&](int r) {
+        Row w;
+        w.slot = slot_of(p.q, r);
+        w.h = load_f4((w.slot >= 0 ? p.h + w.slot * p.dim * kN : p.A) + ch * kN + n0);
+        w.B = *(const Four<T> *)((const T *)p.B + r * p.bc_stride + n0);
+        w.C = *(const Four<T> *)((const T *)p.C + r * p.bc_stride + n0);
+        w.d = ((const T *)p.delta)[r * p.dim + ch];
+        w.x = ((const T *)p.x)[r * p.dim + ch];
+        w.z = (p.z ? (const T *)p.z + r * p.z_stride : (const T *)p.x + r * p.dim)[ch];
+        return w;
+    };
+    auto step = [&](int r, const Row &w) {
+        float h[4] = {w.h.x, w.h.y, w.h.z, w.h.w};
+        float d = Io<T>::f32(w.d) + bias;
         if (p.softplus) d = softplus(d);
-        const float xv = Io<T>::f32(((const T *)p.x)[r * p.dim + ch]), dx = d * xv;
+        const float xv = Io<T>::f32(w.x), dx = d * xv;
         float acc = 0.f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float arg = d * a2[n], e = __builtin_amdgcn_exp2f(arg);
             float g = dx;
             if constexpr (ZOH) g = dx * zoh_phi(e, arg);
-            h[n] = fmaf(e, h[n], g * Io<T>::f32(B[n]));
-            acc = fmaf(Io<T>::f32(C[n]), h[n], acc);
+            h[n] = fmaf(e, w.slot >= 0 ? h[n] : 0.f, g * Io<T>::f32(w.B.v[n]));
+            acc = fmaf(Io<T>::f32(w.C.v[n]), h[n], acc);
         }
-        if (slot >= 0) *(float4 *)hp = make_float4(h[0], h[1], h[2], h[3]);
-        acc += __shfl_xor(acc, 1);
-        acc += __shfl_xor(acc, 2);
+        if (w.slot >= 0) *(float4 *)(p.h + (w.slot * p.dim + ch) * kN + n0) = make_float4(h[0], h[1], h[2], h[3]);
+        acc += quad<kQuadXor1>(acc);
+        acc += quad<kQuadXor2>(acc);
         if (n0 == 0) {
             float v = fmaf(Dd, xv, acc);
-            if (p.z) v *= silu(Io<T>::f32(((const T *)p.z)[r * p.z_stride + ch]));
+            if (p.z) v *= silu(Io<T>::f32(w.z));
             ((T *)p.y)[r * p.dim + ch] = Io<T>::to(v);
         }
+    };
+    const int r0 = blockIdx.y * p.rows_per, r1 = p.rows_per < p.q.tokens - r0 ? r0 + p.rows_per : p.q.tokens;
+    Row w = fetch(r0), next;
+    for (int r = r0; r < r1; r += 2) {
+        next = fetch(r + 1 < r1 ? r + 1 : r);
+        step(r, w);
+        if (r + 1 >= r1) break;
+        w = fetch(r + 2 < r1 ? r + 2 : r + 1);
+        step(r + 1, next);
     }
 }
 
@@ -767,7 +796,7 @@ int launch_scan(const ScanParams &p, int64_t blocks, void *stream) {
     const dim3 grid((unsigned)blocks);
     int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, grid, dim3(256), p, stream);
     if (rc == SELSCAN_OK && p.joined)
-        rc = enqueue(scan_join, dim3((unsigned)p.q.nseq, (unsigned)((p.dim * kN + 63) / 64)), dim3(64), p, stream);
+        rc = enqueue(scan_join, dim3((unsigned)((p.dim * kN + 63) / 64), (unsigned)(p.q.nseq < 65535 ? p.q.nseq : 65535)), dim3(64), p, stream);
     if (rc == SELSCAN_OK && p.seg) rc = enqueue(scan_packed<T, ZOH, GATE, 1>, grid, dim3(256), p, stream);
     return rc;
 }
@@ -876,8 +905,7 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
         p.sdt = p.seg + pieces * dim * kN;
         p.joined = max_seqlen / p.size > kWalk ? 1 : 0;
     }
-    // (the join's grid: 16 channels per workgroup)
-    if (pieces * p.ntiles > INT32_MAX || (dim * kN + 255) / 256 > kGridY) return SELSCAN_E_UNSUPPORTED;
+    if (pieces * p.ntiles > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     const bool zoh = (flags & SELSCAN_FLAG_ZOH) != 0;
     return io_dtype == SELSCAN_BF16 ? launch_scan_io<uint16_t>(p, pieces * p.ntiles, zoh, stream)
                                     : launch_scan_io<float>(p, pieces * p.ntiles, zoh, stream);
