@@ -75,6 +75,19 @@ __device__ __forceinline__ Raw8<T> load_any8(const T *p) {
     for (int i = 0; i < (int)sizeof(T) * 2; ++i) r.w[i] = u.w[i];
     return r;
 }
+// the same without a place in the caches (NT), for what no one reads again before the caches have seen that much else
+template <bool NT, typename T>
+__device__ __forceinline__ Raw8<T> load_stream8(const T *p) {
+    if constexpr (!NT) return load_any8(p);
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const V v = __builtin_nontemporal_load((const V *)p + i);
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+    return r;
+}
 template <typename T>
 __device__ __forceinline__ void store_any8(T *p, const float (&v)[8]) {
     struct __attribute__((packed, aligned(sizeof(T)))) U {

@@ -35,9 +35,9 @@ struct LpParams {
 };
 
 // elements [at, at + 8) of a row of n; those past its end are -inf
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ Raw8<T> load_logits(const T *row, int at, int n) {
-    if (at + 8 <= n) return load_any8(row + at);
+    if (at + 8 <= n) return load_stream8<NT>(row + at);
     Raw8<T> r;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -136,7 +136,7 @@ struct RowEnd {
 // largest logit, so every logit of the slice that can be among the best is at or above the largest of the
 // waves' bounds.  Those few (some hundred for top = 32) are found by the maxima of pieces of 8, gathered in LDS
 // and ranked by counting.  If equal values make them too many, the best are taken out one after another.
-template <typename T, int PIECES, bool WHOLE>
+template <typename T, int PIECES, bool WHOLE, bool NT>
 __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     constexpr int NW = kThreads / 64;
     __shared__ float red[NW], red2[NW][2], bound[NW];
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     const T *x = (const T *)p.x + row * p.stride;
     Raw8<T> r[PIECES];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) r[i] = load_logits(x, base + (i * kThreads + tid) * 8, p.vocab);
+    for (int i = 0; i < PIECES; ++i) r[i] = load_logits<NT>(x, base + (i * kThreads + tid) * 8, p.vocab);
     if (tid == 0) ncand = 0;
     float pm[PIECES], mine = -INFINITY;
 #pragma unroll
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
 #pragma unroll 1
         for (int i = 0; i < PIECES; ++i) {
             // (from memory again: this rare loop then costs the kernel no registers)
-            const Raw8<T> q8 = load_logits(x, base + (i * kThreads + tid) * 8, p.vocab);
+            const Raw8<T> q8 = load_logits<NT>(x, base + (i * kThreads + tid) * 8, p.vocab);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float v = raw_f32(q8, e);
@@ -359,7 +359,7 @@ constexpr int kBwdPieces = 4;
 
 // gradient: reads a logit, writes its gradient; HBM bound (1,000 x 32,001 fp32: 40 us, 6.4 TB/s, the logits partly from the
 // last-level cache that the forward left them in)
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;
     const int base = sl * (kBwdPieces * kThreads * 8);
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     const float k0 = -fmaf(gh, p.in_entropy[row], gl), k1 = -gh * kLn2;
     Raw8<T> r[kBwdPieces];
 #pragma unroll
-    for (int i = 0; i < kBwdPieces; ++i) r[i] = load_logits(x, base + (i * kThreads + (int)threadIdx.x) * 8, p.vocab);
+    for (int i = 0; i < kBwdPieces; ++i) r[i] = load_logits<NT>(x, base + (i * kThreads + (int)threadIdx.x) * 8, p.vocab);
 #pragma unroll
     for (int i = 0; i < kBwdPieces; ++i) {
         const int at = base + (i * kThreads + (int)threadIdx.x) * 8;
@@ -414,6 +414,13 @@ int64_t slices_for(int64_t rows, int64_t vocab) {
     const int64_t n = (int64_t)pieces_for(rows, vocab) * kThreads * 8;
     return (vocab + n - 1) / n;
 }
+
+// Logits of this many bytes are read without a place in the caches: forward, those that a gradient right after it would find
+// there are no more than what they push out (forward and gradient, us, with a place and without: 600 x 50,280 bf16, 60 MB, 37
+// and 38; 1,000, 101 MB, 57 and 59; 1,400, 141 MB, 88 and 76; 4,096 x 32,001, 262 MB, 168 and 160; 1,400 x 32,001 fp32, 179 MB,
+// 111 and 105); gradient, what the forward left is gone by then (2,048 x 50,280, 206 MB, 113 and 102; 4,096 x 32,001 160 and
+// 142; 1,400 x 32,001 fp32 no difference; 128 MB 72 and 78).
+constexpr int64_t kForwardPast = INT64_C(112) << 20, kBackwardPast = INT64_C(160) << 20;
 
 int lp_check(const void *logits, int64_t stride, const int64_t *targets, float scale, int64_t rows, int64_t vocab, int dtype) {
     if (rows < 0 || vocab < 0) return SELSCAN_E_SHAPE;
@@ -463,11 +470,13 @@ int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t 
     p.top_logprob = top_logprob, p.top_index = top_index;
     p.rows = rows, p.stride = logits_stride, p.vocab = (int)vocab, p.top = top;
     p.scale = scale, p.c = scale * kLog2e;
-    const bool bf = io_dtype == SELSCAN_BF16;
+    const bool bf = io_dtype == SELSCAN_BF16, nt = rows * vocab * (int64_t)io_bytes(io_dtype) >= kForwardPast;
+#define PICK(PIECES, WHOLE)                                                                                       \
+    (bf ? nt ? logprobs_slice<uint16_t, PIECES, WHOLE, true> : logprobs_slice<uint16_t, PIECES, WHOLE, false>     \
+        : nt ? logprobs_slice<float, PIECES, WHOLE, true> : logprobs_slice<float, PIECES, WHOLE, false>)
     if (whole_row(vocab)) {
         if (rows > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
-        return enqueue(bf ? logprobs_slice<uint16_t, 4, true> : logprobs_slice<float, 4, true>, dim3((unsigned)rows), dim3(kThreads), p,
-                       stream);
+        return enqueue(PICK(4, true), dim3((unsigned)rows), dim3(kThreads), p, stream);
     }
     const int pieces = pieces_for(rows, vocab);
     p.nsl = (int)slices_for(rows, vocab);
@@ -475,9 +484,10 @@ int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t 
     if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     p.part = (float4 *)workspace;
     p.cand = (unsigned long long *)(p.part + blocks);
-    void (*k)(LpParams) = pieces == 4 ? (bf ? logprobs_slice<uint16_t, 4, false> : logprobs_slice<float, 4, false>)
-                                      : (bf ? logprobs_slice<uint16_t, 2, false> : logprobs_slice<float, 2, false>);
-    rc = enqueue(k, dim3((unsigned)blocks), dim3(kThreads), p, stream);
+    // (slices of 2 pieces are of a few rows)
+    rc = enqueue(pieces == 4 ? PICK(4, false) : bf ? logprobs_slice<uint16_t, 2, false, false> : logprobs_slice<float, 2, false, false>,
+                 dim3((unsigned)blocks), dim3(kThreads), p, stream);
+#undef PICK
     if (rc != SELSCAN_OK) return rc;
     return enqueue(bf ? logprobs_join<uint16_t> : logprobs_join<float>, dim3((unsigned)rows),
                    dim3(top && p.nsl * top > 64 ? kThreads : 64), p, stream);
@@ -510,8 +520,10 @@ int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t 
     p.nsl = (int)((vocab + per - 1) / per);
     const int64_t blocks = rows * p.nsl;
     if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
-    return enqueue(io_dtype == SELSCAN_BF16 ? logprobs_bwd<uint16_t> : logprobs_bwd<float>, dim3((unsigned)blocks), dim3(kThreads),
-                   p, stream);
+    const bool nt = rows * vocab * (int64_t)s >= kBackwardPast;
+    return enqueue(io_dtype == SELSCAN_BF16 ? nt ? logprobs_bwd<uint16_t, true> : logprobs_bwd<uint16_t, false>
+                                            : nt ? logprobs_bwd<float, true> : logprobs_bwd<float, false>,
+                   dim3((unsigned)blocks), dim3(kThreads), p, stream);
 }
 
 }  // extern "C"

@@ -34,11 +34,11 @@ __device__ __forceinline__ int col_of(int v, int e, int tr) {
     return VEC ? (v * TPR + tr) * 8 + e : (v * 8 + e) * TPR + tr;
 }
 
-template <typename T, int TPR, bool VEC>
+template <typename T, int TPR, bool VEC, bool NT = false>
 __device__ __forceinline__ void load_piece(const T *row, int v, int tr, int width, float (&out)[8]) {
     if constexpr (VEC) {
         const int c = col_of<TPR, VEC>(v, 0, tr);
-        const Raw8<T> r = c < width ? load_raw8(row + c, 8, true) : Raw8<T>{};
+        const Raw8<T> r = c < width ? NT ? load_stream8<NT>(row + c) : load_raw8(row + c, 8, true) : Raw8<T>{};
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[e] = raw_f32(r, e);
     } else {
@@ -185,7 +185,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
 
 // Gradients: a slot (the threads of a row) walks rows_per consecutive rows with the weight and its sums of
 // dweight in registers, and leaves the sums in its row of `partial`; norm_dw adds those in order.
-template <typename T, typename R, int TPR, int NV, bool VEC>
+//
+// NT: dy, s and dresidual_out are read without a place in the caches.
+template <typename T, typename R, int TPR, int NV, bool VEC, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd(NormParams p) {
     constexpr int BLOCK = TPR < 256 ? 256 : TPR;
     __shared__ float sh[2 * (BLOCK / 64)];
@@ -207,8 +209,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd(NormParams p) 
         const float rstd = p.rstd[row];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            load_piece<T, TPR, VEC>((const T *)p.x + at, v, tr, p.width, g[v]);
-            load_piece<R, TPR, VEC>((const R *)p.residual + at, v, tr, p.width, xh[v]);
+            load_piece<T, TPR, VEC, NT>((const T *)p.x + at, v, tr, p.width, g[v]);
+            load_piece<R, TPR, VEC, NT>((const R *)p.residual + at, v, tr, p.width, xh[v]);
         }
         if (p.add) {
 #pragma unroll
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd(NormParams p) 
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (p.dres) load_piece<R, TPR, VEC>((const R *)p.dres + at, v, tr, p.width, d);
+            if (p.dres) load_piece<R, TPR, VEC, NT>((const R *)p.dres + at, v, tr, p.width, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = fmaf(rstd, fmaf(-xh[v][e], dot, g[v][e]), d[e]);
             if (p.y) store_piece<T, TPR, VEC>((T *)p.y + at, v, tr, p.width, d);
@@ -288,6 +290,12 @@ int64_t bwd_slots(int64_t rows, int64_t width) {
     return rows < most ? rows : most;
 }
 
+// Gradients of a 16-bit residual stream read dy, the residual and its gradient without a place in the caches once they and x
+// pass this many bytes (forward and gradients, us, with a place and without: 4,096 x 2,048, 67 MB, 32 and 34; 6,000, 98 MB, 46.5
+// and 46; 8,192, 134 MB, 58 and 56.5; 12,000 88 and 80; 16,384 120 and 109; 20,000 x 1,024 82 and 75).  With an fp32 stream it
+// is 1 or 2 % either way, and none does it.
+constexpr int64_t kReadsPast = INT64_C(112) << 20;
+
 template <typename T, typename R, bool BWD, bool VEC>
 int launch_norm(const NormParams &p, void *stream) {
     const Shape s = shape_of(p.width);
@@ -296,10 +304,15 @@ int launch_norm(const NormParams &p, void *stream) {
     const int64_t blocks = (units + per - 1) / per;
     if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), bl(block);
+    const bool past = BWD && p.rows * p.width * 8 >= kReadsPast;
 #define GO(TPR, NV)                                                                        \
     if (s.tpr == TPR && s.nv == NV) {                                                      \
-        if constexpr (BWD) return enqueue(norm_bwd<T, R, TPR, NV, VEC>, grid, bl, p, stream); \
-        else return enqueue(norm_fwd<T, R, TPR, NV, VEC>, grid, bl, p, stream);            \
+        if constexpr (BWD) {                                                               \
+            if constexpr (VEC && sizeof(R) == 2) {                                         \
+                if (past) return enqueue(norm_bwd<T, R, TPR, NV, true, true>, grid, bl, p, stream); \
+            }                                                                              \
+            return enqueue(norm_bwd<T, R, TPR, NV, VEC, false>, grid, bl, p, stream);      \
+        } else return enqueue(norm_fwd<T, R, TPR, NV, VEC>, grid, bl, p, stream);            \
     }
     GO(64, 1) GO(64, 2) GO(256, 1) GO(256, 2) GO(256, 4) GO(1024, 2) GO(1024, 4)
 #undef GO
