@@ -357,8 +357,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
 
 constexpr int kBwdPieces = 4;
 
-// gradient: reads a logit, writes its gradient; HBM bound (1,000 x 32,001 fp32: 40 us, 6.4 TB/s, the logits partly from the
-// last-level cache that the forward left them in)
+// gradient: reads a logit, writes its gradient; HBM bound (1,000 x 32,001 fp32: 43 us, 5.9 TB/s, the logits partly from the
+// last-level cache)
 template <typename T, bool NT>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     const int row = blockIdx.x / p.nsl, sl = blockIdx.x - row * p.nsl;

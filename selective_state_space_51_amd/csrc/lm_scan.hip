@@ -368,8 +368,8 @@ constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;
 //    in order: no barrier.
 //  - The next block's x, delta, z, B and C are in flight during a block's arithmetic.
 //
-// Bound by instruction issue (about 31 VALU instructions and 2 LDS reads per token of a wave; 27,591 tokens in 24 sequences x
-// 4,096 channels bf16: 585 to 625 us, where 150 clocks a token on every SIMD alike would be 450).  A lane per
+// Bound by instruction issue (38 VALU instructions and 2 LDS accesses per token of a wave, with gate and softplus; 27,591 tokens
+// in 24 sequences x 4,096 channels bf16: 585 to 625 us, 84 % of it VALU issue).  A lane per
 // channel with all 16 states and B and C as scalar operands needs a tenth less issue per element, but a
 // quarter of the waves, each token taking four times as long: measured slower wherever the chip was not full
 // of long sequences of equal length.
@@ -625,8 +625,8 @@ struct __attribute__((packed, aligned(sizeof(T)))) Four {
 
 // One token per sequence.  Four lanes per channel hold four states each, so that a wave moves 16 channels' states as
 // 1 KB of adjacent memory in and out; y is summed over the four lanes.  HBM bound by the states (128
-// bytes per row and channel of fp32 state in and out) where there are many rows: 256 rows x 4,096 channels bf16 26 us, 5.5
-// TB/s; one row x 1,536 3.4 us.  A, D and bias are held
+// bytes per row and channel of fp32 state in and out) where there are many rows: 256 rows x 4,096 channels bf16 29.6 us, 4.8
+// TB/s, from states that are in no cache; one row x 1,536 3.3 us.  A, D and bias are held
 // over the rows_per rows that a thread takes.
 //
 // The next row's loads are in flight during a row's arithmetic, none of them under a condition (that would make the wait
