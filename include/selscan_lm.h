@@ -70,6 +70,7 @@ int causal_conv1d_packed_fwd(const void *x, int64_t x_stride, const float *weigh
  *   B, C           : [tokens][dstate] io_dtype, both with row stride bc_stride
  *   A [dim][dstate], D, delta_bias [dim], flags : as for selscan_fwd (dstate must be 16)
  *   h_state        : [nslots][dim][dstate] fp32, 16-byte aligned, nullable (no cache); in place
+ *   dim, bc_stride, z_stride : at most 2^26 (SELSCAN_E_UNSUPPORTED)
  *   max_seqlen     : the longest sequence's length, or any bound on it (tokens if unknown).  It
  *                    only chooses how the work is split and never changes what is computed.
  *   workspace      : selscan_packed_workspace_bytes(...) bytes, 16-byte aligned (0 where the

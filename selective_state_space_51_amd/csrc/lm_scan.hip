@@ -371,8 +371,8 @@ constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;
 //    in order: no barrier.
 //  - The next block's x, delta, z, B and C are in flight during a block's arithmetic.
 //
-// Bound by instruction issue (38 VALU instructions and 2 LDS accesses per token of a wave, with gate and softplus; 27,591 tokens
-// in 24 sequences x 4,096 channels bf16: 585 to 625 us, 84 % of it VALU issue).  A lane per
+// Bound by instruction issue (33 VALU instructions and 2 LDS accesses per token of a wave, with gate and softplus; 27,591 tokens
+// in 24 sequences x 4,096 channels bf16: 545 to 560 us, four fifths of it VALU issue).  A lane per
 // channel with all 16 states and B and C as scalar operands needs a tenth less issue per element, but a
 // quarter of the waves, each token taking four times as long: measured slower wherever the chip was not full
 // of long sequences of equal length.
@@ -401,32 +401,39 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
     const int64_t ch = live ? c0 + cl : dim - 1;  // lanes past the last channel repeat it
     const int len = w.len;
     const float Dd = FULL && p.D ? p.D[ch] : 0.f, bias = p.bias ? p.bias[ch] : 0.f;
-    const T *x = (const T *)p.x + (int64_t)w.t0 * dim + ch;
-    const T *dl = (const T *)p.delta + (int64_t)w.t0 * dim + ch;
-    const T *z = GATE ? (const T *)p.z + (int64_t)w.t0 * p.z_stride + ch : nullptr;
-    T *y = (T *)p.y + (int64_t)w.t0 * dim + ch;
+    // Bytes: a row's start is uniform, and what a lane adds to it for the tokens of a block are four constants (the host
+    // admits strides whose 16 rows lie within 32 bits), cut off at the last token's
+    const uint32_t row = (uint32_t)dim * sizeof(T), zrow = (uint32_t)p.z_stride * sizeof(T), bcrow = (uint32_t)p.bc_stride * sizeof(T);
+    const uint32_t chb = (uint32_t)ch * sizeof(T);
+    uint32_t at[4], zat[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[j] = (4 * j + q) * row + chb, zat[j] = (4 * j + q) * zrow + chb;
+    auto row_of = [&](const void *a, int t, uint32_t bytes) { return (const char *)a + (int64_t)(w.t0 + t) * bytes; };
     // this lane's eighth of a token's B (q < 2) and C
-    const T *src = (q < 2 ? (const T *)p.B + 8 * q : (const T *)p.C + 8 * (q - 2)) + (int64_t)w.t0 * p.bc_stride;
+    const char *src = (const char *)(q < 2 ? (const T *)p.B + 8 * q : (const T *)p.C + 8 * (q - 2));
 
     struct Block {
         uint32_t x[4], d[4], z[4];  // tokens 4 j + q (as 32-bit words: 16-bit pairs would tie two loads together)
         Raw8<T> bc;                 // token lane / 4
     };
-    auto raw = [](const T *a) -> uint32_t {
-        if constexpr (sizeof(T) == 4) return __float_as_uint(*a);
-        else return *a;
+    auto raw = [](const char *a) -> uint32_t {
+        if constexpr (sizeof(T) == 4) return __float_as_uint(*(const T *)a);
+        else return *(const T *)a;
     };
     auto val = [](uint32_t w) { return __uint_as_float(sizeof(T) == 4 ? w : w << 16); };
     auto load = [&](int t, Block &b) {
+        const int ts = t < len ? t : len - 1;
+        const uint32_t left = len - 1 - ts < kBlk - 1 ? len - 1 - ts : kBlk - 1;
+        const uint32_t end = left * row + chb, zend = left * zrow + chb, bcat = (cl < (int)left ? cl : left) * bcrow;
+        const char *x = row_of(p.x, ts, row), *dl = row_of(p.delta, ts, row), *z = row_of(p.z, ts, zrow);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t tt = t + 4 * j + q < len ? t + 4 * j + q : len - 1;
-            b.x[j] = raw(x + tt * dim);
-            b.d[j] = raw(dl + tt * dim);
-            b.z[j] = GATE ? raw(z + tt * p.z_stride) : 0u;
+            const uint32_t o = at[j] < end ? at[j] : end, oz = zat[j] < zend ? zat[j] : zend;
+            b.x[j] = raw(x + o);
+            b.d[j] = raw(dl + o);
+            b.z[j] = GATE ? raw(z + oz) : 0u;
         }
-        const int64_t tb = t + cl < len ? t + cl : len - 1;
-        if (FULL || q < 2) b.bc = load_any8(src + tb * p.bc_stride);
+        if (FULL || q < 2) b.bc = load_any8((const T *)(row_of(src, ts, bcrow) + bcat));
     };
     float sum = 0.f;
     auto compute = [&](int t, const Block &b) {
@@ -434,6 +441,10 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = raw_f32(b.bc, e);
+            if (t + kBlk > len && t + cl >= len) {  // (the last token's again, and 0 times an infinity is not 0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            }
             *(float4 *)&bc[cl][8 * q] = make_float4(v[0], v[1], v[2], v[3]);
             *(float4 *)&bc[cl][8 * q + 4] = make_float4(v[4], v[5], v[6], v[7]);
         }
@@ -446,11 +457,16 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            d[j] = t + 4 * j + q < len ? d[j] : 0.f;  // past the end: the identity step
-            dx[j] = t + 4 * j + q < len ? d[j] * val(b.x[j]) : 0.f;
+            dx[j] = d[j] * val(b.x[j]);
             gate[j] = GATE ? silu(val(b.z[j])) : 1.f;
-            sum += d[j];
         }
+        if (t + kBlk > len) {  // past the end: the identity step
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + 4 * j + q >= len) d[j] = dx[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += d[j];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (t + 4 * j >= len) break;
@@ -486,7 +502,7 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) h[n] = fmaf(e[i][n], h[n], u[i][n]);
-                if constexpr (FULL) yt[i] = fmaf(Cq[i].x, h[0], Cq[i].y * h[1]) + fmaf(Cq[i].z, h[2], Cq[i].w * h[3]);
+                if constexpr (FULL) yt[i] = fmaf(Cq[i].w, h[3], fmaf(Cq[i].z, h[2], fmaf(Cq[i].y, h[1], Cq[i].x * h[0])));
             }
             if constexpr (FULL) {
                 // lane q gets the sum of yt[q] over the four lanes
@@ -495,8 +511,7 @@ __device__ __forceinline__ void scan_piece(const ScanParams &p, const Piece &w, 
                 const float r1 = (b0 ? yt[3] : yt[2]) + quad<kQuadXor1>(b0 ? yt[2] : yt[3]);
                 const float r = (b1 ? r1 : r0) + quad<kQuadXor2>(b1 ? r0 : r1);
                 const float v = fmaf(Dd, val(b.x[j]), r) * gate[j];
-                const int64_t tt = t + 4 * j + q;
-                if (live && tt < len) y[tt * dim] = Io<T>::to(v);
+                if (live && t + 4 * j + q < len) *(T *)((char *)row_of(p.y, t, row) + at[j]) = Io<T>::to(v);
             }
         }
     };
@@ -753,6 +768,8 @@ struct ScanArgs {
     bool packed;
 };
 
+constexpr int64_t kMaxStride = INT64_C(1) << 26;
+
 int scan_check(const ScanArgs &a, bool *nothing) {
     *nothing = false;
     if (a.rows < 0 || a.nseq < 0 || a.nslots < 0 || a.dim < 0 || a.dstate < 0) return SELSCAN_E_SHAPE;
@@ -764,6 +781,8 @@ int scan_check(const ScanArgs &a, bool *nothing) {
         return a.nseq == 0 && a.rows > 0 && a.dim > 0 ? SELSCAN_E_SHAPE : SELSCAN_OK;
     }
     if (a.bc_stride < kN || (a.z && a.z_stride < a.dim)) return SELSCAN_E_SHAPE;
+    // 16 rows of any array within 32 bits
+    if (a.packed && (a.dim > kMaxStride || a.bc_stride > kMaxStride || (a.z && a.z_stride > kMaxStride))) return SELSCAN_E_UNSUPPORTED;
     if (a.h && !a.slots && a.nslots < a.nseq) return SELSCAN_E_SHAPE;
     if (mul_size(a.rows, a.bc_stride) < 0 || (a.z && mul_size(a.rows, a.z_stride) < 0) || mul_size(a.rows, a.dim) < 0 ||
         mul_size(a.nslots, a.dim * kN) < 0)

@@ -74,6 +74,8 @@ def test_scan_packed_refusals():
     assert scan(bcs=15) == SHAPE and scan(z=P + 8 * MB, zs=63) == SHAPE and scan(nslots=1) == SHAPE
     assert scan(nseq=0) == SHAPE and scan(nseq=0, tokens=0) == OK and scan(dim=0) == OK
     assert scan(N=8) == UNSUPPORTED and scan(dt=3) == UNSUPPORTED and scan(flags=4) == UNSUPPORTED
+    far = (1 << 26) + 1  # 16 rows of a longer stride do not lie within 32 bits
+    assert scan(dim=far) == UNSUPPORTED and scan(bcs=far) == UNSUPPORTED and scan(z=P + 8 * MB, zs=far) == UNSUPPORTED
     assert scan(A=P + 2 * MB + 2) == ALIGN and scan(h=P + 6 * MB + 4) == ALIGN and scan(B=P + 3 * MB + 1) == ALIGN
     need = S.selscan_packed_workspace_bytes(1000, 2, 1000, 64)
     assert need > 0
