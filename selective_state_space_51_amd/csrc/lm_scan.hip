@@ -371,8 +371,8 @@ constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;
 //    in order: no barrier.
 //  - The next block's x, delta, z, B and C are in flight during a block's arithmetic.
 //
-// Bound by instruction issue (33 VALU instructions and 2 LDS accesses per token of a wave, with gate and softplus; 27,591 tokens
-// in 24 sequences x 4,096 channels bf16: 545 to 560 us, four fifths of it VALU issue).  A lane per
+// Bound by instruction issue (34 VALU instructions and 2 LDS accesses per token of a wave, with gate and softplus; 27,591 tokens
+// in 24 sequences x 4,096 channels bf16: 550 to 605 us, about four fifths of it VALU issue).  A lane per
 // channel with all 16 states and B and C as scalar operands needs a tenth less issue per element, but a
 // quarter of the waves, each token taking four times as long: measured slower wherever the chip was not full
 // of long sequences of equal length.
@@ -719,13 +719,13 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
 }
 
 // Tokens per segment, or 0: whole sequences.
-//  - In clocks of a SIMD a wave's token takes 245 alone and 150 beside others (measured), a map's 115.  Whole sequences take
+//  - In clocks of a SIMD a wave's token was measured at 245 alone and 150 beside others, a map's at 115.  Whole sequences take
 //    the longest alone, or all evenly plus a quarter for lengths that do not even out; segments take both passes, and 25,000
 //    for the second launch and the join.
 //  - Segments of multiples of 16 (a block) that give each compute unit four workgroups: measured, 4,097 tokens x 1,536
-//    channels fp32 72 us at 96 tokens (4.0 workgroups per unit), 74 at 64, 79 at 112, 90 at 176 and 434 whole; 505 tokens in 8
-//    sequences x 1,536 bf16 18 us at 16, 20 at 32, 22 at 64 and 34 whole; 27,591 tokens in 24 sequences x 4,096 734 us at
-//    256, and 650 whole.
+//    channels fp32 67 us at 96 tokens (4.0 workgroups per unit), 69 at 64, 75 at 112, 85 at 176 and 372 whole; 505 tokens in 8
+//    sequences x 1,536 bf16 17.6 us at 16, 18.4 at 32, 21 at 64 and 28.5 whole; 27,591 tokens in 24 sequences x 4,096 746 us
+//    at 256, and 537 whole.
 constexpr int kSimds = 1024, kUnits = 256;  // MI355X: 256 compute units of 4
 constexpr int kWalk = 16;                   // segments up to which the second launch walks the maps itself
 
