@@ -386,7 +386,8 @@ int add_rms_norm_bwd(const void *dy, const void *s, const void *x, int64_t x_str
     if (rows > 0 && (!dy || !s || !weight || !rstd)) return SELSCAN_E_NULL;
     const size_t b = io_bytes(io_dtype), r = io_bytes(residual_dtype);
     const size_t need = dweight ? add_rms_norm_bwd_workspace_bytes(rows, width) : 0;
-    if (!span_aligned(dy, b) || !span_aligned(x, b) || !span_aligned(dx, b) || !span_aligned(s, r) || !span_aligned(dresidual_out, r) ||
+    if (!span_aligned(dy, b) || !span_aligned(x, b) || !span_aligned(dx, b) || !span_aligned(s, r) ||
+        !span_aligned(dresidual_out, r) ||
         !span_aligned(dresidual, r) || !span_aligned(weight, 4) || !span_aligned(rstd, 4) || !span_aligned(dweight, 4) ||
         (need && !span_aligned(workspace, 16)))
         return SELSCAN_E_ALIGN;
@@ -407,7 +408,8 @@ int add_rms_norm_bwd(const void *dy, const void *s, const void *x, int64_t x_str
         p.rows_per = (rows + p.slots - 1) / p.slots;
         p.slots = (int)((rows + p.rows_per - 1) / p.rows_per);
         const bool vec = width % 8 == 0 && span_aligned(dy, 16) && span_aligned(s, 16) && span_aligned(weight, 16) &&
-                         span_aligned(dresidual_out, 16) && span_aligned(dx, 16) && span_aligned(dresidual, 16) && (!x || (span_aligned(x, 16) && x_stride * b % 16 == 0));
+                         span_aligned(dresidual_out, 16) && span_aligned(dx, 16) && span_aligned(dresidual, 16) &&
+                         (!x || (span_aligned(x, 16) && x_stride * b % 16 == 0));
         rc = launch_types<true>(p, io_dtype, residual_dtype, vec, stream);
         if (rc != SELSCAN_OK || !dweight) return rc;
     }

@@ -823,12 +823,15 @@ ScanParams scan_params(const ScanArgs &a) {
     return p;
 }
 
+constexpr int64_t kGridY = 65535;
+
 template <typename T, bool ZOH, bool GATE>
 int launch_scan(const ScanParams &p, int64_t blocks, void *stream) {
     const dim3 grid((unsigned)blocks);
     int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, grid, dim3(256), p, stream);
     if (rc == SELSCAN_OK && p.joined)
-        rc = enqueue(scan_join, dim3((unsigned)((p.dim * kN + 63) / 64), (unsigned)(p.q.nseq < 65535 ? p.q.nseq : 65535)), dim3(64), p, stream);
+        rc = enqueue(scan_join, dim3((unsigned)((p.dim * kN + 63) / 64), (unsigned)(p.q.nseq < kGridY ? p.q.nseq : kGridY)), dim3(64),
+                     p, stream);
     if (rc == SELSCAN_OK && p.seg) rc = enqueue(scan_packed<T, ZOH, GATE, 1>, grid, dim3(256), p, stream);
     return rc;
 }
@@ -846,8 +849,6 @@ int step_rows(int64_t rows, int64_t threads_per_row) {
     int64_t n = rows * threads_per_row / full;
     return n < 1 ? 1 : n > 8 ? 8 : (int)n;
 }
-
-constexpr int64_t kGridY = 65535;
 
 // States of this many bytes go without a place in the caches.  By the time a model's next token comes to a layer again the
 // other layers' states have passed, 256 MB of them from 32 layers on.  Measured with states that are in no cache, with a

@@ -123,8 +123,8 @@ def add_rms_norm_bwd_workspace_bytes(rows: int, width: int) -> int:
 
 def add_rms_norm_bwd(dy, s, weight, rstd, x_dtype=None, dresidual_out=None, workspace=None, stream=None):
     """Gradients of add_rms_norm_fwd's "io" output: dy [rows, width]; s and rstd (its rstd=True result, as it is)
-    from the forward; dresidual_out the gradient that reaches s by the residual path (None: none).  Returns a dict: dx (x_dtype, which is dy's),
-    dresidual (the same numbers in s's dtype; dx itself where the dtypes agree) and dweight (fp32 [width])."""
+    from the forward; dresidual_out the gradient that reaches s by the residual path (None: none).  Returns a dict:
+    dx (x_dtype, which is dy's), dresidual (the same numbers in s's dtype; dx itself where the dtypes agree) and dweight (fp32 [width])."""
     if x_dtype not in (None, dy.dtype):
         raise TypeError("dy must have x's dtype")
     # a sum that was rounded to 16 bits is formed anew from x and the residual
