@@ -92,25 +92,25 @@ __device__ __forceinline__ Base base_of(float m, float c) {
 // what a row comes to: from its largest logit m and s, t as they were taken with base_of(m)
 template <typename T, bool WRITE>
 struct RowEnd {
-    float m, c, ls;  // ls: log2 of sum 2^(c (x - m))
+    float m, scale, ls;  // ls: log of sum exp(scale (x - m))
     bool empty, nan;
 
     // (lead: one thread of those that call this writes)
-    __device__ __forceinline__ RowEnd(const LpParams &p, int row, float m_, float s, float t, bool lead) : m(m_), c(p.c) {
+    __device__ __forceinline__ RowEnd(const LpParams &p, int row, float m_, float s, float t, bool lead) : m(m_), scale(p.scale) {
         const float l = __builtin_amdgcn_logf(s);
-        ls = l - base_of(m, c).rest;
+        ls = (l - base_of(m, p.c).rest) * kLn2;
         empty = s == 0.f, nan = s != s;
         if (!WRITE || !lead) return;
         p.stats[2 * (int64_t)row] = m;
-        p.stats[2 * (int64_t)row + 1] = ls * kLn2;
+        p.stats[2 * (int64_t)row + 1] = ls;
         p.entropy[row] = empty ? 0.f : (l - t / s) * kLn2;
         const int64_t y = p.targets[row];
         float lp = 0.f;
         if (y >= 0 && y < p.vocab) lp = empty ? -INFINITY : logp(Io<T>::f32(((const T *)p.x)[row * p.stride + y]));
         p.logprob[row] = lp;
     }
-    // (c (x - m) exactly as far as x - m is)
-    __device__ __forceinline__ float logp(float x) const { return fmaf(x - m, c, -ls) * kLn2; }
+    // exactly as far as x - m is; by the scale itself, since c (x - m) of a masked logit of the type's lowest value overflows
+    __device__ __forceinline__ float logp(float x) const { return fmaf(x - m, scale, -ls); }
     __device__ __forceinline__ void put(const LpParams &p, int row, unsigned long long k, int rank) const {
         if (rank >= p.top) return;
         p.top_logprob[(int64_t)row * p.top + rank] = logp(value_of((uint32_t)(k >> 32)));
