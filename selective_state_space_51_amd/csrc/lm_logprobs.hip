@@ -3,8 +3,9 @@
 // MI355X (gfx950).
 //
 // With c = scale log2 e, m the largest logit of a row and a = c (x - m):
-//     s = sum 2^a,  t = sum 2^a a,  logprob = ln 2 (a[target] - log2 s),  entropy = ln 2 (log2 s - t / s).
-// (x - m before the product: a row of the type's lowest value, whose c x overflows, is a row of equal logits.)
+//     s = sum 2^a,  t = sum 2^a a,  logprob = scale (x[target] - m) - ln s,  entropy = ln 2 (log2 s - t / s).
+// a is c x - fl(c m) in one fma where c m is below 2^24; else x - m comes before the product, so that a row of the
+// type's lowest value, whose c x overflows, is a row of equal logits.
 // A row is cut into slices that a workgroup holds in registers, so the logits are read once; the
 // slices' (m, s, t) and their best alternatives are joined by a second, small kernel.  HBM bound: 2,048 x 50,280 bf16 with
 // five alternatives 48 us (4.3 TB/s of reads; a plain reduction of a large array reaches 4.05) and 5 for the join.  Few rows
@@ -79,14 +80,19 @@ __device__ __forceinline__ float kth_of_wave(float v, int k) {
     return value_of(sizeof(T) == 2 ? (best << 16) | (best & 0x8000u ? 0u : 0xFFFFu) : best);
 }
 
-// c m as it was taken off the logits: its rounding where that is finite, else nothing (the subtraction came first)
+// How a largest logit m is taken off: c x - fl(c m) in one fma, whose terms all carry the factor 2^(c m - fl(c m)), taken out
+// again at the end; or, where c m is so large that its rounding would be more than half a step of the exponent (a factor
+// that can itself overflow, and at the far end a c x that does), c (x - m).
+constexpr float kPlainBase = 16777216.f;  // 2^24: fl(c m) is off by 1/2 at most
 struct Base {
-    float mc, rest;  // c m = mc + rest
+    float mc;
+    bool plain;
+    float rest;  // plain: c m - fl(c m)
 };
 __device__ __forceinline__ Base base_of(float m, float c) {
     const float mc = m * c;
-    if (fabsf(mc) < INFINITY) return {mc, fmaf(m, c, -mc)};
-    return {mc, 0.f};
+    const bool plain = fabsf(mc) < kPlainBase;
+    return {mc, plain, plain ? fmaf(m, c, -mc) : 0.f};
 }
 
 // what a row comes to: from its largest logit m and s, t as they were taken with base_of(m)
@@ -129,8 +135,8 @@ struct RowEnd {
 // workgroup finishes it; else a slice for logprobs_join.
 //
 // a = c x - fl(c m) takes one fma per logit instead of c (x - m)'s two operations; the rounding of c m is the same
-// for all logits and so a factor of s and t, which the join takes out again (from the exact residue of c m).  Where
-// c m overflows (a row of the type's lowest value), the subtraction comes first.
+// for all logits and so a factor of s and t, which the join takes out again (from the exact residue of c m).  base_of says
+// where the subtraction has to come first.
 //
 // Alternatives: the `top`-th largest of a wave's 64 per-lane maxima is no larger than the slice's `top`-th
 // largest logit, so every logit of the slice that can be among the best is at or above the largest of the
@@ -168,9 +174,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
     m = red[0];
 #pragma unroll
     for (int i = 1; i < NW; ++i) m = fmaxf(m, red[i]);
-    const float mc = m * p.c;  // (-inf: nothing but -inf)
+    const Base off = base_of(m, p.c);
+    const float mc = off.mc;
     float s = 0.f, t = 0.f;
-    if (fabsf(mc) < INFINITY) {
+    if (off.plain) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
 #pragma unroll
@@ -180,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_slice(LpParams p) {
                 t = fmaf(w, fmaxf(a, -200.f), t);  // 2^-200 is 0: no 0 * inf for a logit of -inf
             }
     } else {
-        const float mm = m == -INFINITY ? 0.f : m;
+        const float mm = m == -INFINITY ? 0.f : m;  // (nothing but -inf)
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
 #pragma unroll
@@ -303,15 +310,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_join(LpParams p) {
     for (int i = lane; i < p.nsl; i += 64) M = fmaxf(M, part[i].x);
     M = wave_max(M);
     const Base B = base_of(M, p.c);
-    const bool finite = fabsf(B.mc) < INFINITY;
     float s = 0.f, t = 0.f;
     for (int i = lane; i < p.nsl; i += 64) {
         const float4 q = part[i];
         // a slice of nothing but -inf has s = t = 0, or NaN where it holds one: taken as it is
         const bool none = q.x == -INFINITY;
-        const Base b = base_of(q.x, p.c);
         // how far the slice's base lies below the row's, as both were taken off
-        const float d = none ? 0.f : finite && fabsf(b.mc) < INFINITY ? b.mc - B.mc : (q.x - M) * p.c;
+        const float d = none ? 0.f : fmaf(q.x - M, p.c, B.rest - base_of(q.x, p.c).rest);
         const float f = none ? 1.f : __builtin_amdgcn_exp2f(d);
         s = fmaf(q.y, f, s);
         t = fmaf(f, fmaf(q.y, fmaxf(d, -200.f), q.z), t);

@@ -27,6 +27,89 @@ def _say(*a):
     print("[case]", *a, file=sys.stderr, flush=True)
 
 
+def rows_of(vocab, rows, dtype, seed):
+    """Logits whose rows each hold one kind of large magnitude, targets and gradients."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    io = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = 3.0 * torch.randn(rows, vocab, generator=g, device="cuda")
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    lows = [-1e9, -1e10, -1e12, -1e30, float(torch.finfo(io).min)]
+    first, last = slice(0, vocab // 2), slice(vocab // 2, vocab)  # at 20,000 logits each holds a whole slice
+    r = 0
+    for low in lows:
+        x[r, first] = low          # half the row masked, the target among the masked or not
+        x[r + 1, last] = low
+        t[r], t[r + 1] = 3, 4
+        x[r + 2] = low             # all of it: equal logits
+        x[r + 3] = low
+        x[r + 3, vocab - 7] = 2.0  # all but one
+        t[r + 3] = vocab - 7
+        x[r + 4] = -low            # the same magnitudes above zero
+        x[r + 5, 11] = -low
+        t[r + 5] = 11
+        x[r + 6] = low * (1 + torch.rand(vocab, generator=g, device="cuda")) if low > -1e30 else low
+        r += 7
+    # bases either side of 2^24 / c in neighbouring slices, as close as the type has them
+    x[r] = 11_600_000.0 + torch.randint(0, 9, (vocab,), generator=g, device="cuda")
+    x[r, last] = 11_700_000.0
+    x[r + 1] = 1e4 + x[r + 1]
+    assert rows >= r + 2
+    return x.to(io), t, torch.randn(rows, generator=g, device="cuda"), torch.randn(rows, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.5, 1 / 1.5, 1.0, 1.43])
+@pytest.mark.parametrize("vocab,rows", [(5000, 40), (20000, 40), (20000, 400), (40000, 300)])
+def test_logits_of_any_magnitude(vocab, rows, scale, dtype):
+    import selective_state_space_51_amd as S
+    torch = _torch()
+    _say("logprobs", vocab, rows, scale, dtype)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    x, t, dl, dh = rows_of(vocab, rows, dtype, seed=vocab + rows)
+    top = 5
+    lp, ent, stats, val, idx = S.token_logprobs_fwd(x, t, top=top, scale=scale)
+    grads = [S.token_logprobs_bwd(x, t, stats, ent, *g, scale=scale) for g in ((dl, dh), (dl, None), (None, dh))]
+    torch.cuda.synchronize()
+    n = 40  # the rows with large magnitudes, and a few ordinary ones
+    x, t, dl, dh = x[:n], t[:n], dl[:n].double(), dh[:n].double()
+    v = x.double() * scale
+    want = torch.log_softmax(v, 1)
+    p = want.exp()
+    h = torch.special.entr(p).sum(1)
+
+    def close(name, got, exact, bar):
+        out = exact.abs() > FLT_MAX * (1 - 8 * U)  # a log probability that fp32 does not hold, or only just
+        assert bool((got[out].double() <= -FLT_MAX * (1 - 16 * U)).all()), name
+        got, exact, bar = got[~out].double(), exact[~out], bar[~out]
+        assert bool(torch.isfinite(got).all()), name
+        assert float(((got - exact).abs() - bar).max()) <= 0, (name, float((got - exact).abs().max()))
+
+    pick = want.gather(1, t[:, None])[:, 0]
+    close("logprob", lp[:n], pick, 135 * U + 8 * U * pick.abs())
+    close("entropy", ent[:n], h, (135 + 135 * 15 + 8 * 15) * U * torch.ones_like(h))
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True)[1][:, :top]
+    assert torch.equal(idx[:n], order)
+    best = want.gather(1, order)
+    close("alternatives", val[:n], best, 135 * U + 8 * U * best.abs())
+    assert torch.equal(stats[:n, 0], x.float().amax(1))
+    # the gradients; where p is 0 so are they
+    hot = torch.zeros_like(p)
+    hot.scatter_(1, t[:, None], 1.0)
+    lg = torch.where(p > 0, want, torch.zeros_like(want))
+    for got, (gl, gh) in zip(grads, ((dl, dh), (dl, 0 * dh), (0 * dl, dh))):
+        gl, gh = gl[:, None], gh[:, None]
+        exact = scale * (gl * (hot - p) - gh * p * (lg + h[:, None]))
+        bar = scale * p * (gl.abs() * (135 + 5 * lg.abs() + 4)
+                           + gh.abs() * ((lg.abs() + h[:, None]) * (135 + 5 * lg.abs() + 4) + 300 + 8 * lg.abs() + 2300)) * U
+        bar = bar + 4 * U * exact.abs()
+        if dtype == "bf16":
+            bar = bar + 2.0 ** -8 * (exact.abs() + bar)
+        got = got[:n].double()
+        assert bool(torch.isfinite(got).all())
+        assert float(((got - exact).abs() - bar - 1e-36).max()) <= 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab", [5000, 20000])
 def test_a_masked_logit_of_the_lowest_value_has_its_log_probability(vocab, dtype):
