@@ -173,6 +173,21 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _launch_stream(stream, operands):
+    """The torch stream that `stream` names: itself, or by its raw handle (an integer) a stream of the operands' device.
+    Handle 0 is that device's default stream; torch.cuda.ExternalStream takes it for no handle and hands out a stream of its
+    pool, which nothing orders with the default one."""
+    torch = _torch()
+    device = next((t.device for t in operands if isinstance(t, torch.Tensor)), None)
+    device = device if device is not None and device.type == "cuda" else None  # (others are refused with the operand's name)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if device is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands are on {device}")
+    return stream
+
+
 def _on_launch_stream(fn):
     """Run `fn` with its `stream` argument (when given) as the current stream, so that every tensor
     it allocates -- outputs, and workspaces dropped once the launch is enqueued -- belongs to the
@@ -185,7 +200,7 @@ def _on_launch_stream(fn):
         if stream is None:
             return fn(*args, stream=None, **kwargs)
         torch = _torch()
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        s = _launch_stream(stream, (*args, *kwargs.values()))
         with torch.cuda.stream(s):
             return fn(*args, stream=s, **kwargs)
 

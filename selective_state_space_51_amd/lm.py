@@ -51,23 +51,19 @@ def _load():
 
 
 lm_lib = _load()
-from . import _lm_binding as _C  # noqa: E402
+from . import _launch_stream, _lm_binding as _C  # noqa: E402
 
 
 def lm_abi_version() -> int:
     return int(lm_lib.selscan_lm_abi_version())
 
 
-def _on(stream):
-    """`stream` (a torch stream or a raw handle) as the current one: kernels run there, and what a call allocates
-    belongs to it."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-
-
 def _run(stream, fn, *args):
+    """fn(*args) with `stream` (a torch stream or a raw handle; None: the current one) as the current one: kernels run
+    there, and what a call allocates belongs to it."""
     if stream is None:
         return fn(*args)
-    with _on(stream):
+    with torch.cuda.stream(_launch_stream(stream, args)):
         return fn(*args)
 
 
