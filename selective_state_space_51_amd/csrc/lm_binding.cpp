@@ -7,6 +7,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -45,13 +46,20 @@ int io_code(const Tensor &t) {
 void want_device(const char *name, const Tensor &t) {
     if (!t.is_cuda()) throw py::value_error(std::string(name) + " must be a device tensor");
 }
+// on the device of the launch, which is the current one (see Launch)
+void want_here(const char *name, const Tensor &t) {
+    want_device(name, t);
+    if (t.get_device() != c10::hip::current_device())
+        throw py::value_error(std::string(name) + " is on " + t.device().str() + ", the first argument is on cuda:" +
+                              std::to_string(c10::hip::current_device()));
+}
 void want_dtype(const char *name, const Tensor &t, at::ScalarType dt) {
     if (t.scalar_type() != dt) throw py::type_error(std::string(name) + " must be " + c10::toString(dt));
 }
 
-// address of a contiguous device tensor of one dtype
+// address of a contiguous tensor of one dtype
 void *ptr(const char *name, const Tensor &t, at::ScalarType dt) {
-    want_device(name, t);
+    want_here(name, t);
     if (!t.is_contiguous()) throw py::value_error(std::string(name) + " must be contiguous");
     want_dtype(name, t, dt);
     return t.numel() ? t.data_ptr() : nullptr;
@@ -69,7 +77,7 @@ struct Rows {
     int64_t stride = 0;
 };
 Rows rows_of(const char *name, const Tensor &t, at::ScalarType dt) {
-    want_device(name, t);
+    want_here(name, t);
     want_dtype(name, t, dt);
     if (t.dim() != 2) throw py::value_error(std::string(name) + " must have two dimensions");
     const int64_t rows = t.size(0), width = t.size(1);
@@ -115,7 +123,7 @@ Workspace workspace(size_t need, const Opt &given, const Tensor &like) {
     Workspace w;
     if (!need) return w;
     w.own = given ? *given : empty({(int64_t)need}, like, at::kByte);
-    want_device("workspace", w.own);
+    want_here("workspace", w.own);
     if (!w.own.is_contiguous()) throw py::value_error("workspace must be contiguous");
     w.p = w.own.data_ptr();
     w.bytes = w.own.nbytes();
