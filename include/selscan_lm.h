@@ -19,6 +19,11 @@
  *    its array, as each call says below.
  *  - No output may overlap an input or another output unless a call says so (SELSCAN_E_ALIAS).
  *  - All sums are in a fixed order: results are the same from run to run.
+ *  - A launch holds 2^32 - 1 threads along an axis, 16,777,215 workgroups of 256; calls that take more are refused
+ *    (SELSCAN_E_UNSUPPORTED, before any launch).  Workgroups of 256 are: of the packed scan, 64 channels of a sequence or of one of
+ *    its segments; of the packed convolution, 2,048 channels of at least 4 tokens; of the log probabilities, a row of up to 8,192
+ *    logits or 4,096 and more of a longer one's; of the norm, four rows up to width 1,024, one up to 8,192 (beyond, 1,024
+ *    threads each: 4,194,303 rows); of the 4-bit product, 64 rows of the matrix.
  */
 #ifndef SELSCAN_LM_H
 #define SELSCAN_LM_H

@@ -27,6 +27,9 @@ inline int64_t mul_size(int64_t a, int64_t b) {
     return a > (INT64_C(1) << 62) / b ? -1 : a * b;
 }
 
+// A dispatch counts its threads along an axis in 32 bits: whether that many workgroups of that many threads are a launch
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 // every output against every input and every other output
 inline bool any_alias(const Span *in, int nin, const Span *out, int nout) {
     for (int i = 0; i < nout; ++i) {

@@ -374,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd(LpParams p) {
     const bool valid = y >= 0 && y < p.vocab;
     const float gl = p.dlogprob && valid ? p.dlogprob[row] * p.scale : 0.f;
     const float gh = p.dentropy ? p.dentropy[row] * p.scale : 0.f;
-    const float m = p.in_stats[2 * row], ls = p.in_stats[2 * row + 1] * kLog2e;
+    const float m = p.in_stats[2 * (int64_t)row], ls = p.in_stats[2 * (int64_t)row + 1] * kLog2e;
     const bool empty = m == -INFINITY && !(ls != ls);
     // -gl p - gh p (ln 2 a + H) = p (k0 + k1 a), a = log2 p
     const float k0 = -fmaf(gh, p.in_entropy[row], gl), k1 = -gh * kLn2;
@@ -480,13 +480,13 @@ int token_logprobs_fwd(const void *logits, int64_t logits_stride, const int64_t 
     (bf ? nt ? logprobs_slice<uint16_t, PIECES, WHOLE, true> : logprobs_slice<uint16_t, PIECES, WHOLE, false>     \
         : nt ? logprobs_slice<float, PIECES, WHOLE, true> : logprobs_slice<float, PIECES, WHOLE, false>)
     if (whole_row(vocab)) {
-        if (rows > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+        if (!grid_fits(rows, kThreads)) return SELSCAN_E_UNSUPPORTED;
         return enqueue(PICK(4, true), dim3((unsigned)rows), dim3(kThreads), p, stream);
     }
     const int pieces = pieces_for(rows, vocab);
     p.nsl = (int)slices_for(rows, vocab);
     const int64_t blocks = rows * p.nsl;
-    if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (!grid_fits(blocks, kThreads)) return SELSCAN_E_UNSUPPORTED;
     p.part = (float4 *)workspace;
     p.cand = (unsigned long long *)(p.part + blocks);
     // (slices of 2 pieces are of a few rows)
@@ -524,7 +524,7 @@ int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t 
     const int64_t per = kBwdPieces * kThreads * 8;
     p.nsl = (int)((vocab + per - 1) / per);
     const int64_t blocks = rows * p.nsl;
-    if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (!grid_fits(blocks, kThreads)) return SELSCAN_E_UNSUPPORTED;
     const bool nt = rows * vocab * (int64_t)s >= kBackwardPast;
     return enqueue(io_dtype == SELSCAN_BF16 ? nt ? logprobs_bwd<uint16_t, true> : logprobs_bwd<uint16_t, false>
                                             : nt ? logprobs_bwd<float, true> : logprobs_bwd<float, false>,

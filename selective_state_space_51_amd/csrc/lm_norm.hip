@@ -302,7 +302,7 @@ int launch_norm(const NormParams &p, void *stream) {
     const int64_t units = BWD ? p.slots : p.rows;
     const int block = s.tpr < 256 ? 256 : s.tpr, per = block / s.tpr;
     const int64_t blocks = (units + per - 1) / per;
-    if (blocks > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (!grid_fits(blocks, block)) return SELSCAN_E_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), bl(block);
     const bool past = BWD && p.rows * p.width * 8 >= kReadsPast;
 #define GO(TPR, NV)                                                                        \

@@ -880,7 +880,7 @@ int causal_conv1d_packed_fwd(const void *x, int64_t x_stride, const float *weigh
     // sequences, 117 waves: 9.4 and 5.8)
     const int shift = segments(tokens, nseq, 1 << kConvLong) * ((groups + 63) / 64) >= kSimds / 2 ? kConvLong : kConvShort;
     const dim3 grid((unsigned)segments(tokens, nseq, 1 << shift), (unsigned)((groups + block - 1) / block));
-    if (grid.y > kGridY) return SELSCAN_E_UNSUPPORTED;
+    if (grid.y > kGridY || !grid_fits(segments(tokens, nseq, 1 << shift), block)) return SELSCAN_E_UNSUPPORTED;
     void (*k)(ConvParams) = nullptr;
 #define PICK(T, S) (width == 1 ? conv_packed<T, 1, S> : width == 2 ? conv_packed<T, 2, S> : width == 3 ? conv_packed<T, 3, S> : conv_packed<T, 4, S>)
 #define PICK_T(S) (io_dtype == SELSCAN_BF16 ? PICK(uint16_t, S) : PICK(float, S))
@@ -944,7 +944,7 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
         p.sdt = p.seg + pieces * dim * kN;
         p.joined = max_seqlen / p.size > kWalk ? 1 : 0;
     }
-    if (pieces * p.ntiles > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (!grid_fits(pieces * p.ntiles, 256)) return SELSCAN_E_UNSUPPORTED;
     const bool zoh = (flags & SELSCAN_FLAG_ZOH) != 0;
     return io_dtype == SELSCAN_BF16 ? launch_scan_io<uint16_t>(p, pieces * p.ntiles, zoh, stream)
                                     : launch_scan_io<float>(p, pieces * p.ntiles, zoh, stream);
@@ -964,6 +964,7 @@ int selscan_step(const void *x, const void *delta, const float *A, const void *B
     p.rows_per = step_rows(rows, dim * 4);
     while ((rows + p.rows_per - 1) / p.rows_per > kGridY) p.rows_per *= 2;
     const dim3 grid((unsigned)((dim * 4 + 255) / 256), (unsigned)((rows + p.rows_per - 1) / p.rows_per));
+    if (!grid_fits(grid.x, 256)) return SELSCAN_E_UNSUPPORTED;
     const bool zoh = (flags & SELSCAN_FLAG_ZOH) != 0;
     const bool nt = rows * dim * kN * 4 >= kStatesPast;
 #define PICK(T) (zoh ? nt ? scan_step<T, true, true> : scan_step<T, true, false> : nt ? scan_step<T, false, true> : scan_step<T, false, false>)

@@ -473,7 +473,7 @@ int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *
     if (rows == 0 || n == 0) return SELSCAN_OK;
     if (k == 0 || x_stride < k || mul_size(rows, x_stride) < 0 || mul_size(rows, n) < 0 || mul_size(n, k) < 0) return SELSCAN_E_SHAPE;
     // sizes that the launch grid and 32-bit indexes within a row hold
-    if (k > (1 << 24) || x_stride > (1 << 26) || rows > 32 * INT64_C(65535) || n > 16 * (int64_t)INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (k > (1 << 24) || x_stride > (1 << 26) || rows > 32 * INT64_C(65535) || !grid_fits((n + 63) / 64, 256)) return SELSCAN_E_UNSUPPORTED;
     if (!x || !qweight || !scales || !y) return SELSCAN_E_NULL;
     const size_t s = io_bytes(io_dtype);
     if (!span_aligned(x, s) || !span_aligned(y, s) || !span_aligned(qweight, 16) || !span_aligned(scales, 2) ||
