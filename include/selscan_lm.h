@@ -164,7 +164,7 @@ size_t add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
  *   top         : 0..32 (SELSCAN_E_UNSUPPORTED above; no more than vocab, SELSCAN_E_SHAPE)
  *   top_logprob : [rows][top] fp32, top_index : [rows][top] int64; entries without probability
  *                 (a logit of -inf) are (-inf, -1)
- *   scale       : finite and > 0, vocab at most 2^21 (SELSCAN_E_UNSUPPORTED)
+ *   scale       : > 0 and at most 2.35e38 (times log2 e it is finite); vocab at most 2^21 (SELSCAN_E_UNSUPPORTED)
  * A logit of -inf has probability 0.  A row of nothing but -inf has stats -inf, logprob -inf and
  * entropy 0.  A row with a NaN or +inf has NaN for its log sum, logprob, entropy and alternatives (index -1).
  *   workspace   : token_logprobs_workspace_bytes(...) bytes, 16-byte aligned (0, and NULL will do, where a workgroup holds

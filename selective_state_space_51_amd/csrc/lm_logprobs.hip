@@ -429,7 +429,7 @@ constexpr int64_t kForwardPast = INT64_C(112) << 20, kBackwardPast = INT64_C(160
 
 int lp_check(const void *logits, int64_t stride, const int64_t *targets, float scale, int64_t rows, int64_t vocab, int dtype) {
     if (rows < 0 || vocab < 0) return SELSCAN_E_SHAPE;
-    if (!io_known(dtype) || !(scale > 0.f) || !(scale < INFINITY) || vocab > kMaxVocab) return SELSCAN_E_UNSUPPORTED;
+    if (!io_known(dtype) || !(scale > 0.f) || !(scale * kLog2e < INFINITY) || vocab > kMaxVocab) return SELSCAN_E_UNSUPPORTED;
     if (rows == 0 || vocab == 0) return SELSCAN_OK;
     if (stride < vocab || mul_size(rows, stride) < 0) return SELSCAN_E_SHAPE;
     if (!logits || !targets) return SELSCAN_E_NULL;

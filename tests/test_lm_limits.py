@@ -30,6 +30,16 @@ def test_logprobs_rows():
         assert call(1 << 30, 2) == UNSUPPORTED
 
 
+def test_logprobs_scale():
+    # the exponents are of base 2: a scale whose product with log2 e overflows would make every one of them NaN
+    fwd = lambda scale: L.token_logprobs_fwd(A(0), 8, A(1), scale, 0, A(2), A(3), A(4), None, None, 0, 8, 1, None, 0, None)
+    bwd = lambda scale: L.token_logprobs_bwd(A(0), 8, A(1), A(2), A(3), A(4), None, scale, A(5), 0, 8, 1, None)
+    for call in (fwd, bwd):
+        assert call(2.35e38) == OK and call(1e-38) == OK
+        for scale in (2.4e38, 3.4e38):
+            assert call(scale) == UNSUPPORTED
+
+
 def test_packed_sequences():
     def conv(tokens, nseq, dim):
         return L.causal_conv1d_packed_fwd(A(0), dim, A(1), None, A(2), None, None, None, 0, A(3), tokens, nseq, 0, dim, 4, 1, None)
