@@ -197,7 +197,9 @@ int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t 
  *   bias    : [n] fp32, nullable;  y : [rows][n] io_dtype
  *   group   : 32, 64 or 128 (SELSCAN_E_UNSUPPORTED), dividing k (SELSCAN_E_SHAPE)
  *   k at most 2^24 and x_stride at most 2^26 (SELSCAN_E_UNSUPPORTED)
- * The products and sums of a group are exact up to fp32 accumulation; fp32 x is not rounded.
+ * The products and sums of a group are exact up to fp32 accumulation; fp32 x is not rounded.  An output whose sums pass
+ * fp32's range on the way (an infinite x, or one above 1e37) is formed anew in 64 bits, with the infinities and NaN of the
+ * formula.
  * Meant for few rows; any number is computed, 32 at a time per pass over the weights.
  */
 int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *scales, const void *zeros,

@@ -196,6 +196,30 @@ __device__ __forceinline__ void unit_products(F fx, const uint4 *w, const uint32
     }
 }
 
+// One output by its definition in 64 bits, for those that the matrix cores leave infinite or NaN.  An infinite x or one
+// above 1e37 does that where the definition has a number or an infinity: (16 + q) x and -(16 + zero) x overflow before they
+// cancel.  Neither goes away in what is added after it, so the end is where to look; a row without such x never comes here.
+template <typename T, int GM>
+__device__ __forceinline__ float output_in_64_bits(const W4Params &p, int64_t tok, int64_t row) {
+    const T *x = (const T *)p.x + tok * p.x_stride;
+    const uint8_t *q = p.q + row * (p.k >> 1);
+    double sum = 0.;
+#pragma unroll 1
+    for (int g = 0; g < p.groups && sum == sum; ++g) {
+        const double scale = Io<uint16_t>::f32(p.scales[row * p.groups + g]);
+        const int zero = p.zeros ? p.zeros[row * p.groups + g] & 15 : 8;
+#pragma unroll 1
+        for (int i = 0; i < 16 * GM; ++i) {
+            const int b = q[g * 16 * GM + i];
+            const T *at = x + 2 * (g * 16 * GM + i);
+            sum = fma((double)((b & 15) - zero) * scale, (double)Io<T>::f32(at[0]), sum);
+            sum = fma((double)((b >> 4) - zero) * scale, (double)Io<T>::f32(at[1]), sum);
+        }
+    }
+    return (float)(p.bias ? sum + p.bias[row] : sum);
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
 // Many rows of the matrix: the four waves of a workgroup take 16 rows each and the whole of k together, so that x is
 // staged, split and reordered once for all of them, and no sums are left to join.  x has two buffers: one barrier
 // per unit.  The matrix is loaded two units ahead, x one.
@@ -289,13 +313,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void w4_rows(W4Params 
     const int64_t row = row0 + i;
     if (row >= p.n) return;
     const float b = p.bias ? p.bias[row] : 0.f;
+    uint32_t again = 0;  // outputs 4 t + c
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int64_t tok = tok0 + 16 * t + 4 * g + c;
-            if (tok < p.rows) ((T *)p.y)[tok * p.n + row] = Io<T>::to(acc[t][c] + b);
+            if (tok < p.rows) {
+                ((T *)p.y)[tok * p.n + row] = Io<T>::to(acc[t][c] + b);
+                if (!finite(acc[t][c])) again |= 1u << (4 * t + c);
+            }
         }
+#pragma unroll 1
+    for (; again; again &= again - 1) {
+        const int o = __builtin_ctz(again);
+        const int64_t tok = tok0 + 16 * (o >> 2) + 4 * g + (o & 3);
+        ((T *)p.y)[tok * p.n + row] = Io<T>::to(output_in_64_bits<T, GM>(p, tok, row));
+    }
 }
 
 // Few rows of the matrix: a workgroup takes 16 of them and its waves share out k, upw units each, and add their sums in
@@ -423,7 +457,8 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
         if (tok >= p.rows || row >= p.n) continue;
         float v = 0.f;
         for (int w = 0; w < nw; ++w) v += red[w * TM * 256 + o];
-        if (p.bias) v += p.bias[row];
+        if (!finite(v)) v = output_in_64_bits<T, GM>(p, tok, row);
+        else if (p.bias) v += p.bias[row];
         ((T *)p.y)[tok * p.n + row] = Io<T>::to(v);
     }
 }
