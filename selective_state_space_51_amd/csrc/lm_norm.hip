@@ -10,6 +10,8 @@
 // int8 output 2.8 us in a graph.
 #include "lm_common.h"
 
+#include <float.h>
+
 namespace {
 
 struct NormParams {
@@ -138,8 +140,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
         for (int v = 0; v < NV; ++v)
             store_piece<R, TPR, VEC>((R *)p.residual_out + row * p.width, v, tr, p.width, s[v]);
     }
-    const float mean = (float)(row_reduce<TPR, false>(ss, sums, 0) * p.inv_width64);
-    const float rstd = 1.f / sqrtf(mean + p.eps);
+    const double mean64 = row_reduce<TPR, false>(ss, sums, 0) * p.inv_width64;
+    const float mean = (float)mean64, under = mean + p.eps;
+    float rstd = 1.f / sqrtf(under);
+    // a row of values past 1.8e19, or below 1e-19 with an eps of 0: its mean square is no normal number of fp32, its root is
+    if (!(under >= FLT_MIN && under < INFINITY)) rstd = (float)(1. / sqrt(mean64 + (double)p.eps));
     if (p.rstd && tr == 0) p.rstd[row] = rstd;
     float amax = 0.f;
 #pragma unroll

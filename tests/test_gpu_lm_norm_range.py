@@ -1,0 +1,50 @@
+"""GPU tests of add_rms_norm_fwd and add_rms_norm_bwd on rows of any magnitude: values whose squares pass fp32's range
+either way, non-finite weights, against the formulas in 64 bits.
+
+Bars as in the operator's other tests, with U = 2^-24: y within 34 U of itself (and half an ulp of bf16), rstd within 32
+U; where rstd is below 2^-126 its spacing is 2^-149, half of which is 4 U of the least there is, 2^-128."""
+import sys
+
+import pytest
+
+from tests import test_gpu_lm_norm as N
+
+pytestmark = pytest.mark.gpu
+U = N.U
+
+
+def _say(*a):
+    print("[case]", *a, file=sys.stderr, flush=True)
+
+
+@pytest.mark.parametrize("width", [8, 100, 640, 2048, 5000, 20000])
+@pytest.mark.parametrize("dtype,res", [("bf16", "f32"), ("bf16", "io"), ("f32", "f32")])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_rows_whose_squares_leave_fp32(width, dtype, res, eps):
+    import torch
+
+    import selective_state_space_51_amd as S
+    _say("norm range", width, dtype, res, eps)
+    i = N.make(9, width, dtype, res, seed=21)
+    size = torch.tensor([1e20, 3e19, 1e30, 2e37, 1.0, 1e-18, 1e-21, 1e-30, 1e19], device="cuda")[:, None]
+    i["x"] = (i["x"].float().clamp(-4, 4) * size).to(i["x"].dtype)
+    i["r"] = (i["r"].float().clamp(-4, 4) * size).to(i["r"].dtype)
+    s32 = i["x"].float() + i["r"].float()
+    # (against the sum as fp32 holds it: its own rounding is a bar of the other tests)
+    s = s32.double()
+    rstd = 1 / torch.sqrt((s * s).mean(1, keepdim=True) + eps)
+    y = s * rstd * i["w"].double()
+    got, so, saved = S.add_rms_norm_fwd(i["x"], i["w"], residual=i["r"], eps=eps, rstd=True)
+    rs = saved[0] if isinstance(saved, tuple) else saved
+    assert torch.equal(so, s32.to(i["r"].dtype))
+    N.within("rstd", rs[:, None], rstd, 36 * U * rstd)
+    N.within("y", got, y, (38 * U + N.half_ulp(got) * (1 + 64 * U)) * y.abs() + 2.0 ** -40 * min(1.0, eps * 1e9))
+    # the gradients take rstd and the sum as they are
+    i["dres"].zero_()
+    ds, dw, mags, bar = N.backward64(i, s, rs.double()[:, None])
+    g = S.add_rms_norm_bwd(i["dy"], so, i["w"], saved, dresidual_out=i["dres"])
+    ok = ds.abs().amax(1) > 1e-30  # (of the largest rows they are smaller than fp32's normal numbers)
+    ok &= ds.abs().amax(1) < 1e37
+    for k in ("dx", "dresidual"):
+        N.within(k, g[k][ok], ds[ok], (bar + N.half_ulp(g[k]) * (ds.abs() + bar))[ok] + 1e-37)
+    N.within("dweight", g["dweight"], dw, (5 + 72) * U * mags + 2.0 ** -40)
