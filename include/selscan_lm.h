@@ -121,7 +121,8 @@ int selscan_step(const void *x, const void *delta, const float *A, const void *B
  *                  scale[r] * y[r][c], scale = max|row| / 127 (/ 448), each element rounded to
  *                  nearest even.  A row of zeros (or smaller than 1e-32) has scale 0 and zeros; a row whose
  *                  mean square is not finite in fp32 has scale NaN and zeros (values past 1.8e19, which
- *                  SELSCAN_LM_OUT_IO norms as any other).
+ *                  SELSCAN_LM_OUT_IO norms as any other), and so has one whose normed row holds a NaN or an
+ *                  infinity (a weight's, or a product's past fp32's range).
  *   rstd         : [rows] fp32, nullable
  *   eps          : >= 0, finite (SELSCAN_E_UNSUPPORTED); width at most 32768 (SELSCAN_E_UNSUPPORTED)
  */

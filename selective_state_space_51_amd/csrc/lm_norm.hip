@@ -146,15 +146,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
     // a row of values past 1.8e19, or below 1e-19 with an eps of 0: its mean square is no normal number of fp32, its root is
     if (!(under >= FLT_MIN && under < INFINITY)) rstd = (float)(1. / sqrt(mean64 + (double)p.eps));
     if (p.rstd && tr == 0) p.rstd[row] = rstd;
-    float amax = 0.f;
+    // the largest magnitude as a whole number, in whose order a NaN is the largest (fmaxf would drop it)
+    uint32_t most = 0;
+    // (a row of zeros with an eps of 0 has an infinite rstd; its 8-bit output is zeros all the same)
+    const float by = p.kind != SELSCAN_LM_OUT_IO && mean64 == 0. ? 0.f : rstd;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         float w[8];
         load_piece<float, TPR, VEC>(p.weight, v, tr, p.width, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            s[v][e] = s[v][e] * rstd * w[e];
-            amax = fmaxf(amax, fabsf(s[v][e]));
+            s[v][e] = s[v][e] * by * w[e];
+            const uint32_t u = __float_as_uint(s[v][e]) & 0x7FFFFFFFu;
+            most = u > most ? u : most;
         }
     }
     if (p.kind == SELSCAN_LM_OUT_IO) {
@@ -162,10 +166,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd(NormParams p) 
         for (int v = 0; v < NV; ++v) store_piece<T, TPR, VEC>((T *)p.y + row * p.width, v, tr, p.width, s[v]);
         return;
     }
-    amax = row_reduce<TPR, true>(amax, sh, 0);
+    const float amax = row_reduce<TPR, true>(most > 0x7F800000u ? INFINITY : __uint_as_float(most), sh, 0);
     const float top = p.kind == SELSCAN_LM_OUT_INT8 ? 127.f : 448.f;
-    // fmaxf drops a NaN: a row that holds one (or whose mean square overflows) is marked by its scale
-    const bool bad = !(mean < INFINITY), zero = bad || amax < 1e-32f;
+    // a row that holds an infinity or a NaN (or whose mean square overflows) is marked by its scale
+    const bool bad = !(mean < INFINITY) || amax == INFINITY, zero = bad || amax < 1e-32f;
     const float inv = zero ? 0.f : top * (1.f / amax);
     if (tr == 0) p.scale[row] = bad ? NAN : zero ? 0.f : amax * (1.f / top);
     uint8_t *y = (uint8_t *)p.y + row * p.width;

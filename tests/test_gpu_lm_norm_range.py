@@ -48,3 +48,36 @@ def test_rows_whose_squares_leave_fp32(width, dtype, res, eps):
     for k in ("dx", "dresidual"):
         N.within(k, g[k][ok], ds[ok], (bar + N.half_ulp(g[k]) * (ds.abs() + bar))[ok] + 1e-37)
     N.within("dweight", g["dweight"], dw, (5 + 72) * U * mags + 2.0 ** -40)
+
+
+@pytest.mark.parametrize("width", [8, 100, 640, 2048, 5000, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_8_bit_rows_with_a_weight_that_is_no_number(width, dtype):
+    """y is NaN or infinite at the weight's column, in every row but those of zeros times an infinity, which are NaN there:
+    no 8-bit row stands for that, and its scale says so."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    _say("norm 8-bit weights", width, dtype)
+    i = N.make(5, width, dtype, "f32", seed=4)
+    i["x"][2], i["r"][2] = 0, 0
+    for bad in (float("nan"), float("inf"), -float("inf"), 3e38):
+        w = i["w"].clone()
+        w[width - 3] = bad
+        x, r = i["x"].clone(), i["r"].clone()
+        x[:, width - 3], r[:, width - 3] = 5.0, 1.0  # (normed it is above 1.2: 3e38 times that is infinite)
+        x[2], r[2] = 0, 0
+        finite = bad == 3e38
+        for kind in ("int8", "fp8"):
+            q, s, sc = S.add_rms_norm_fwd(x, w, residual=r, out=kind)
+            assert torch.equal(s, x.float() + r)
+            for row in range(5):
+                if row == 2 and finite:  # 0 times a number
+                    assert float(sc[2]) == 0
+                else:
+                    assert bool(torch.isnan(sc[row])), (kind, bad, row)
+                assert float(q[row].float().abs().max()) == 0
+    # a row of zeros is zeros with an eps of 0 too
+    for kind in ("int8", "fp8"):
+        q, _, sc = S.add_rms_norm_fwd(i["x"], i["w"], residual=i["r"], out=kind, eps=0.0)
+        assert float(sc[2]) == 0 and float(q[2].float().abs().max()) == 0 and bool((sc[[0, 1, 3, 4]] > 0).all())
