@@ -54,15 +54,23 @@ struct Segment {
 // entries past 2^31 are none: slots are int32
 __device__ __forceinline__ int slot_in(const Seqs &q, int v) { return v >= 0 && v < q.nslots ? v : -1; }
 
+// What is kept of a segment until the next one starts from it has a place of its own, its entry: floor(cu[s] / z) + j for
+// segment j of sequence s.  A segment that is not its sequence's last ends at j z + z < len, so that entries of different
+// sequences differ and all of them lie below floor(tokens / z): none is set aside for a sequence of one segment.
+//
 // The sequence of a segment is the last one whose first segment is not after it: a search 64 positions wide,
 // whose last round also brings the offsets, slots and carries (one trip to memory in all for up to 64 sequences).
 // Every lane of the wave takes part.  div_z: division by z.
-template <class F>
+//
+// BY_ENTRY: the segment that starts from entry `seg` (the last sequence whose first entry is not after it is the entry's, or it
+// is no one's and the segment found lies past that sequence's end).
+template <bool BY_ENTRY = false, class F>
 __device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, F div_z, int lane) {
+    constexpr int OWN = BY_ENTRY ? 0 : 1;  // numbers that a sequence has beyond its entries
     int lo = 0, n = q.nseq;
     while (n > 64) {
         const int step = (n + 63) >> 6, i = lane * step;
-        const bool at_or_before = i < n && div_z(cu_at(q, lo + i)) + lo + i <= seg;
+        const bool at_or_before = i < n && div_z(cu_at(q, lo + i)) + OWN * (lo + i) <= seg;
         int c = __popcll(__ballot(at_or_before));
         c = c < 1 ? 1 : c;
         lo += (c - 1) * step;
@@ -72,11 +80,12 @@ __device__ __forceinline__ Segment find_segment(const Seqs &q, int seg, F div_z,
     const int i = lo + (lane < n ? lane : n - 1);
     const int a = cu_at(q, i), b = cu_at(q, i + 1);
     const int sl = q.slots ? q.slots[i] : i, ca = q.carry ? q.carry[i] : 0;
-    int c = __popcll(__ballot(lane < n && div_z(a) + lo + lane <= seg));
+    int c = __popcll(__ballot(lane < n && div_z(a) + OWN * (lo + lane) <= seg));
     c = __builtin_amdgcn_readfirstlane(c < 1 ? 0 : c - 1);
     const int s = lo + c, t0 = __builtin_amdgcn_readlane(a, c), t1 = __builtin_amdgcn_readlane(b, c);
-    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0, seg - __builtin_amdgcn_readfirstlane(div_z(t0)) - s,
-            slot_in(q, __builtin_amdgcn_readlane(sl, c)), __builtin_amdgcn_readlane(ca, c) != 0};
+    return {__builtin_amdgcn_readfirstlane(s), t0, t1 > t0 ? t1 - t0 : 0,
+            seg - __builtin_amdgcn_readfirstlane(div_z(t0)) + (BY_ENTRY ? 1 : -s), slot_in(q, __builtin_amdgcn_readlane(sl, c)),
+            __builtin_amdgcn_readlane(ca, c) != 0};
 }
 // a sequence as one segment
 __device__ __forceinline__ Segment whole_sequence(const Seqs &q, int s) {
@@ -335,8 +344,8 @@ struct ScanParams {
     const float *A, *D, *bias;
     void *y;
     float *h;     // cache, or NULL
-    float *seg;   // split: [nsegs][dim][16] end state of a segment, from zero but for a sequence's first
-    float *sdt;   // split: [nsegs][dim] sum of delta over the segment
+    float *seg;   // split: [entries][dim][16] end state of a segment, from zero but for a sequence's first
+    float *sdt;   // split: [entries][dim] sum of delta over the segment
     Seqs q;
     int64_t dim, bc_stride, z_stride;
     int softplus;
@@ -345,6 +354,7 @@ struct ScanParams {
     int ntiles;    // blocks of 64 channels
     int round;     // whole sequences: how many fill the compute units once (0: taken as they come)
     int joined;    // split: scan_join runs between the launches
+    int entries;   // split: of seg and sdt
     int rows_per;  // step: rows a thread takes one after another
 };
 
@@ -549,7 +559,9 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     const int64_t ch = c0 + (lane >> 2) < dim ? c0 + (lane >> 2) : dim - 1;
     const float4 av = load_f4(p.A + ch * kN + 4 * q);
     const bool split = p.seg != nullptr;
-    const Segment g = split ? find_segment(p.q, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane)
+    const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
+    const Segment g = LAUNCH == 1 ? find_segment<true>(p.q, seg, div, lane)
+                      : split     ? find_segment(p.q, seg, div, lane)
                       : p.round ? dealt_sequence(p.q, seg, p.round, lane)
                                 : whole_sequence(p.q, seg);
     const int first = split ? g.j * p.size : 0, size = split ? p.size : g.len;
@@ -560,8 +572,8 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     float *cache = p.h && g.slot >= 0 ? p.h + g.slot * st : nullptr;
     Piece w{g.t0 + first, last ? g.len - first : size, nullptr, nullptr, nullptr};
     if (last) w.h_out = cache;
-    else if (LAUNCH == 0) w.h_out = p.seg + seg * st;
-    if (LAUNCH == 0) w.sdt = split ? p.sdt + seg * dim : nullptr;
+    else if (LAUNCH == 0) w.h_out = p.seg + (int64_t)(seg - g.s) * st;
+    if (LAUNCH == 0) w.sdt = split ? p.sdt + (int64_t)(seg - g.s) * dim : nullptr;
 
     const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
     float h[4] = {0.f, 0.f, 0.f, 0.f};
@@ -574,8 +586,9 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
         else scan_piece<T, ZOH, false, false>(p, w, bc_lds[wave], c0, lane, a2, h);
     } else {
         // the state this segment starts from: the maps of those before it, in order, or what scan_join left
-        const float *e = p.seg + (int64_t)(seg - g.j) * st + ch * kN + 4 * q;
-        const float *d = p.sdt + (int64_t)(seg - g.j) * dim + ch;
+        const int entry0 = seg - (g.j - 1);  // of the sequence
+        const float *e = p.seg + entry0 * st + ch * kN + 4 * q;
+        const float *d = p.sdt + entry0 * dim + ch;
         const int n = p.joined ? 1 : g.j;
         if (p.joined) e += (g.j - 1) * st;
         constexpr int U = 4;  // maps loaded ahead
@@ -602,33 +615,43 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
 }
 
 // Joins the segments of long sequences between the launches: one thread per (sequence, channel, state) walks the
-// maps in order and leaves the state at the end of each segment in its place.
+// maps in order and leaves the state at the end of each segment in its place.  Sequences are dealt out by their numbers, or,
+// where there are more sequences than entries, by those entries that are their first.
 __global__ __launch_bounds__(64) void scan_join(ScanParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x, ch = i / kN, st = p.dim * kN;
-    if (ch >= p.dim) return;
-    const float a2 = p.A[i] * kLog2e;
-    for (int s = blockIdx.y; s < p.q.nseq; s += gridDim.y) {
-        const Range rg = range_of(p.q, s);
-        const int first = (int)fdiv((uint32_t)rg.t0, p.dsize) + s;
-        const int n = (int)fdiv((uint32_t)(rg.len + p.size - 1), p.dsize) - 1;  // all but the last
-        if (n < 2) continue;
-        float *e = p.seg + (int64_t)first * st + i;
-        const float *d = p.sdt + (int64_t)first * p.dim + ch;
-        float h = e[0];
-        constexpr int U = 16;  // segments loaded ahead
-        for (int j0 = 1; j0 < n; j0 += U) {
-            float ev[U], dv[U];
+    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x, st = p.dim * kN, ch = i / kN < p.dim ? i / kN : p.dim - 1;
+    const bool live = i < st, by_entry = p.q.nseq > p.entries;
+    const float a2 = p.A[live ? i : 0] * kLog2e;
+    const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
+    for (int b = blockIdx.y; b < (by_entry ? p.entries : p.q.nseq); b += gridDim.y) {
+        Range rg;
+        if (by_entry) {
+            const Segment g = find_segment<true>(p.q, b, div, threadIdx.x);
+            if (g.j != 1) continue;  // not its sequence's first
+            rg = {g.t0, g.len};
+        } else {
+            rg = range_of(p.q, b);
+        }
+        const int first = div(rg.t0);
+        const int n = rg.len > 0 ? div(rg.len - 1) : 0;  // all but the last
+        if (n >= 2 && live) {
+            float *e = p.seg + (int64_t)first * st + i;
+            const float *d = p.sdt + (int64_t)first * p.dim + ch;
+            float h = e[0];
+            constexpr int U = 16;  // segments loaded ahead
+            for (int j0 = 1; j0 < n; j0 += U) {
+                float ev[U], dv[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t j = j0 + u < n ? j0 + u : n - 1;
-                ev[u] = e[j * st];
-                dv[u] = d[j * p.dim];
-            }
+                for (int u = 0; u < U; ++u) {
+                    const int64_t j = j0 + u < n ? j0 + u : n - 1;
+                    ev[u] = e[j * st];
+                    dv[u] = d[j * p.dim];
+                }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (j0 + u >= n) break;
-                h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
-                e[(j0 + u) * st] = h;
+                for (int u = 0; u < U; ++u) {
+                    if (j0 + u >= n) break;
+                    h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
+                    e[(j0 + u) * st] = h;
+                }
             }
         }
     }
@@ -742,9 +765,9 @@ int split_size(int64_t tokens, int64_t max_seqlen, int64_t dim) {
     return 2 * size <= longest ? size : 0;
 }
 
-size_t packed_workspace(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim) {
+size_t packed_workspace(int64_t tokens, int64_t max_seqlen, int64_t dim) {
     const int size = split_size(tokens, max_seqlen, dim);
-    return size ? (size_t)segments(tokens, nseq, size) * (size_t)dim * (kN + 1) * sizeof(float) : 0;
+    return size ? (size_t)(tokens / size) * (size_t)dim * (kN + 1) * sizeof(float) : 0;
 }
 
 struct ScanArgs {
@@ -827,12 +850,13 @@ constexpr int64_t kGridY = 65535;
 
 template <typename T, bool ZOH, bool GATE>
 int launch_scan(const ScanParams &p, int64_t blocks, void *stream) {
-    const dim3 grid((unsigned)blocks);
-    int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, grid, dim3(256), p, stream);
-    if (rc == SELSCAN_OK && p.joined)
-        rc = enqueue(scan_join, dim3((unsigned)((p.dim * kN + 63) / 64), (unsigned)(p.q.nseq < kGridY ? p.q.nseq : kGridY)), dim3(64),
-                     p, stream);
-    if (rc == SELSCAN_OK && p.seg) rc = enqueue(scan_packed<T, ZOH, GATE, 1>, grid, dim3(256), p, stream);
+    int rc = enqueue(scan_packed<T, ZOH, GATE, 0>, dim3((unsigned)blocks), dim3(256), p, stream);
+    if (rc == SELSCAN_OK && p.joined) {
+        const int64_t y = p.q.nseq < p.entries ? p.q.nseq : p.entries;
+        rc = enqueue(scan_join, dim3((unsigned)((p.dim * kN + 63) / 64), (unsigned)(y < kGridY ? y : kGridY)), dim3(64), p, stream);
+    }
+    if (rc == SELSCAN_OK && p.seg)
+        rc = enqueue(scan_packed<T, ZOH, GATE, 1>, dim3((unsigned)((int64_t)p.entries * p.ntiles)), dim3(256), p, stream);
     return rc;
 }
 
@@ -913,7 +937,7 @@ size_t selscan_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_
     if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || dim <= 0 || dstate != kN || tokens > INT32_MAX || nseq > INT32_MAX / 2 ||
         dim > INT32_MAX)
         return 0;
-    return packed_workspace(tokens, nseq, max_seqlen, dim);
+    return packed_workspace(tokens, max_seqlen, dim);
 }
 
 int selscan_packed_fwd(const void *x, const void *delta, const float *A, const void *B, const void *C,
@@ -941,7 +965,8 @@ int selscan_packed_fwd(const void *x, const void *delta, const float *A, const v
         p.dsize = make_div((uint32_t)p.size);
         pieces = segments(tokens, nseq, p.size);
         p.seg = (float *)workspace;
-        p.sdt = p.seg + pieces * dim * kN;
+        p.entries = (int)(tokens / p.size);
+        p.sdt = p.seg + (int64_t)p.entries * dim * kN;
         p.joined = max_seqlen / p.size > kWalk ? 1 : 0;
     }
     if (!grid_fits(pieces * p.ntiles, 256)) return SELSCAN_E_UNSUPPORTED;

@@ -90,7 +90,8 @@ def selscan_packed_fwd(x, delta, A, B, C, cu_seqlens, h_state=None, D=None, z=No
                        workspace=None, stream=None):
     """selscan_fwd on packed prompts: x, delta, z [tokens, dim]; B, C [tokens, 16]; A [dim, 16]; cu_seqlens int32
     [nseq + 1].  h_state fp32 [nslots, dim, 16] is read for the sequences whose carry is set and updated in
-    place for all.  max_seqlen: the longest length or a bound on it (speed only)."""
+    place for all.  max_seqlen: the longest length or a bound on it (speed only; None: all tokens could be one sequence's,
+    which costs a set of short ones a second launch that finds little to do)."""
     return _run(stream, _C.selscan_packed_fwd, x, delta, A, B, C, cu_seqlens, h_state, D, z, delta_bias, delta_softplus,
                 zoh, slots, carry, max_seqlen, y, workspace)
 
