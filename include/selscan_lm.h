@@ -43,7 +43,8 @@ typedef enum { SELSCAN_LM_OUT_IO = 0, SELSCAN_LM_OUT_INT8 = 1, SELSCAN_LM_OUT_FP
  * Packed prompts.  The tokens of nseq sequences lie one after another in arrays of `tokens` rows;
  * sequence s has rows cu_seqlens[s] <= t < cu_seqlens[s+1] (int32 [nseq+1], rising, from 0 to
  * tokens; a sequence may be empty).  Offsets are clamped to [0, tokens], and a pair that falls
- * counts as an empty sequence; then, and for rows that no sequence holds, outputs are unspecified.
+ * counts as an empty sequence; then, and for rows that no sequence holds, outputs are unspecified.  At most 2^31 - 2^17
+ * tokens, or rows of a token step (SELSCAN_E_UNSUPPORTED).
  *
  * The cache has nslots entries.  slots[s] (int32 [nseq], NULL: slots[s] = s, which needs
  * nslots >= nseq) is the entry of sequence s; a value outside [0, nslots) means none: the sequence

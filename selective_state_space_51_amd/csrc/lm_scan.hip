@@ -15,6 +15,10 @@ namespace {
 // packed sequences
 // ------------------------------------------------------------------------------------
 
+// Tokens or rows of a call: tokens are counted in 32 bits, and a count may pass the last by two blocks of the scan or by
+// the rows that a thread of a step takes (65,536 at most).
+constexpr int64_t kMaxTokens = (INT64_C(1) << 31) - (1 << 17);
+
 struct Seqs {
     const int32_t *cu;     // [nseq + 1]
     const int32_t *slots;  // [nseq], or NULL: slot s
@@ -298,7 +302,7 @@ int conv_check(const void *x, int64_t x_stride, const float *weight, const float
     *nothing = false;
     if (rows < 0 || nseq < 0 || nslots < 0 || dim < 0) return SELSCAN_E_SHAPE;
     if (!io_known(io_dtype) || (flags & ~SELSCAN_FLAG_SILU) || width < 1 || width > 4) return SELSCAN_E_UNSUPPORTED;
-    if (rows > INT32_MAX || nseq > INT32_MAX / 2 || dim > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (rows > kMaxTokens || nseq > INT32_MAX / 2 || dim > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     if (dim == 0 || nseq == 0) {
         *nothing = true;
         return nseq == 0 && rows > 0 && dim > 0 ? SELSCAN_E_SHAPE : SELSCAN_OK;
@@ -798,7 +802,7 @@ int scan_check(const ScanArgs &a, bool *nothing) {
     if (a.rows < 0 || a.nseq < 0 || a.nslots < 0 || a.dim < 0 || a.dstate < 0) return SELSCAN_E_SHAPE;
     if (!io_known(a.dtype) || (a.flags & ~(SELSCAN_FLAG_DELTA_SOFTPLUS | SELSCAN_FLAG_ZOH)) || a.dstate != kN)
         return SELSCAN_E_UNSUPPORTED;
-    if (a.rows > INT32_MAX || a.nseq > INT32_MAX / 2 || a.dim > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
+    if (a.rows > kMaxTokens || a.nseq > INT32_MAX / 2 || a.dim > INT32_MAX) return SELSCAN_E_UNSUPPORTED;
     if (a.dim == 0 || a.nseq == 0) {
         *nothing = true;
         return a.nseq == 0 && a.rows > 0 && a.dim > 0 ? SELSCAN_E_SHAPE : SELSCAN_OK;
@@ -934,7 +938,7 @@ int causal_conv1d_step(const void *x, int64_t x_stride, const float *weight, con
 }
 
 size_t selscan_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t dim, int64_t dstate) {
-    if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || dim <= 0 || dstate != kN || tokens > INT32_MAX || nseq > INT32_MAX / 2 ||
+    if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || dim <= 0 || dstate != kN || tokens > kMaxTokens || nseq > INT32_MAX / 2 ||
         dim > INT32_MAX)
         return 0;
     return packed_workspace(tokens, max_seqlen, dim);

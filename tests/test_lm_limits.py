@@ -55,6 +55,23 @@ def test_packed_sequences():
     assert scan(1 << 30, 1 << 18, 1 << 29, 4096) == UNSUPPORTED
 
 
+def test_tokens_are_counted_in_32_bits():
+    # a walk in blocks, two of them ahead, must not pass 2^31
+    def scan(tokens):
+        return L.selscan_packed_fwd(A(0), A(1), A(2), A(3), A(4), 32, None, None, 0, None, 0, A(5), None, None, None, A(6), tokens,
+                                    1, 0, 1, 4, 16, 1, None, 0, None)
+
+    def step(rows):
+        return L.selscan_step(A(0), A(1), A(2), A(3), A(4), 32, None, None, 0, None, 0, A(5), A(6), A(7), rows, 1, 4, 16, 1, None)
+
+    def conv_step(rows):
+        return L.causal_conv1d_step(A(0), 4, A(1), None, A(2), A(3), 0, A(4), rows, 1, 4, 4, 1, None)
+    for call in (scan, step, conv_step):
+        for n in ((1 << 31) - 1, (1 << 31) - (1 << 17) + 1):
+            assert call(n) == UNSUPPORTED
+    assert S.selscan_packed_workspace_bytes((1 << 31) - 1, 1, (1 << 31) - 1, 64) == 0
+
+
 def test_step_channels_and_matrix_rows():
     def step(dim):
         return L.selscan_step(A(0), A(1), A(2), A(3), A(4), 32, None, None, 0, None, 0, A(5), A(6), A(7), 1, 1, dim, 16, 1, None)
