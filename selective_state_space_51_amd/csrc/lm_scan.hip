@@ -3,6 +3,8 @@
 // causal_conv1d_step, selscan_step of include/selscan_lm.h).  MI355X (gfx950).
 #include "lm_common.h"
 
+#include <float.h>
+
 #include <type_traits>
 
 namespace selscan_rt {
@@ -399,6 +401,13 @@ constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;
 // state that the maps before it lead to.  Whole sequences are the first launch alone, one segment each.
 constexpr int kBlk = 16;  // tokens per block
 
+// A as an exponent of 2.  An infinite one (a state that forgets at once) becomes the largest number, whose product with any
+// delta that is not 0 is as good, and with the 0 of a token past the end is 0.
+__device__ __forceinline__ float rate(float A) {
+    const float a = A * kLog2e;
+    return fabsf(a) == INFINITY ? copysignf(FLT_MAX, a) : a;
+}
+
 struct Piece {
     int t0, len;          // tokens
     const float *h_in;    // [dim][16] start state, or NULL: zero
@@ -579,7 +588,7 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
     else if (LAUNCH == 0) w.h_out = p.seg + (int64_t)(seg - g.s) * st;
     if (LAUNCH == 0) w.sdt = split ? p.sdt + (int64_t)(seg - g.s) * dim : nullptr;
 
-    const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
+    const float a2[4] = {rate(av.x), rate(av.y), rate(av.z), rate(av.w)};
     float h[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (LAUNCH == 0) {
         if (g.j == 0 && cache && g.carry) {
@@ -624,7 +633,7 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
 __global__ __launch_bounds__(64) void scan_join(ScanParams p) {
     const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x, st = p.dim * kN, ch = i / kN < p.dim ? i / kN : p.dim - 1;
     const bool live = i < st, by_entry = p.q.nseq > p.entries;
-    const float a2 = p.A[live ? i : 0] * kLog2e;
+    const float a2 = rate(p.A[live ? i : 0]);
     const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
     for (int b = blockIdx.y; b < (by_entry ? p.entries : p.q.nseq); b += gridDim.y) {
         Range rg;
@@ -685,7 +694,7 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
     if (ch >= p.dim) return;  // whole groups of four lanes leave
     const int n0 = (int)(i & 3) * 4;
     const float4 a = load_f4(p.A + ch * kN + n0);
-    const float a2[4] = {a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e};
+    const float a2[4] = {rate(a.x), rate(a.y), rate(a.z), rate(a.w)};
     const float Dd = p.D ? p.D[ch] : 0.f, bias = p.bias ? p.bias[ch] : 0.f;
     struct Row {
         int64_t slot;
