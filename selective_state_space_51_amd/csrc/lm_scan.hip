@@ -408,6 +408,14 @@ __device__ __forceinline__ float rate(float A) {
     return fabsf(a) == INFINITY ? copysignf(FLT_MAX, a) : a;
 }
 
+// The state after a segment, a map h -> 2^x h + end.  A negative delta can let x pass fp32's exponents (as a decay can on
+// the other side) over a segment whose own states do not, and a state of 0 has to stay 0: the power goes in as two finite
+// ones of half the exponent.  (Past 2 * 127 only a state below 2^-126 would not be infinite.)
+__device__ __forceinline__ float through_map(float h, float x, float end) {
+    const float e = __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(0.5f * x, -126.f, 127.f));
+    return fmaf(e, e * h, end);
+}
+
 struct Piece {
     int t0, len;          // tokens
     const float *h_in;    // [dim][16] start state, or NULL: zero
@@ -617,10 +625,10 @@ __global__ __launch_bounds__(256) void scan_packed(ScanParams p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (i0 + u >= n) break;
-                h[0] = fmaf(__builtin_amdgcn_exp2f(a2[0] * dv[u]), h[0], ev[u].x);
-                h[1] = fmaf(__builtin_amdgcn_exp2f(a2[1] * dv[u]), h[1], ev[u].y);
-                h[2] = fmaf(__builtin_amdgcn_exp2f(a2[2] * dv[u]), h[2], ev[u].z);
-                h[3] = fmaf(__builtin_amdgcn_exp2f(a2[3] * dv[u]), h[3], ev[u].w);
+                h[0] = through_map(h[0], a2[0] * dv[u], ev[u].x);
+                h[1] = through_map(h[1], a2[1] * dv[u], ev[u].y);
+                h[2] = through_map(h[2], a2[2] * dv[u], ev[u].z);
+                h[3] = through_map(h[3], a2[3] * dv[u], ev[u].w);
             }
         }
         scan_piece<T, ZOH, true, GATE>(p, w, bc_lds[wave], c0, lane, a2, h);
@@ -662,7 +670,7 @@ __global__ __launch_bounds__(64) void scan_join(ScanParams p) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (j0 + u >= n) break;
-                    h = fmaf(__builtin_amdgcn_exp2f(a2 * dv[u]), h, ev[u]);
+                    h = through_map(h, a2 * dv[u], ev[u]);
                     e[(j0 + u) * st] = h;
                 }
             }
