@@ -115,7 +115,9 @@ class MambaLM:
 
     def generate(self, prompts, n, slots=None):
         """n greedy tokens after each prompt: ([sequences][n] tokens, their log probabilities, the entropies)."""
-        slots = torch.arange(len(prompts), dtype=torch.int32, device=self.embed.device) if slots is None else slots
+        if not all(prompts):
+            raise ValueError("a prompt without tokens has no last one to go on from")
+        slots = torch.as_tensor(range(len(prompts)) if slots is None else slots, dtype=torch.int32, device=self.embed.device)
         x, residual, last = self.prefill(prompts, slots)
         out = []
         x, residual = x[last], residual[last]
