@@ -771,7 +771,11 @@ __global__ __launch_bounds__(256) void scan_step(ScanParams p) {
 //    sequences x 1,536 bf16 17.6 us at 16, 18.4 at 32, 21 at 64 and 28.5 whole; 27,591 tokens in 24 sequences x 4,096 746 us
 //    at 256, and 537 whole.
 constexpr int kSimds = 1024, kUnits = 256;  // MI355X: 256 compute units of 4
-constexpr int kWalk = 16;                   // segments up to which the second launch walks the maps itself
+// Segments of the longest sequence up to which the second launch walks the maps itself, without a join (the scan's time in
+// us, walked and joined, bf16: 256 tokens x 1,536 in 16 segments 12.3 and 15.2, 512 in 32 18.2 and 20.1, 4,097 in 42 61.3 and
+// 62.7; 800 x 512 in 50 16.5 and 17.6; 1,000 x 768 in 62 23.6 and 21.9; 1,300 x 512 in 81 23.9 and 23.1; 2,048 x 512 in 128 36
+// and 30)
+constexpr int kWalk = 48;
 
 int64_t segments(int64_t tokens, int64_t nseq, int64_t size) { return tokens / size + nseq; }
 

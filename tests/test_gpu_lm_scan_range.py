@@ -16,7 +16,8 @@ def _say(*a):
 
 @pytest.mark.parametrize("zoh", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens,whole", [((1, 2, 3, 5, 18, 31), True), ((100, 7, 333, 16, 35), False), ((700, 2), False)])
+@pytest.mark.parametrize("lens,whole", [((1, 2, 3, 5, 18, 31), True), ((100, 7, 333, 16, 35), False), ((700, 2), False),
+                                        ((1300, 2), False)])
 def test_states_that_forget_at_once(lens, whole, dtype, zoh):
     """A of -inf: the state is what the last token put there.  The lengths end inside groups of four tokens and blocks."""
     import selective_state_space_51_amd as S
@@ -32,7 +33,7 @@ def test_states_that_forget_at_once(lens, whole, dtype, zoh):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [(200, 190), (700, 333)])  # the second launch's walk, and a join of its own
+@pytest.mark.parametrize("lens", [(200, 190), (700, 333), (1500, 333)])  # the second launch's walk, and a join of its own
 def test_zero_states_outlast_growth(lens, dtype):
     """delta below zero (no softplus): exp(A sum delta) of 16 tokens is exp(32 n) for state n, and nothing comes in before
     token 60, so that every state is 0 until then and whatever delta does matters not."""
@@ -50,7 +51,7 @@ def test_zero_states_outlast_growth(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [(200, 190), (700, 333)])
+@pytest.mark.parametrize("lens", [(200, 190), (700, 333), (1500, 333)])
 def test_small_states_that_grow_past_the_exponents(lens, dtype):
     """States of about 2^-110 that one segment's 16 tokens raise by exp(6.25 n), up to exp(100) = 2^144, and the next 16 let
     fall again.  Up to 100 nats of exponent in fp32, each with three roundings (A log2 e, its product with delta, the constant),
