@@ -468,9 +468,11 @@ __global__ __launch_bounds__(512) void w4_split(W4Params p) {
 template <typename T, int GM, int TM>
 int launch_w4(const W4Params &p, void *stream) {
     const int64_t tiles = (p.n + 15) / 16, blocks_y = (p.rows + 16 * TM - 1) / (16 * TM);
-    // shared x where that leaves two workgroups per compute unit (measured at 1 and 32 rows, k 2,048 / n 16,384: 13.1 and
-    // 18.0 us with it, 8.2 and 13.3 without; n 50,280: 18.0 and 25, without 20.3 and 35)
-    if (tiles >= 4 * 2 * 256)
+    // shared x where that leaves two workgroups per compute unit, of fp32 x one: its stages let fewer waves share out k.
+    // Measured at 1 and 32 rows, us, with it and without, k 2,048: n 16,384 bf16 11.2 and 13.8, 8.6 and 14.4; n 50,280 bf16
+    // 16.9 and 23.3, 21.1 and 37.4; n 8,192 fp32 14.2 and 22.8, 9.0 and 21.7; n 16,384 fp32 14.5 and 23.4, 15.8 and 26.1; n 24,576
+    // fp32 17.5 and 28.1, 22.3 and 43.7.  k 8,192: n 20,000 bf16 43.5 and 51.5, 26.8 and 46.0, fp32 59.6 and 97, 57.6 and 121.
+    if (tiles >= 4 * 256 * (sizeof(T) == 2 ? 2 : 1))
         return enqueue(w4_rows<T, GM, TM>, dim3((unsigned)((tiles + 3) / 4), (unsigned)blocks_y), dim3(256), p, stream);
     // waves over k: four, or eight where there are few workgroups (n 8,192, k 2,048, one row: 5.6 us with four, 6.3 with
     // eight; n 16,384: 8.2 and 10.8); at most one per unit
