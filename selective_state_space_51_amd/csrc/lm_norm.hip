@@ -5,8 +5,8 @@
 // threads share a row, each with 8 NV of its elements, the fewest threads that hold it in 32 registers each or fewer (a
 // wave up to 1,024 elements, so that no barrier is needed; four waves up to 8,192; 16 beyond).
 //
-// HBM bound where there are many rows: 16,384 x 2,048, bf16 with an fp32 residual, takes 71 us forward (5.7 TB/s of what it
-// reads and writes) and 110 + 5 us backward (4.9 TB/s).  With few it is the launch and one trip to memory: 5 x 2,048 with an
+// HBM bound where there are many rows: 16,384 x 2,048, bf16 with an fp32 residual, takes 72 us forward (5.6 TB/s of what it
+// reads and writes; with an int8 output 69 us, with e4m3 68, 5.4 TB/s) and 110 + 5 us backward (4.9 TB/s).  With few it is the launch and one trip to memory: 5 x 2,048 with an
 // int8 output 2.8 us in a graph.
 #include "lm_common.h"
 
