@@ -6,7 +6,9 @@
  *     lengths, with each prompt's state kept in a cache, and on one token per sequence;
  *   - residual addition + root-mean-square norm, with an 8-bit output, and its gradients;
  *   - log probability of a token, entropy and top alternatives from logits, and their gradient;
- *   - a few rows times a 4-bit weight matrix with group scales.
+ *   - a few rows times a 4-bit weight matrix with group scales;
+ *   - linear attention with a decay for each head, on packed prompts and on one token per sequence;
+ *   - the next token drawn from logits; entries of a cache copied, moved and freed.
  *
  * Conventions: those of selscan.h (status codes, device pointers owned by the caller, work only
  * enqueued on `stream`, nothing allocated or kept by the library, host validation before any HIP
@@ -208,6 +210,80 @@ int token_logprobs_bwd(const void *logits, int64_t logits_stride, const int64_t 
 int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *scales, const void *zeros,
               const float *bias, void *y, int64_t rows, int64_t n, int64_t k, int64_t group, int io_dtype,
               void *stream);
+
+/*
+ * linear_attn_packed_fwd - linear attention with a decay for each head, on packed prompts (cu_seqlens, slots and carry as
+ * above).  Each head has a state S [dk][dv]; for token t of a sequence
+ *     S_t = exp(log_decay[t][h]) S_{t-1} + k_t v_t^T,   out[t][h] = scale * q_t^T S_t,
+ * with q and k of the head's group: heads / groups heads one after another share them.
+ *   q, k       : [tokens][groups][dk] io_dtype, row strides q_stride and k_stride (of a token)
+ *   v          : [tokens][heads][dv] io_dtype, row stride v_stride;  out : [tokens][heads][dv], contiguous
+ *   log_decay  : [tokens][heads] fp32, row stride decay_stride; decay_stride 0: one row for all tokens (a fixed decay for
+ *                each head).  Usually <= 0; -infinity clears the state before the token's own product is added (the
+ *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow.
+ *   state      : [nslots][heads][dk][dv] fp32, 16-byte aligned, nullable (no cache); in place
+ *   dk         : 1..256, dv : 1..1024, heads a multiple of groups (SELSCAN_E_UNSUPPORTED, SELSCAN_E_SHAPE); row strides at
+ *                most 2^26 (SELSCAN_E_UNSUPPORTED)
+ *   max_seqlen : the longest sequence's length, or any bound on it (tokens if unknown); speed only
+ *   workspace  : linear_attn_packed_workspace_bytes(...) bytes, 16-byte aligned (0 where the heads of the sequences fill
+ *                the chip: NULL will do).  Where it is not 0, a long sequence is read in segments side by side.
+ */
+int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, const float *log_decay, int64_t decay_stride, float scale,
+                           const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *carry, float *state, void *out,
+                           int64_t tokens, int64_t nseq, int64_t nslots, int64_t max_seqlen, int64_t heads, int64_t groups,
+                           int64_t dk, int64_t dv, int io_dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t linear_attn_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t heads, int64_t dk,
+                                          int64_t dv);
+
+/*
+ * linear_attn_step - one token for each of `rows` running sequences: the call above with every sequence one token long,
+ * carried, and row r on cache entry slots[r] (NULL: r, which needs nslots >= rows).  A row whose slot is outside
+ * [0, nslots) starts from zeros and keeps nothing.
+ */
+int linear_attn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                     const float *log_decay, int64_t decay_stride, float scale, const int32_t *slots, float *state,
+                     void *out, int64_t rows, int64_t nslots, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                     int io_dtype, void *stream);
+
+/*
+ * token_sample - draws a token from each row of logits x, given a number u in [0, 1) for each.  With T the temperature and m
+ * the row's largest logit, a token has weight exp((x - m) / T).  Of the tokens (largest logit first, equal ones by index) stay
+ *     the first top_k (0: all);  of these the fewest whose weights reach top_p of their sum (1: all; at least one);
+ *     and only those of weight min_p and more (the largest has weight 1).
+ * The token drawn is the first of those that stay, in the order of their indices, at which the sum of weights passes u
+ * times the whole.  T = 0: the largest logit.
+ *   logits  : [rows][vocab] io_dtype, row stride logits_stride;  uniform : [rows] fp32
+ *   temperature, top_p, min_p : [rows] fp32, top_k : [rows] int32, for each row; or NULL, and the value after it is every
+ *             row's: temperature >= 0 and finite, top_k >= 0, top_p and min_p in [0, 1] (SELSCAN_E_UNSUPPORTED).  In the
+ *             arrays, which the host does not see, a temperature that is not > 0 counts as 0, a top_k below 0 as 0, a top_p
+ *             or min_p outside [0, 1] as the nearer end, a NaN of them as no limit.  A u outside [0, 1) counts as the nearer
+ *             end, a NaN as 0.
+ *   token   : [rows] int64
+ *   logprob : [rows] fp32, the log of the token's weight over the weights of all that stay
+ *   kept    : [rows] int32, how many tokens stay
+ *   vocab   : 1..2^21 (SELSCAN_E_SHAPE, SELSCAN_E_UNSUPPORTED)
+ * Weights are whole multiples of 2^-45 (for vocab 2^17; of vocab 2^-62, rounded up to a power of 2, and at least 2^-52), summed as whole numbers: what is drawn does not
+ * depend on how a row is split.  A logit of -infinity never stays.  A row of nothing else has token -1, logprob -infinity and
+ * kept 0; a row with a NaN or +infinity has token -1, logprob NaN and kept 0.
+ */
+int token_sample(const void *logits, int64_t logits_stride, const float *uniform, const float *temperature,
+                 float temperature_all, const int32_t *top_k, int top_k_all, const float *top_p, float top_p_all,
+                 const float *min_p, float min_p_all, int64_t *token, float *logprob, int32_t *kept, int64_t rows,
+                 int64_t vocab, int io_dtype, void *stream);
+
+/*
+ * cache_entries_copy - entry dst[i] of every one of `ncaches` caches becomes what entry src[i] was before the call, for all i
+ * at once: entries are forked (one src for several dst), moved and exchanged.  A src outside [0, nslots) stands for zeros
+ * (the entry is freed); a dst outside [0, nslots) is passed over.  The dst of one call must differ from one another (if two
+ * are alike, that entry's content is unspecified).
+ *   caches, entry_bytes : host arrays of ncaches device addresses (any alignment) and of the bytes of an entry of each; a
+ *              cache is nslots entries one after another.  The caches may not overlap one another.
+ *   src, dst : [n] int32, n at most 16384 (SELSCAN_E_UNSUPPORTED)
+ *   entry_bytes at most 2^32; entries of all caches together within one launch (SELSCAN_E_UNSUPPORTED)
+ */
+int cache_entries_copy(void *const *caches, const int64_t *entry_bytes, int64_t ncaches, const int32_t *src,
+                       const int32_t *dst, int64_t n, int64_t nslots, void *stream);
 
 int selscan_lm_abi_version(void);
 /* text of the calling thread's most recent launch that the HIP runtime rejected */

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("selscan_fwd.hip", "selscan_bwd.hip", "selscan_conv.hip")]
 OUT = os.path.join(PKG, "libselscan.so")
-LM_SRCS = [os.path.join(CSRC, f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logprobs.hip", "lm_w4.hip")]
+LM_SRCS = [os.path.join(CSRC, f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logprobs.hip", "lm_w4.hip", "lm_linattn.hip",
+                                               "lm_sample.hip", "lm_cache.hip")]
 LM_OUT = os.path.join(PKG, "libselscan_lm.so")
 BINDING_SRC = os.path.join(CSRC, "lm_binding.cpp")  # its binding to torch tensors (host code, linked to it)
 BINDING_OUT = os.path.join(PKG, "_lm_binding.so")

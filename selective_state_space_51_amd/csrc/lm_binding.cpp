@@ -8,11 +8,13 @@
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
 #include <string>
 #include <tuple>
+#include <vector>
 
 #include "selscan_lm.h"
 
@@ -388,6 +390,134 @@ Tensor matvec(const Tensor &x, const Tensor &q, const Tensor &scales, const Opt 
     return out;
 }
 
+// address and row stride of [rows][n][d] whose rows (tokens) are contiguous
+Rows heads_of(const char *name, const Tensor &t, at::ScalarType dt) {
+    want_here(name, t);
+    want_dtype(name, t, dt);
+    const int64_t rows = t.size(0), n = t.size(1), d = t.size(2), width = n * d;
+    if ((d > 1 && t.stride(2) != 1) || (n > 1 && d > 0 && t.stride(1) != d))
+        throw py::value_error(std::string("the rows of ") + name + " must be contiguous");
+    const int64_t stride = rows > 1 ? t.stride(0) : width;
+    if (stride < width) throw py::value_error(std::string("the rows of ") + name + " overlap");
+    return {t.numel() ? t.data_ptr() : nullptr, stride};
+}
+
+struct Heads {
+    int64_t rows, heads, groups, dk, dv;
+};
+Heads heads_shapes(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &decay, const Opt &state) {
+    if (q.dim() != 3) throw py::value_error("q must have three dimensions");
+    if (v.dim() != 3) throw py::value_error("v must have three dimensions");
+    const Heads s{q.size(0), v.size(1), q.size(1), q.size(2), v.size(2)};
+    want_shape("k", k, {s.rows, s.groups, s.dk});
+    want_shape("v", v, {s.rows, s.heads, s.dv});
+    if (decay.dim() == 1) want_shape("log_decay", decay, {s.heads});
+    else want_shape("log_decay", decay, {s.rows, s.heads});
+    if (s.heads > 0 && (s.groups == 0 || s.heads % s.groups))
+        throw py::value_error(std::to_string(s.groups) + " groups of q and k do not divide " + std::to_string(s.heads) + " heads");
+    if (state) {
+        if (state->dim() != 4) throw py::value_error("state must have four dimensions");
+        want_shape("state", *state, {state->size(0), s.heads, s.dk, s.dv});
+    }
+    return s;
+}
+// one row for all tokens: stride 0
+Rows decay_rows(const Tensor &decay) {
+    if (decay.dim() == 1) return {(void *)f32("log_decay", decay), 0};
+    return rows_of("log_decay", decay, at::kFloat);
+}
+
+Tensor linattn_packed(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &decay, const Tensor &cu, const Opt &state,
+                      double scale, const Opt &slots, const Opt &carry, std::optional<int64_t> max_seqlen, const Opt &out_,
+                      const Opt &ws_) {
+    const Heads s = heads_shapes(q, k, v, decay, state);
+    const Launch l(q);
+    const int io = io_code(q);
+    const at::ScalarType dt = q.scalar_type();
+    const Packed p = packed(cu, slots, carry, state);
+    const int64_t longest = max_seqlen.value_or(s.rows);
+    const Tensor out = out_ ? *out_ : empty({s.rows, s.heads, s.dv}, q, dt);
+    want_shape("out", out, {s.rows, s.heads, s.dv});
+    const Workspace ws = workspace(linear_attn_packed_workspace_bytes(s.rows, p.nseq, longest, s.heads, s.dk, s.dv), ws_, q);
+    const Rows qr = heads_of("q", q, dt), kr = heads_of("k", k, dt), vr = heads_of("v", v, dt), dr = decay_rows(decay);
+    check(linear_attn_packed_fwd(qr.p, qr.stride, kr.p, kr.stride, vr.p, vr.stride, (const float *)dr.p, dr.stride, (float)scale,
+                                 p.cu, p.slots, p.carry, ptr<float>("state", state, at::kFloat), ptr("out", out, dt), s.rows,
+                                 p.nseq, p.nslots, longest, s.heads, s.groups, s.dk, s.dv, io, ws.p, ws.bytes, l.stream),
+          "linear_attn_packed_fwd");
+    return out;
+}
+
+Tensor linattn_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &decay, const Tensor &state, double scale,
+                    const Opt &slots, const Opt &out_) {
+    const Heads s = heads_shapes(q, k, v, decay, state);
+    want_shape("slots", slots, {s.rows});
+    const Launch l(q);
+    const int io = io_code(q);
+    const at::ScalarType dt = q.scalar_type();
+    const Tensor out = out_ ? *out_ : empty({s.rows, s.heads, s.dv}, q, dt);
+    want_shape("out", out, {s.rows, s.heads, s.dv});
+    const Rows qr = heads_of("q", q, dt), kr = heads_of("k", k, dt), vr = heads_of("v", v, dt), dr = decay_rows(decay);
+    check(linear_attn_step(qr.p, qr.stride, kr.p, kr.stride, vr.p, vr.stride, (const float *)dr.p, dr.stride, (float)scale,
+                           ptr<const int32_t>("slots", slots, at::kInt), (float *)ptr("state", state, at::kFloat),
+                           ptr("out", out, dt), s.rows, state.size(0), s.heads, s.groups, s.dk, s.dv, io, l.stream),
+          "linear_attn_step");
+    return out;
+}
+
+// a setting of token_sample: a number for all rows, or a tensor of one for each
+struct Setting {
+    const void *p = nullptr;
+    double all = 0.;
+};
+Setting setting(const char *name, const py::object &o, int64_t rows, at::ScalarType dt) {
+    if (THPVariable_Check(o.ptr())) {
+        const Tensor t = o.cast<Tensor>();
+        want_shape(name, t, {rows});
+        return {ptr(name, t, dt), 0.};
+    }
+    return {nullptr, o.cast<double>()};
+}
+
+std::tuple<Tensor, Tensor, Tensor> sample(const Tensor &logits, const Tensor &uniform, const py::object &temperature,
+                                          const py::object &top_k, const py::object &top_p, const py::object &min_p) {
+    want_matrix("logits", logits);
+    const int64_t rows = logits.size(0), vocab = logits.size(1);
+    want_shape("uniform", uniform, {rows});
+    const Launch l(logits);
+    const int io = io_code(logits);
+    const Setting t = setting("temperature", temperature, rows, at::kFloat), k = setting("top_k", top_k, rows, at::kInt),
+                  p = setting("top_p", top_p, rows, at::kFloat), m = setting("min_p", min_p, rows, at::kFloat);
+    if (!(k.all >= 0 && k.all <= INT32_MAX && k.all == (double)(int)k.all)) throw py::value_error("top_k must be a whole number >= 0");
+    const Tensor token = empty({rows}, logits, at::kLong), lp = empty({rows}, logits, at::kFloat), kept = empty({rows}, logits, at::kInt);
+    const Rows xr = rows_of("logits", logits, logits.scalar_type());
+    check(token_sample(xr.p, xr.stride, f32("uniform", uniform), (const float *)t.p, (float)t.all, (const int32_t *)k.p, (int)k.all,
+                       (const float *)p.p, (float)p.all, (const float *)m.p, (float)m.all, (int64_t *)token.data_ptr(),
+                       (float *)lp.data_ptr(), (int32_t *)kept.data_ptr(), rows, vocab, io, l.stream),
+          "token_sample");
+    return {token, lp, kept};
+}
+
+void copy_entries(const std::vector<Tensor> &caches, const Tensor &src, const Tensor &dst) {
+    if (caches.empty()) return;
+    if (src.dim() != 1) throw py::value_error("src must be a vector");
+    const int64_t n = src.size(0);
+    want_shape("dst", dst, {n});
+    const Launch l(caches[0]);
+    std::vector<void *> at;
+    std::vector<int64_t> bytes;
+    at.reserve(caches.size()), bytes.reserve(caches.size());
+    if (caches[0].dim() < 1) throw py::value_error("a cache must have a dimension of entries");
+    const int64_t nslots = caches[0].size(0);
+    for (const Tensor &c : caches) {
+        if (c.dim() < 1 || c.size(0) != nslots) throw py::value_error("the caches must have the same number of entries, " + std::to_string(nslots));
+        at.push_back(ptr("a cache", c, c.scalar_type()));
+        bytes.push_back(nslots ? (int64_t)c.nbytes() / nslots : 0);
+    }
+    check(cache_entries_copy(at.data(), bytes.data(), (int64_t)at.size(), (const int32_t *)ptr("src", src, at::kInt),
+                             (const int32_t *)ptr("dst", dst, at::kInt), n, nslots, l.stream),
+          "cache_entries_copy");
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_lm_binding, m) {
@@ -400,4 +530,8 @@ PYBIND11_MODULE(_lm_binding, m) {
     m.def("token_logprobs_fwd", &logprobs_fwd);
     m.def("token_logprobs_bwd", &logprobs_bwd);
     m.def("w4_matvec", &matvec);
+    m.def("linear_attn_packed_fwd", &linattn_packed);
+    m.def("linear_attn_step", &linattn_step);
+    m.def("token_sample", &sample);
+    m.def("cache_entries_copy", &copy_entries);
 }

@@ -1,0 +1,134 @@
+// libselscan_lm - entries of a model's cache copied, moved and freed (cache_entries_copy of include/selscan_lm.h).
+// MI355X (gfx950).
+//
+// A workgroup takes CW pieces of 16 bytes of an entry of one cache, and all n pairs of entries: it reads those pieces of
+// every source, waits, and writes them to every destination.  No other workgroup touches these pieces, so that any set of
+// moves, rings among them, needs neither an order nor a second copy of the data.
+#include "lm_common.h"
+
+namespace {
+
+constexpr int kCaches = 128;  // caches of a launch (their addresses are kernel arguments)
+constexpr int64_t kMaxPairs = 16384, kMaxEntry = INT64_C(1) << 32;
+
+struct Cache {
+    char *p;
+    int64_t bytes;  // of an entry
+};
+struct CopyParams {
+    const int32_t *src, *dst;
+    int64_t nslots;
+    int n, ncaches;
+    uint32_t first[kCaches];  // workgroup
+    Cache c[kCaches];
+};
+
+struct __attribute__((packed, aligned(1))) Any16 {
+    uint32_t w[4];
+};
+
+// 16 bytes or, at an entry's end, the nb < 16 that are left
+__device__ __forceinline__ uint4 load_piece(const char *p, int nb) {
+    if (nb >= 16) {
+        const Any16 a = *(const Any16 *)p;
+        return make_uint4(a.w[0], a.w[1], a.w[2], a.w[3]);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+        if (i < nb) w[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_piece(char *p, int nb, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (nb >= 16) {
+        Any16 a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a.w[i] = w[i];
+        *(Any16 *)p = a;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+        if (i < nb) p[i] = (char)(w[i >> 2] >> (8 * (i & 3)));
+}
+
+// CW pieces wide, THREADS / CW pairs side by side, NR of them in each thread
+template <int THREADS, int CW, int NR>
+__global__ __launch_bounds__(THREADS) void copy_entries(CopyParams p) {
+    int lo = 0, n = p.ncaches;  // the last cache whose first workgroup is not after this one
+    while (n > 1) {
+        const int half = n >> 1;
+        if (p.first[lo + half] <= blockIdx.x) lo += half, n -= half;
+        else n = half;
+    }
+    const Cache c = p.c[lo];
+    const int64_t at = ((int64_t)(blockIdx.x - p.first[lo]) * CW + threadIdx.x % CW) * 16;
+    const int64_t left = c.bytes - at;
+    const int nb = left < 0 ? 0 : left < 16 ? (int)left : 16, pair = threadIdx.x / CW;
+    constexpr int PL = THREADS / CW;
+    uint4 v[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int i = r * PL + pair;
+        const int64_t s = i < p.n ? p.src[i] : -1;
+        v[r] = s >= 0 && s < p.nslots && nb > 0 ? load_piece(c.p + s * c.bytes + at, nb) : make_uint4(0, 0, 0, 0);
+    }
+    // every read of the workgroup has come back before any of its writes
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int i = r * PL + pair;
+        const int64_t d = i < p.n ? p.dst[i] : -1;
+        if (d >= 0 && d < p.nslots && nb > 0) store_piece(c.p + d * c.bytes + at, nb, v[r]);
+    }
+}
+
+}  // namespace
+
+extern "C" int cache_entries_copy(void *const *caches, const int64_t *entry_bytes, int64_t ncaches, const int32_t *src,
+                                  const int32_t *dst, int64_t n, int64_t nslots, void *stream) {
+    if (ncaches < 0 || n < 0 || nslots < 0) return SELSCAN_E_SHAPE;
+    if (n > kMaxPairs) return SELSCAN_E_UNSUPPORTED;
+    if (ncaches == 0 || n == 0 || nslots == 0) return SELSCAN_OK;
+    if (!caches || !entry_bytes || !src || !dst) return SELSCAN_E_NULL;
+    if (!span_aligned(src, 4) || !span_aligned(dst, 4)) return SELSCAN_E_ALIGN;
+    for (int64_t i = 0; i < ncaches; ++i) {
+        if (entry_bytes[i] < 0 || mul_size(nslots, entry_bytes[i]) < 0) return SELSCAN_E_SHAPE;
+        if (entry_bytes[i] > kMaxEntry) return SELSCAN_E_UNSUPPORTED;
+        if (entry_bytes[i] > 0 && !caches[i]) return SELSCAN_E_NULL;
+    }
+    const auto span = [&](int64_t i) { return Span{caches[i], (size_t)(nslots * entry_bytes[i])}; };
+    const Span s{src, (size_t)n * 4}, d{dst, (size_t)n * 4};
+    for (int64_t i = 0; i < ncaches; ++i) {
+        if (overlap(span(i), s) || overlap(span(i), d)) return SELSCAN_E_ALIAS;
+        for (int64_t j = 0; j < i; ++j)
+            if (overlap(span(i), span(j))) return SELSCAN_E_ALIAS;
+    }
+    void (*kernel)(CopyParams) = copy_entries<1024, 1, 16>;
+    int threads = 1024, cw = 1;
+    if (n <= 4) kernel = copy_entries<256, 64, 1>, threads = 256, cw = 64;
+    else if (n <= 32) kernel = copy_entries<256, 64, 8>, threads = 256, cw = 64;
+    else if (n <= 256) kernel = copy_entries<256, 16, 16>, threads = 256, cw = 16;
+    else if (n <= 1024) kernel = copy_entries<1024, 16, 16>, cw = 16;
+    else if (n <= 4096) kernel = copy_entries<1024, 4, 16>, cw = 4;
+    int64_t all = 0;
+    for (int64_t i = 0; i < ncaches; ++i) all += (entry_bytes[i] + 16 * cw - 1) / (16 * cw);
+    if (!grid_fits(all, threads)) return SELSCAN_E_UNSUPPORTED;
+    CopyParams p;
+    p.src = src, p.dst = dst, p.nslots = nslots, p.n = (int)n;
+    for (int64_t i0 = 0; i0 < ncaches; i0 += kCaches) {
+        int64_t blocks = 0;
+        p.ncaches = 0;
+        for (int64_t i = i0; i < ncaches && i < i0 + kCaches; ++i) {
+            if (entry_bytes[i] == 0) continue;
+            p.first[p.ncaches] = (uint32_t)blocks;
+            p.c[p.ncaches++] = {(char *)caches[i], entry_bytes[i]};
+            blocks += (entry_bytes[i] + 16 * cw - 1) / (16 * cw);
+        }
+        if (blocks == 0) continue;
+        const int rc = enqueue(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), p, stream);
+        if (rc != SELSCAN_OK) return rc;
+    }
+    return SELSCAN_OK;
+}

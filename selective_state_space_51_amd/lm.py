@@ -45,6 +45,11 @@ def _load():
     sig("token_logprobs_workspace_bytes", [i64, i64, ci], sz)
     sig("token_logprobs_bwd", [vp, i64] + [vp] * 5 + [cf, vp, i64, i64, ci, vp])
     sig("w4_matvec", [vp, i64] + [vp] * 5 + [i64] * 4 + [ci, vp])
+    sig("linear_attn_packed_fwd", [vp, i64] * 4 + [cf] + [vp] * 5 + [i64] * 8 + [ci, vp, sz, vp])
+    sig("linear_attn_packed_workspace_bytes", [i64] * 6, sz)
+    sig("linear_attn_step", [vp, i64] * 4 + [cf] + [vp] * 3 + [i64] * 6 + [ci, vp])
+    sig("token_sample", [vp, i64, vp, vp, cf, vp, ci, vp, cf, vp, cf] + [vp] * 3 + [i64, i64, ci, vp])
+    sig("cache_entries_copy", [vp, vp, i64, vp, vp, i64, i64, vp])
     sig("selscan_lm_abi_version", [])
     sig("selscan_lm_last_hip_error", [], ctypes.c_char_p)
     return lib
@@ -153,3 +158,41 @@ def w4_matvec(x, qweight, scales, zeros=None, group=128, bias=None, out=None, st
     high bits of byte i), weight (q - zero) * scale with scales bf16 and zeros uint8 (None: 8), [n, k // group]
     each; bias fp32 [n].  Returns [rows, n] in x's dtype."""
     return _run(stream, _C.w4_matvec, x, qweight, scales, zeros, group, bias, out)
+
+
+def linear_attn_packed_workspace_bytes(tokens: int, nseq: int, max_seqlen: int, heads: int, dk: int, dv: int) -> int:
+    return int(lm_lib.linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv))
+
+
+def linear_attn_packed_fwd(q, k, v, log_decay, cu_seqlens, state=None, scale=1.0, slots=None, carry=None, max_seqlen=None,
+                           out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head, on packed prompts: S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T and
+    out_t = scale q_t^T S_t.  q, k [tokens, groups, dk] (heads / groups heads one after another share them), v [tokens, heads, dv],
+    whose tokens may be strided; log_decay fp32 [tokens, heads], or [heads] for a fixed decay; cu_seqlens int32 [nseq + 1].
+    state fp32 [nslots, heads, dk, dv] is read for the sequences whose carry is set and updated in place for all, at entry
+    slots[s] (int32; None: s).  max_seqlen: the longest length or a bound on it (speed only).  Returns [tokens, heads, dv]."""
+    return _run(stream, _C.linear_attn_packed_fwd, q, k, v, log_decay, cu_seqlens, state, scale, slots, carry, max_seqlen, out,
+                workspace)
+
+
+def linear_attn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, stream=None):
+    """One token of linear attention for each row: q, k [rows, groups, dk], v [rows, heads, dv], log_decay [rows, heads] or
+    [heads]; state fp32 [nslots, heads, dk, dv] is updated in place at entry slots[r] (int32; None: r)."""
+    return _run(stream, _C.linear_attn_step, q, k, v, log_decay, state, scale, slots, out)
+
+
+def token_sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """Draws a token from softmax(logits / temperature), logits [rows, vocab], with the number in [0, 1) that uniform (fp32
+    [rows]) has for each row, among the top_k largest (0: all), of them the fewest that reach top_p of the probability, and
+    of them those at least min_p times as likely as the likeliest.  Each setting is a number or a tensor [rows] (fp32; top_k
+    int32); temperature 0 takes the largest logit.  Returns (token int64, logprob fp32 among those that stay, kept int32: how many stay); a
+    row without a finite logit, or with a NaN or +inf, has token -1 and kept 0."""
+    return _run(stream, _C.token_sample, logits, uniform, temperature, top_k, top_p, min_p)
+
+
+def cache_entries_copy(caches, src, dst, stream=None):
+    """Entry dst[i] of every cache (a tensor [nslots, ...], or a list of them with the same nslots and any types) becomes what
+    entry src[i] was, all at once and in place: forks, moves and exchanges.  src, dst int32 [n], n up to 16384; a src outside
+    [0, nslots) frees the entry (zeros), a dst outside is passed over."""
+    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    _run(stream, _C.cache_entries_copy, caches, src, dst)
