@@ -21,54 +21,390 @@ struct LaParams {
 // chunk's worth can be added and subtracted again.
 __device__ __forceinline__ float finite_decay(float g) { return g < -16384.f ? -16384.f : g; }
 
-// Packed prompts, token by token: 64 columns of a head's state in a workgroup, a quarter of their rows in each thread.
+typedef float F4 __attribute__((ext_vector_type(4)));
+typedef __bf16 B8 __attribute__((ext_vector_type(8)));
+typedef short I4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ F4 mma(B8 a, B8 b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ F4 mma(float a, float b, F4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// Waits out the longest of these products (16 passes of 4 clocks at most), for results that another block reads: the compiler
+// counts the clocks between a product and its reader along one path of those that join, not along the shortest.
+__device__ __forceinline__ void results_ready() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// 4 x 16 bf16 of LDS, one row of 4 adjacent columns from each lane's address (16 lanes: 4 rows of 4 such pieces), transposed:
+// lane i of 16 gets column i's 4 rows
+__device__ __forceinline__ I4 read_transposed(const uint16_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) I4 *)p);
+}
+__device__ __forceinline__ B8 join8(I4 a, I4 b) {
+    struct {
+        I4 a, b;
+    } u = {a, b};
+    return __builtin_bit_cast(B8, u);
+}
+__device__ __forceinline__ B8 pack8(const F4 &a, const F4 &b) {
+    const uint4 w = {Io<uint16_t>::to2(a[0], a[1]), Io<uint16_t>::to2(a[2], a[3]), Io<uint16_t>::to2(b[0], b[1]), Io<uint16_t>::to2(b[2], b[3])};
+    return __builtin_bit_cast(B8, w);
+}
+
+// A chunk of C tokens of one head, with G_t the sum of the log decays up to token t and S the state before it:
+//     out_t = scale (e^{G_t} q_t S + sum_{j <= t} e^{G_t - G_j} (q_t . k_j) v_j),
+//     S' = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
+// as products of matrices on the matrix cores.  A workgroup of four waves has 64 columns of the head's values; a wave keeps the 16
+// columns of S that are its own in registers from chunk to chunk, in the places in which the matrix cores leave a result.
+// bf16: these places are also those of an operand, if the 32 rows of a step are taken in the order in which two tiles hold
+// them: rows 4 g .. 4 g + 3 of both from lanes 16 g .. 16 g + 15.  So q and k lie in LDS in that order (store_piece), and S
+// never leaves the registers.
+template <typename T, int KB>
+struct Chunk {
+    static constexpr bool BF = sizeof(T) == 2;
+    static constexpr int C = BF || KB <= 2 ? 64 : 32, NT = C / 16;  // tokens, and tiles of 16 of them
+    static constexpr int D = 32 * KB;                               // rows of the state, padded
+    static constexpr int E = 16 / sizeof(T);                        // elements of 16 bytes
+    static constexpr int LQ = D + E, LV = 64 + E, LP = C + E;       // row strides in LDS
+    static constexpr int NQ = C * D / E / 256, NV = C * 64 / E / 256;  // 16-byte pieces of a thread
+    T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP];
+    float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
+    float fh, fl;              // 2^G_C in two parts
+    double total;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void la_tokens(LaParams p) {
-    __shared__ float kq[2][kMaxKeys];
-    __shared__ float part[4][64];
-    const int col = threadIdx.x & 63, quarter = threadIdx.x >> 6;
-    const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads;
-    const Segment g = whole_sequence(p.s, hs / p.heads);
-    const int c = vb * 64 + col, rows = (p.dk + 3) / 4;
-    const bool live = c < p.dv;
-    float *cache = p.state && g.slot >= 0 ? p.state + ((int64_t)g.slot * p.heads + h) * p.dk * p.dv : nullptr;
-    float S[kMaxKeys / 4];
-#pragma unroll
-    for (int i = 0; i < kMaxKeys / 4; ++i) {
-        const int d = quarter * rows + i;
-        S[i] = cache && g.carry && live && i < rows && d < p.dk ? cache[(int64_t)d * p.dv + c] : 0.f;
+struct __attribute__((packed, aligned(sizeof(T)))) Piece16 {
+    uint32_t w[4];
+};
+// elements [at, at + E) of a row of n, zeros past its end
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T *row, int at, int n) {
+    constexpr int E = 16 / sizeof(T);
+    if (at + E <= n) {
+        const Piece16<T> a = *(const Piece16<T> *)(row + at);
+        return make_uint4(a.w[0], a.w[1], a.w[2], a.w[3]);
     }
-    for (int t = 0; t < g.len; ++t) {
-        const int64_t row = g.t0 + t;
-        for (int d = threadIdx.x; d < kMaxKeys; d += 256) {
-            const int64_t at = (int64_t)(h / p.share) * p.dk + d;
-            kq[0][d] = d < p.dk ? Io<T>::f32(((const T *)p.k)[row * p.k_stride + at]) : 0.f;
-            kq[1][d] = d < p.dk ? Io<T>::f32(((const T *)p.q)[row * p.q_stride + at]) : 0.f;
-        }
-        __syncthreads();
-        const float e = __builtin_amdgcn_exp2f(finite_decay(p.decay[row * p.decay_stride + h]) * kLog2e);
-        const float x = live ? Io<T>::f32(((const T *)p.v)[row * p.v_stride + (int64_t)h * p.dv + c]) : 0.f;
-        float o = 0.f;
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kMaxKeys / 4; ++i) {
-            const int d = quarter * rows + i;
-            if (i < rows && d < p.dk) {
-                S[i] = fmaf(e, S[i], kq[0][d] * x);
-                o = fmaf(kq[1][d], S[i], o);
+    for (int e = 0; e < E; ++e) {
+        if (at + e >= n) continue;
+        if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(row[at + e]);
+        else w[e >> 1] |= (uint32_t)row[at + e] << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What a workgroup does: `n` tokens from row t0 on, outputs or only the state.
+struct LaPiece {
+    int t0, n;
+    bool outputs;
+};
+
+template <typename T, int KB>
+__device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Chunk<T, KB> &m, int h, int c0, F4 (&S)[2 * KB],
+                                         double *total) {
+    typedef Chunk<T, KB> M;
+    constexpr int C = M::C, NT = M::NT, E = M::E;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, g = lane >> 4;
+    const int group = h / p.share;
+    const T *q = (const T *)p.q + w.t0 * p.q_stride + (int64_t)group * p.dk;
+    const T *k = (const T *)p.k + w.t0 * p.k_stride + (int64_t)group * p.dk;
+    const T *v = (const T *)p.v + w.t0 * p.v_stride + (int64_t)h * p.dv + c0;
+    const float *decay = p.decay + w.t0 * p.decay_stride + h;
+    T *out = (T *)p.out + ((int64_t)w.t0 * p.heads + h) * p.dv + c0;
+    const int nv = p.dv - c0 < 64 ? p.dv - c0 : 64;
+    uint4 qr[M::NQ], kr[M::NQ], vr[M::NV];
+    float gr = 0.f;
+    const auto fetch = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < M::NQ; ++i) {
+            const int at = tid + 256 * i, r = first + at / (M::D / E), c = at % (M::D / E) * E;
+            const bool on = r < w.n && c < p.dk;
+            if (w.outputs) qr[i] = on ? load_piece(q + r * p.q_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
+            kr[i] = on ? load_piece(k + r * p.k_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < M::NV; ++i) {
+            const int at = tid + 256 * i, r = first + at / (64 / E), c = at % (64 / E) * E;
+            vr[i] = r < w.n && c < nv ? load_piece(v + r * p.v_stride, c, nv) : make_uint4(0, 0, 0, 0);
+        }
+        gr = wave == 0 && lane < C && first + lane < w.n ? decay[(first + lane) * p.decay_stride] : 0.f;
+    };
+    const auto store_piece = [&](T *to, int at, uint4 x) {
+        const int r = at / (M::D / E), c = at % (M::D / E);
+        if constexpr (M::BF) {
+            // columns 8 c .. 8 c + 7: two pieces of 4, of tile T of the 32 and lane groups gg and gg + 1
+            const int s = c >> 2, tile = (c >> 1) & 1, gg = (c & 1) * 2;
+            T *row = to + r * M::LQ + 32 * s + 4 * (2 * gg + tile);
+            *(uint2 *)row = make_uint2(x.x, x.y);
+            *(uint2 *)(row + 8) = make_uint2(x.z, x.w);
+        } else {
+            *(uint4 *)(to + r * M::LQ + c * E) = x;
+        }
+    };
+    double sum = 0.;
+    if (w.n > 0) fetch(0);
+    for (int first = 0; first < w.n; first += C) {
+        lds_barrier();  // the chunk before is no longer read
+#pragma unroll
+        for (int i = 0; i < M::NQ; ++i) {
+            if (w.outputs) store_piece(m.q, tid + 256 * i, qr[i]);
+            store_piece(m.k, tid + 256 * i, kr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < M::NV; ++i) {
+            const int at = tid + 256 * i;
+            *(uint4 *)(m.v + at / (64 / E) * M::LV + at % (64 / E) * E) = vr[i];
+        }
+        if (wave == 0) {
+            // sums of up to 64 x 16384 whose differences count: 64 bits, then two parts of 32
+            double G = (double)finite_decay(gr) * 1.44269504088896340735992468100;
+            G += dpp_or_zero<0x111, 0xF>(G);
+            G += dpp_or_zero<0x112, 0xF>(G);
+            G += dpp_or_zero<0x114, 0xF>(G);
+            G += dpp_or_zero<0x118, 0xF>(G);
+            G += dpp_or_zero<0x142, 0xA>(G);
+            G += dpp_or_zero<0x143, 0xC>(G);
+            const int64_t b = __double_as_longlong(G);
+            const double all = __longlong_as_double((int64_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((int)b, 63));
+            if (lane < C) {
+                const float hi = (float)G;
+                m.gh[lane] = hi, m.gl[lane] = (float)(G - (double)hi);
+                m.w[lane] = __builtin_amdgcn_exp2f((float)(all - G));
+            }
+            const double f = exp2(all);
+            if (lane == 0) m.fh = (float)f, m.fl = (float)(f - (double)(float)f);
+            sum += all;
+        }
+        if (first + C < w.n) fetch(first + C);
+        lds_barrier();
+        if (w.outputs) {
+            // scores of key tile jt and query tile tt, keys down, so that a lane's four are adjacent in a row of p
+#pragma unroll
+            for (int i = 0; i < (NT * (NT + 1) / 2 + 3) / 4; ++i) {
+                int jt = wave + 4 * i, tt = 0;
+#pragma unroll
+                for (int t = 1; t < NT; ++t)
+                    if (jt >= t * (t + 1) / 2 && wave + 4 * i >= t * (t + 1) / 2) tt = t;
+                jt -= tt * (tt + 1) / 2;
+                if (wave + 4 * i < NT * (NT + 1) / 2) {
+                    const T *kp = m.k + (16 * jt + l) * M::LQ, *qp = m.q + (16 * tt + l) * M::LQ;
+                    F4 acc = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (M::BF) {
+#pragma unroll
+                        for (int s = 0; s < KB; ++s) acc = mma(*(const B8 *)(kp + 32 * s + 8 * g), *(const B8 *)(qp + 32 * s + 8 * g), acc);
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < 2 * KB; ++d) {
+                            const F4 a = *(const F4 *)(kp + 16 * d + 4 * g), b = *(const F4 *)(qp + 16 * d + 4 * g);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc = mma(a[r], b[r], acc);
+                        }
+                    }
+                    const int t = 16 * tt + l, j = 16 * jt + 4 * g;
+                    const float th = m.gh[t], tl = m.gl[t];
+                    const F4 jh = *(const F4 *)(m.gh + j), jl = *(const F4 *)(m.gl + j);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = __builtin_amdgcn_exp2f((th - jh[r]) + (tl - jl[r]));
+                        acc[r] = j + r <= t ? acc[r] * e : 0.f;
+                    }
+                    T *to = m.p + t * M::LP + j;
+                    if constexpr (M::BF) {
+                        *(uint2 *)to = make_uint2(Io<T>::to2(acc[0], acc[1]), Io<T>::to2(acc[2], acc[3]));
+                        if (jt == tt && !(tt & 1)) *(uint2 *)(to + 16) = make_uint2(0, 0);  // the other half of a step of 32
+                    } else {
+                        *(F4 *)to = acc;
+                    }
+                }
             }
         }
-        part[quarter][col] = o;
-        __syncthreads();
-        if (quarter == 0 && live)
-            ((T *)p.out)[(row * p.heads + h) * p.dv + c] =
-                Io<T>::to(p.scale * (part[0][col] + part[1][col] + part[2][col] + part[3][col]));
-    }
-    if (!cache || !live) return;
+        // this wave's columns of the values: lane l has column l; bf16: 8 rows (tokens) of each step of 32, fp32: 4 of each 16
+        B8 vf[M::BF ? C / 32 : 1];
+        float vx[M::BF ? 1 : NT][4];
+        const int vrow = 8 * g + (l >> 2), vcol = 16 * wave + 4 * (l & 3);
+        const auto read_values = [&] {
+            if constexpr (M::BF) {
 #pragma unroll
-    for (int i = 0; i < kMaxKeys / 4; ++i) {
-        const int d = quarter * rows + i;
-        if (i < rows && d < p.dk) cache[(int64_t)d * p.dv + c] = S[i];
+                for (int s = 0; s < C / 32; ++s)
+                    vf[s] = join8(read_transposed(m.v + (32 * s + vrow) * M::LV + vcol), read_transposed(m.v + (32 * s + vrow + 4) * M::LV + vcol));
+            } else {
+#pragma unroll
+                for (int s = 0; s < NT; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) vx[s][r] = m.v[(16 * s + 4 * g + r) * M::LV + 16 * wave + l];
+            }
+        };
+        if (w.outputs) {
+            read_values();
+            // A score of 0 (a later token's) times a value that is no number would reach the tokens before it: such values
+            // are taken out of the product and added one by one.
+            bool odd;
+            {
+                float z = 0.f;
+                if constexpr (M::BF) {
+#pragma unroll
+                    for (int i = 0; i < C / 4; ++i) z = fmaf((float)vf[i >> 3][i & 7], 0.f, z);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C / 4; ++i) z = fmaf(vx[i >> 2][i & 3], 0.f, z);
+                }
+                odd = __any(z != z);
+                if (odd) {
+                    if constexpr (M::BF) {
+#pragma unroll
+                        for (int i = 0; i < C / 4; ++i)
+                            if (!(fabsf((float)vf[i >> 3][i & 7]) < INFINITY)) vf[i >> 3][i & 7] = (__bf16)0.f;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C / 4; ++i)
+                            if (!(fabsf(vx[i >> 2][i & 3]) < INFINITY)) vx[i >> 2][i & 3] = 0.f;
+                    }
+                }
+            }
+            lds_barrier();  // the scores are there
+            B8 sf[M::BF ? KB : 1];
+            if constexpr (M::BF) {
+#pragma unroll
+                for (int s = 0; s < KB; ++s) sf[s] = pack8(S[2 * s], S[2 * s + 1]);
+            }
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+                const int t = 16 * tt + l;
+                const T *qp = m.q + t * M::LQ, *pp = m.p + t * M::LP;
+                F4 o = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (M::BF) {
+#pragma unroll
+                    for (int s = 0; s < KB; ++s) o = mma(sf[s], *(const B8 *)(qp + 32 * s + 8 * g), o);
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 2 * KB; ++d) {
+                        const F4 b = *(const F4 *)(qp + 16 * d + 4 * g);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o = mma(S[d][r], b[r], o);
+                    }
+                }
+                o *= __builtin_amdgcn_exp2f(m.gh[t] + m.gl[t]);
+                if constexpr (M::BF) {
+#pragma unroll
+                    for (int s = 0; s <= tt / 2; ++s) o = mma(vf[s], *(const B8 *)(pp + 32 * s + 8 * g), o);
+                } else {
+#pragma unroll
+                    for (int s = 0; s <= tt; ++s) {
+                        const F4 b = *(const F4 *)(pp + 16 * s + 4 * g);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o = mma(vx[s][r], b[r], o);
+                    }
+                }
+                // (before the branch: a result of the matrix cores is read in the block that makes it)
+                o *= p.scale;
+                if (odd) {
+                    for (int j = 0; j <= t; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = Io<T>::f32(m.v[j * M::LV + 16 * wave + 4 * g + r]);
+                            if (!(fabsf(x) < INFINITY)) o[r] = fmaf(Io<T>::f32(pp[j]) * p.scale, x, o[r]);
+                        }
+                }
+                if (first + t < w.n) {
+                    T *to = out + (int64_t)(first + t) * p.heads * p.dv + 16 * wave + 4 * g;
+                    const int left = nv - 16 * wave - 4 * g;
+                    if (left >= 4) {
+                        struct __attribute__((packed, aligned(sizeof(T)))) {
+                            uint32_t x[sizeof(T)];
+                        } u;
+                        if constexpr (M::BF) u.x[0] = Io<T>::to2(o[0], o[1]), u.x[1] = Io<T>::to2(o[2], o[3]);
+                        else u.x[0] = __float_as_uint(o[0]), u.x[1] = __float_as_uint(o[1]), u.x[2] = __float_as_uint(o[2]), u.x[3] = __float_as_uint(o[3]);
+                        *(decltype(u) *)to = u;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 3; ++r)
+                            if (r < left) to[r] = Io<T>::to(o[r]);
+                    }
+                }
+            }
+        }
+        // the state
+        read_values();
+        const float fh = m.fh, fl = m.fl;
+#pragma unroll
+        for (int d = 0; d < 2 * KB; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[d][r] = fmaf(S[d][r], fh, S[d][r] * fl);
+        if constexpr (M::BF) {
+            // k is exact, a weighted value goes in as three bf16 parts whose sum it is
+            B8 part[C / 32][3];
+#pragma unroll
+            for (int s = 0; s < C / 32; ++s) {
+                F4 x[2] = {*(const F4 *)(m.w + 32 * s + 8 * g), *(const F4 *)(m.w + 32 * s + 8 * g + 4)};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] *= (float)vf[s][e];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    part[s][i] = pack8(x[0], x[1]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] -= (float)part[s][i][e];
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < 2 * KB; ++d) {
+                const T *kp = m.k + vrow * M::LQ + 32 * (d >> 1) + 4 * (2 * (l & 3) + (d & 1));
+#pragma unroll
+                for (int s = 0; s < C / 32; ++s) {
+                    const B8 a = join8(read_transposed(kp + 32 * s * M::LQ), read_transposed(kp + (32 * s + 4) * M::LQ));
+#pragma unroll
+                    for (int i = 2; i >= 0; --i) S[d] = mma(a, part[s][i], S[d]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NT; ++s) {
+                const F4 x = *(const F4 *)(m.w + 16 * s + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) vx[s][r] *= x[r];
+            }
+#pragma unroll
+            for (int d = 0; d < 2 * KB; ++d)
+#pragma unroll
+                for (int s = 0; s < NT; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[d] = mma(m.k[(16 * s + 4 * g + r) * M::LQ + 16 * d + l], vx[s][r], S[d]);
+        }
+        results_ready();
     }
+    *total = sum;
+}
+
+// Packed prompts.  A workgroup has 64 columns of a head's values and a whole sequence of one of its segments.
+template <typename T, int KB>
+__global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
+    __shared__ __attribute__((aligned(16))) Chunk<T, KB> m;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, gq = lane >> 4;
+    const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads;
+    const Segment g = whole_sequence(p.s, hs / p.heads);
+    const int c0 = vb * 64, c = c0 + 16 * wave + l;
+    float *cache = p.state && g.slot >= 0 ? p.state + ((int64_t)g.slot * p.heads + h) * p.dk * p.dv + c : nullptr;
+    F4 S[2 * KB];
+#pragma unroll
+    for (int d = 0; d < 2 * KB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * d + 4 * gq + r;
+            S[d][r] = cache && g.carry && c < p.dv && row < p.dk ? cache[(int64_t)row * p.dv] : 0.f;
+        }
+    double total;
+    la_piece<T, KB>(p, {g.t0, g.len, true}, m, h, c0, S, &total);
+    if (!cache || c >= p.dv) return;
+#pragma unroll
+    for (int d = 0; d < 2 * KB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * d + 4 * gq + r;
+            if (row < p.dk) cache[(int64_t)row * p.dv] = S[d][r];
+        }
 }
 
 // One token per sequence: 4 x CG columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in
@@ -241,7 +577,11 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
     const LaParams p = la_params(a, 64);
     const int64_t per = heads * p.vblocks;
     if (mul_size(nseq, per) < 0 || !grid_fits(nseq * per, 256)) return SELSCAN_E_UNSUPPORTED;
-    return enqueue(io_dtype == SELSCAN_BF16 ? la_tokens<uint16_t> : la_tokens<float>, dim3((unsigned)(nseq * per)), dim3(256), p, stream);
+    void (*kernel)(LaParams) = nullptr;
+#define PICK(T) (dk <= 32 ? la_packed<T, 1> : dk <= 64 ? la_packed<T, 2> : dk <= 128 ? la_packed<T, 4> : la_packed<T, 8>)
+    kernel = io_dtype == SELSCAN_BF16 ? PICK(uint16_t) : PICK(float);
+#undef PICK
+    return enqueue(kernel, dim3((unsigned)(nseq * per)), dim3(256), p, stream);
 }
 
 int linear_attn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
