@@ -223,7 +223,7 @@ int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *
  *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow.
  *   state      : [nslots][heads][dk][dv] fp32, 16-byte aligned, nullable (no cache); in place
  *   dk         : 1..256, dv : 1..1024, heads a multiple of groups (SELSCAN_E_UNSUPPORTED, SELSCAN_E_SHAPE); row strides at
- *                most 2^26 (SELSCAN_E_UNSUPPORTED)
+ *                most 2^23 (SELSCAN_E_UNSUPPORTED)
  *   max_seqlen : the longest sequence's length, or any bound on it (tokens if unknown); speed only
  *   workspace  : linear_attn_packed_workspace_bytes(...) bytes, 16-byte aligned (0 where the heads of the sequences fill
  *                the chip: NULL will do).  Where it is not 0, a long sequence is read in segments side by side.

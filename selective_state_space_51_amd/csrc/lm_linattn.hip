@@ -15,6 +15,12 @@ struct LaParams {
     int64_t q_stride, k_stride, v_stride, decay_stride;
     int heads, share, dk, dv, vblocks;  // share: heads of a group
     float scale;
+    // sequences in segments of `size` tokens: what each entry holds (the state at the end of a segment that another
+    // follows, from zero but for a sequence's first), and the sum of its log decays (base 2)
+    float *seg;    // [entries][heads][dk][dv]
+    double *total; // [entries][heads]
+    int size, entries;
+    FastDiv dsize;
 };
 
 // A log decay as it is used: one of -infinity, or below any whose exponential is not 0 in fp32, is a number of which a
@@ -57,21 +63,24 @@ __device__ __forceinline__ B8 pack8(const F4 &a, const F4 &b) {
 //     S' = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
 // as products of matrices on the matrix cores.  A workgroup of four waves has 64 columns of the head's values; a wave keeps the 16
 // columns of S that are its own in registers from chunk to chunk, in the places in which the matrix cores leave a result.
-// bf16: these places are also those of an operand, if the 32 rows of a step are taken in the order in which two tiles hold
-// them: rows 4 g .. 4 g + 3 of both from lanes 16 g .. 16 g + 15.  So q and k lie in LDS in that order (store_piece), and S
-// never leaves the registers.
+// bf16: these places are also those of an operand, if of the 32 rows of a step two tiles hold rows 8 g .. 8 g + 3 and 8 g + 4 .. 8 g +
+// 7 in lanes 16 g .. 16 g + 15.  So S never leaves the registers: row_of says which row a place is.
 template <typename T, int KB>
 struct Chunk {
     static constexpr bool BF = sizeof(T) == 2;
     static constexpr int C = BF || KB <= 2 ? 64 : 32, NT = C / 16;  // tokens, and tiles of 16 of them
     static constexpr int D = 32 * KB;                               // rows of the state, padded
     static constexpr int E = 16 / sizeof(T);                        // elements of 16 bytes
-    static constexpr int LQ = D + E, LV = 64 + E, LP = C + E;       // row strides in LDS
+    // Row strides in LDS: rows start at different banks, for 16 rows of 16 bytes and (bf16) for 4 rows of 4 pieces 16 bytes apart
+    static constexpr int LQ = BF ? D + (KB >= 4 ? 40 : 8) : D + 4, LV = 64 + E, LP = C + E;
     static constexpr int NQ = C * D / E / 256, NV = C * 64 / E / 256;  // 16-byte pieces of a thread
     T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP];
     float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
     float fh, fl;              // 2^G_C in two parts
-    double total;
+    // row of the state that register r of tile d has in lanes 16 g .. 16 g + 15
+    static __device__ __forceinline__ int row_of(int d, int g, int r) {
+        return BF ? 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r : 16 * d + 4 * g + r;
+    }
 };
 
 template <typename T>
@@ -96,68 +105,98 @@ __device__ __forceinline__ uint4 load_piece(const T *row, int at, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Reads and writes of up to 64 rows through a buffer descriptor: what lies past the end of the last row reads as zeros and is not
+// written, so that the rows of a short chunk need no branch.  kNowhere: an offset that no buffer reaches.
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef unsigned int U4 __attribute__((ext_vector_type(4)));
+typedef unsigned int U2 __attribute__((ext_vector_type(2)));
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const T *at, int rows, int64_t stride, int width) {
+    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + width) * sizeof(T)) : 0u;
+    return __builtin_amdgcn_make_buffer_rsrc((void *)at, 0, bytes, 0x00027000);
+}
+
 // What a workgroup does: `n` tokens from row t0 on, outputs or only the state.
 struct LaPiece {
     int t0, n;
     bool outputs;
 };
 
-template <typename T, int KB>
+// VEC: the heads' rows are whole 16-byte pieces that start at words.
+template <typename T, int KB, bool VEC>
 __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Chunk<T, KB> &m, int h, int c0, F4 (&S)[2 * KB],
                                          double *total) {
     typedef Chunk<T, KB> M;
-    constexpr int C = M::C, NT = M::NT, E = M::E;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, g = lane >> 4;
+    constexpr int C = M::C, NT = M::NT, E = M::E, PQ = M::D / E, PV = 64 / E, PAIRS = (NT * (NT + 1) / 2 + 3) / 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane & 15, g = lane >> 4;
     const int group = h / p.share;
     const T *q = (const T *)p.q + w.t0 * p.q_stride + (int64_t)group * p.dk;
     const T *k = (const T *)p.k + w.t0 * p.k_stride + (int64_t)group * p.dk;
     const T *v = (const T *)p.v + w.t0 * p.v_stride + (int64_t)h * p.dv + c0;
     const float *decay = p.decay + w.t0 * p.decay_stride + h;
-    T *out = (T *)p.out + ((int64_t)w.t0 * p.heads + h) * p.dv + c0;
+    const int64_t out_stride = (int64_t)p.heads * p.dv;
+    T *out = (T *)p.out + w.t0 * out_stride + (int64_t)h * p.dv + c0;
     const int nv = p.dv - c0 < 64 ? p.dv - c0 : 64;
     uint4 qr[M::NQ], kr[M::NQ], vr[M::NV];
     float gr = 0.f;
     const auto fetch = [&](int first) {
+        const int rows = w.n - first < C ? w.n - first : C;
+        const T *q1 = q + first * p.q_stride, *k1 = k + first * p.k_stride, *v1 = v + first * p.v_stride;
+        if constexpr (VEC) {
+            const __amdgpu_buffer_rsrc_t qb = rows_buffer(q1, rows, p.q_stride, p.dk), kb = rows_buffer(k1, rows, p.k_stride, p.dk),
+                                         vb = rows_buffer(v1, rows, p.v_stride, nv);
 #pragma unroll
-        for (int i = 0; i < M::NQ; ++i) {
-            const int at = tid + 256 * i, r = first + at / (M::D / E), c = at % (M::D / E) * E;
-            const bool on = r < w.n && c < p.dk;
-            if (w.outputs) qr[i] = on ? load_piece(q + r * p.q_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
-            kr[i] = on ? load_piece(k + r * p.k_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
-        }
+            for (int i = 0; i < M::NQ; ++i) {
+                const int r = (tid + 256 * i) / PQ, c = tid % PQ * E;  // (256 is whole rows)
+                const uint32_t qa = c < p.dk ? (uint32_t)(r * (int)p.q_stride + c) * sizeof(T) : kNowhere;
+                const uint32_t ka = c < p.dk ? (uint32_t)(r * (int)p.k_stride + c) * sizeof(T) : kNowhere;
+                if (w.outputs) qr[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(qb, qa, 0, 0));
+                kr[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(kb, ka, 0, 0));
+            }
 #pragma unroll
-        for (int i = 0; i < M::NV; ++i) {
-            const int at = tid + 256 * i, r = first + at / (64 / E), c = at % (64 / E) * E;
-            vr[i] = r < w.n && c < nv ? load_piece(v + r * p.v_stride, c, nv) : make_uint4(0, 0, 0, 0);
-        }
-        gr = wave == 0 && lane < C && first + lane < w.n ? decay[(first + lane) * p.decay_stride] : 0.f;
-    };
-    const auto store_piece = [&](T *to, int at, uint4 x) {
-        const int r = at / (M::D / E), c = at % (M::D / E);
-        if constexpr (M::BF) {
-            // columns 8 c .. 8 c + 7: two pieces of 4, of tile T of the 32 and lane groups gg and gg + 1
-            const int s = c >> 2, tile = (c >> 1) & 1, gg = (c & 1) * 2;
-            T *row = to + r * M::LQ + 32 * s + 4 * (2 * gg + tile);
-            *(uint2 *)row = make_uint2(x.x, x.y);
-            *(uint2 *)(row + 8) = make_uint2(x.z, x.w);
+            for (int i = 0; i < M::NV; ++i) {
+                const int r = (tid + 256 * i) / PV, c = tid % PV * E;
+                const uint32_t va = c < nv ? (uint32_t)(r * (int)p.v_stride + c) * sizeof(T) : kNowhere;
+                vr[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(vb, va, 0, 0));
+            }
         } else {
-            *(uint4 *)(to + r * M::LQ + c * E) = x;
+#pragma unroll
+            for (int i = 0; i < M::NQ; ++i) {
+                const int r = (tid + 256 * i) / PQ, c = tid % PQ * E;
+                const bool on = r < rows && c < p.dk;
+                if (w.outputs) qr[i] = on ? load_piece(q1 + r * p.q_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
+                kr[i] = on ? load_piece(k1 + r * p.k_stride, c, p.dk) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < M::NV; ++i) {
+                const int r = (tid + 256 * i) / PV, c = tid % PV * E;
+                vr[i] = r < rows && c < nv ? load_piece(v1 + r * p.v_stride, c, nv) : make_uint4(0, 0, 0, 0);
+            }
         }
+        if (wave == 0) gr = lane < rows ? decay[(first + lane) * p.decay_stride] : 0.f;
     };
+    // tiles of the scores that are this wave's: pair i is key tile jt and query tile tt, jt <= tt
+    const auto pair_of = [&](int i, int &jt, int &tt) {
+        const int at = wave + 4 * i;
+        tt = 0;
+#pragma unroll
+        for (int t = 1; t < NT; ++t) tt = at >= t * (t + 1) / 2 ? t : tt;
+        jt = at - tt * (tt + 1) / 2;
+        return at < NT * (NT + 1) / 2;
+    };
+    const int vrow = 8 * g + (l >> 2), vcol = 16 * wave + 4 * (l & 3);  // of a transposed read
     double sum = 0.;
     if (w.n > 0) fetch(0);
     for (int first = 0; first < w.n; first += C) {
         lds_barrier();  // the chunk before is no longer read
+        T *to = m.k + tid / PQ * M::LQ + tid % PQ * E, *qto = m.q + tid / PQ * M::LQ + tid % PQ * E;
 #pragma unroll
         for (int i = 0; i < M::NQ; ++i) {
-            if (w.outputs) store_piece(m.q, tid + 256 * i, qr[i]);
-            store_piece(m.k, tid + 256 * i, kr[i]);
+            if (w.outputs) *(uint4 *)(qto + i * (256 / PQ) * M::LQ) = qr[i];
+            *(uint4 *)(to + i * (256 / PQ) * M::LQ) = kr[i];
         }
 #pragma unroll
-        for (int i = 0; i < M::NV; ++i) {
-            const int at = tid + 256 * i;
-            *(uint4 *)(m.v + at / (64 / E) * M::LV + at % (64 / E) * E) = vr[i];
-        }
+        for (int i = 0; i < M::NV; ++i) *(uint4 *)(m.v + (tid / PV + i * (256 / PV)) * M::LV + tid % PV * E) = vr[i];
         if (wave == 0) {
             // sums of up to 64 x 16384 whose differences count: 64 bits, then two parts of 32
             double G = (double)finite_decay(gr) * 1.44269504088896340735992468100;
@@ -182,15 +221,11 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         if (first + C < w.n) fetch(first + C);
         lds_barrier();
         if (w.outputs) {
-            // scores of key tile jt and query tile tt, keys down, so that a lane's four are adjacent in a row of p
+            // scores, keys down, so that a lane's four are adjacent in a row of p
 #pragma unroll
-            for (int i = 0; i < (NT * (NT + 1) / 2 + 3) / 4; ++i) {
-                int jt = wave + 4 * i, tt = 0;
-#pragma unroll
-                for (int t = 1; t < NT; ++t)
-                    if (jt >= t * (t + 1) / 2 && wave + 4 * i >= t * (t + 1) / 2) tt = t;
-                jt -= tt * (tt + 1) / 2;
-                if (wave + 4 * i < NT * (NT + 1) / 2) {
+            for (int i = 0; i < PAIRS; ++i) {
+                int jt, tt;
+                if (pair_of(i, jt, tt)) {
                     const T *kp = m.k + (16 * jt + l) * M::LQ, *qp = m.q + (16 * tt + l) * M::LQ;
                     F4 acc = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (M::BF) {
@@ -212,12 +247,12 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                         const float e = __builtin_amdgcn_exp2f((th - jh[r]) + (tl - jl[r]));
                         acc[r] = j + r <= t ? acc[r] * e : 0.f;
                     }
-                    T *to = m.p + t * M::LP + j;
+                    T *pto = m.p + t * M::LP + j;
                     if constexpr (M::BF) {
-                        *(uint2 *)to = make_uint2(Io<T>::to2(acc[0], acc[1]), Io<T>::to2(acc[2], acc[3]));
-                        if (jt == tt && !(tt & 1)) *(uint2 *)(to + 16) = make_uint2(0, 0);  // the other half of a step of 32
+                        *(uint2 *)pto = make_uint2(Io<T>::to2(acc[0], acc[1]), Io<T>::to2(acc[2], acc[3]));
+                        if (jt == tt && !(tt & 1)) *(uint2 *)(pto + 16) = make_uint2(0, 0);  // the other half of a step of 32
                     } else {
-                        *(F4 *)to = acc;
+                        *(F4 *)pto = acc;
                     }
                 }
             }
@@ -225,7 +260,6 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         // this wave's columns of the values: lane l has column l; bf16: 8 rows (tokens) of each step of 32, fp32: 4 of each 16
         B8 vf[M::BF ? C / 32 : 1];
         float vx[M::BF ? 1 : NT][4];
-        const int vrow = 8 * g + (l >> 2), vcol = 16 * wave + 4 * (l & 3);
         const auto read_values = [&] {
             if constexpr (M::BF) {
 #pragma unroll
@@ -243,26 +277,31 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
             // A score of 0 (a later token's) times a value that is no number would reach the tokens before it: such values
             // are taken out of the product and added one by one.
             bool odd;
-            {
+            if constexpr (M::BF) {
+                typedef unsigned short H2 __attribute__((ext_vector_type(2)));
+                H2 most = {0, 0};
+#pragma unroll
+                for (int s = 0; s < C / 32; ++s) {
+                    const U4 b = __builtin_bit_cast(U4, vf[s]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(H2, b[i] & 0x7FFF7FFFu));
+                }
+                odd = __any(most.x >= 0x7F80 || most.y >= 0x7F80);
+            } else {
                 float z = 0.f;
+#pragma unroll
+                for (int i = 0; i < C / 4; ++i) z = fmaf(vx[i >> 2][i & 3], 0.f, z);
+                odd = __any(z != z);
+            }
+            if (odd) {
                 if constexpr (M::BF) {
 #pragma unroll
-                    for (int i = 0; i < C / 4; ++i) z = fmaf((float)vf[i >> 3][i & 7], 0.f, z);
+                    for (int i = 0; i < C / 4; ++i)
+                        if (!(fabsf((float)vf[i >> 3][i & 7]) < INFINITY)) vf[i >> 3][i & 7] = (__bf16)0.f;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < C / 4; ++i) z = fmaf(vx[i >> 2][i & 3], 0.f, z);
-                }
-                odd = __any(z != z);
-                if (odd) {
-                    if constexpr (M::BF) {
-#pragma unroll
-                        for (int i = 0; i < C / 4; ++i)
-                            if (!(fabsf((float)vf[i >> 3][i & 7]) < INFINITY)) vf[i >> 3][i & 7] = (__bf16)0.f;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < C / 4; ++i)
-                            if (!(fabsf(vx[i >> 2][i & 3]) < INFINITY)) vx[i >> 2][i & 3] = 0.f;
-                    }
+                    for (int i = 0; i < C / 4; ++i)
+                        if (!(fabsf(vx[i >> 2][i & 3]) < INFINITY)) vx[i >> 2][i & 3] = 0.f;
                 }
             }
             lds_barrier();  // the scores are there
@@ -271,6 +310,9 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
 #pragma unroll
                 for (int s = 0; s < KB; ++s) sf[s] = pack8(S[2 * s], S[2 * s + 1]);
             }
+            const int rows = w.n - first < C ? w.n - first : C, left = nv - 16 * wave - 4 * g;
+            T *out1 = out + first * out_stride;
+            const __amdgpu_buffer_rsrc_t ob = rows_buffer(out1, rows, out_stride, nv);
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt) {
                 const int t = 16 * tt + l;
@@ -309,32 +351,26 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                             if (!(fabsf(x) < INFINITY)) o[r] = fmaf(Io<T>::f32(pp[j]) * p.scale, x, o[r]);
                         }
                 }
-                if (first + t < w.n) {
-                    T *to = out + (int64_t)(first + t) * p.heads * p.dv + 16 * wave + 4 * g;
-                    const int left = nv - 16 * wave - 4 * g;
-                    if (left >= 4) {
-                        struct __attribute__((packed, aligned(sizeof(T)))) {
-                            uint32_t x[sizeof(T)];
-                        } u;
-                        if constexpr (M::BF) u.x[0] = Io<T>::to2(o[0], o[1]), u.x[1] = Io<T>::to2(o[2], o[3]);
-                        else u.x[0] = __float_as_uint(o[0]), u.x[1] = __float_as_uint(o[1]), u.x[2] = __float_as_uint(o[2]), u.x[3] = __float_as_uint(o[3]);
-                        *(decltype(u) *)to = u;
-                    } else {
+                if constexpr (VEC) {
+                    const uint32_t at = left > 0 ? (uint32_t)(t * (int)out_stride + 16 * wave + 4 * g) * sizeof(T) : kNowhere;
+                    if constexpr (M::BF)
+                        __builtin_amdgcn_raw_buffer_store_b64((U2){Io<T>::to2(o[0], o[1]), Io<T>::to2(o[2], o[3])}, ob, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, o), ob, at, 0, 0);
+                } else if (t < rows) {
+                    T *oto = out1 + t * out_stride + 16 * wave + 4 * g;
 #pragma unroll
-                        for (int r = 0; r < 3; ++r)
-                            if (r < left) to[r] = Io<T>::to(o[r]);
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if (r < left) oto[r] = Io<T>::to(o[r]);
                 }
             }
         }
         // the state
         read_values();
         const float fh = m.fh, fl = m.fl;
-#pragma unroll
-        for (int d = 0; d < 2 * KB; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[d][r] = fmaf(S[d][r], fh, S[d][r] * fl);
         if constexpr (M::BF) {
+            // (the rounding of a chunk's factor, 2^-25 of a state, is far below a sum's with k and v in bf16)
+#pragma unroll
+            for (int d = 0; d < 2 * KB; ++d) S[d] *= fh;
             // k is exact, a weighted value goes in as three bf16 parts whose sum it is
             B8 part[C / 32][3];
 #pragma unroll
@@ -351,7 +387,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
             }
 #pragma unroll
             for (int d = 0; d < 2 * KB; ++d) {
-                const T *kp = m.k + vrow * M::LQ + 32 * (d >> 1) + 4 * (2 * (l & 3) + (d & 1));
+                const T *kp = m.k + vrow * M::LQ + 8 * (l & 3) + 32 * (d >> 1) + 4 * (d & 1);
 #pragma unroll
                 for (int s = 0; s < C / 32; ++s) {
                     const B8 a = join8(read_transposed(kp + 32 * s * M::LQ), read_transposed(kp + (32 * s + 4) * M::LQ));
@@ -360,6 +396,10 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                 }
             }
         } else {
+#pragma unroll
+            for (int d = 0; d < 2 * KB; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[d][r] = fmaf(S[d][r], fh, S[d][r] * fl);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
                 const F4 x = *(const F4 *)(m.w + 16 * s + 4 * g);
@@ -378,33 +418,95 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
     *total = sum;
 }
 
-// Packed prompts.  A workgroup has 64 columns of a head's values and a whole sequence of one of its segments.
-template <typename T, int KB>
+// Packed prompts.  A workgroup has 64 columns of a head's values and a whole sequence or one of its segments.  Segments take
+// two launches: the first (LAUNCH 0) reads every sequence's first segment for good, and of every other one that a further one
+// follows only what it makes of a state of zero; the states are joined; the second (LAUNCH 1) reads the segments but the first
+// from the states that they start from.
+template <typename T, int KB, bool VEC, int LAUNCH>
 __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
-    __shared__ __attribute__((aligned(16))) Chunk<T, KB> m;
+    typedef Chunk<T, KB> M;
+    __shared__ __attribute__((aligned(16))) M m;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, gq = lane >> 4;
-    const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads;
-    const Segment g = whole_sequence(p.s, hs / p.heads);
+    const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads, seg = hs / p.heads;
+    const bool split = p.seg != nullptr;
+    const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
+    const Segment g = LAUNCH == 1 ? find_segment<true>(p.s, seg, div, lane) : split ? find_segment(p.s, seg, div, lane) : whole_sequence(p.s, seg);
+    const int first = split ? g.j * p.size : 0;
+    if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
+    const bool last = !split || g.len - first <= p.size;
+    if (LAUNCH == 0 && g.j > 0 && last) return;
     const int c0 = vb * 64, c = c0 + 16 * wave + l;
-    float *cache = p.state && g.slot >= 0 ? p.state + ((int64_t)g.slot * p.heads + h) * p.dk * p.dv + c : nullptr;
+    const int64_t head = (int64_t)p.dk * p.dv;
+    float *cache = p.state && g.slot >= 0 ? p.state + ((int64_t)g.slot * p.heads + h) * head : nullptr;
+    const float *from = LAUNCH == 1 ? p.seg + ((int64_t)seg * p.heads + h) * head : g.j == 0 && g.carry ? cache : nullptr;
     F4 S[2 * KB];
 #pragma unroll
     for (int d = 0; d < 2 * KB; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = 16 * d + 4 * gq + r;
-            S[d][r] = cache && g.carry && c < p.dv && row < p.dk ? cache[(int64_t)row * p.dv] : 0.f;
+            const int row = M::row_of(d, gq, r);
+            S[d][r] = from && c < p.dv && row < p.dk ? from[row * p.dv + c] : 0.f;
         }
     double total;
-    la_piece<T, KB>(p, {g.t0, g.len, true}, m, h, c0, S, &total);
-    if (!cache || c >= p.dv) return;
+    la_piece<T, KB, VEC>(p, {g.t0 + first, last ? g.len - first : p.size, LAUNCH == 1 || g.j == 0}, m, h, c0, S, &total);
+    float *to = last ? cache : nullptr;
+    if (LAUNCH == 0 && !last) {
+        const int64_t e = (int64_t)(seg - g.s) * p.heads + h;
+        to = p.seg + e * head;
+        if (threadIdx.x == 0 && vb == 0) p.total[e] = total;
+    }
+    if (!to || c >= p.dv) return;
 #pragma unroll
     for (int d = 0; d < 2 * KB; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = 16 * d + 4 * gq + r;
-            if (row < p.dk) cache[(int64_t)row * p.dv] = S[d][r];
+            const int row = M::row_of(d, gq, r);
+            if (row < p.dk) to[row * p.dv + c] = S[d][r];
         }
+}
+
+// Between the launches: a thread per number of a head's state walks the entries of a sequence in order and leaves the state at
+// the end of each segment in its place.  Sequences are dealt out by their numbers, or, where there are more of them than
+// entries, by those entries that are their first.
+__global__ __launch_bounds__(64) void la_join(LaParams p) {
+    const int64_t head = (int64_t)p.dk * p.dv, entry = p.heads * head, i = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const bool live = i < entry, by_entry = p.s.nseq > p.entries;
+    const int h = (int)((live ? i : 0) / head);
+    const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
+    for (int b = blockIdx.y; b < (by_entry ? p.entries : p.s.nseq); b += gridDim.y) {
+        Range rg;
+        if (by_entry) {
+            const Segment g = find_segment<true>(p.s, b, div, threadIdx.x);
+            if (g.j != 1) continue;  // not its sequence's first
+            rg = {g.t0, g.len};
+        } else {
+            rg = range_of(p.s, b);
+        }
+        const int n = rg.len > 0 ? div(rg.len - 1) : 0;  // all but the last
+        if (n < 2 || !live) continue;
+        const int64_t first = div(rg.t0);
+        float *e = p.seg + first * entry + i;
+        const double *t = p.total + first * p.heads + h;
+        float S = e[0];
+        constexpr int U = 8;  // loaded ahead
+        for (int j0 = 1; j0 < n; j0 += U) {
+            float ev[U];
+            double tv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t j = j0 + u < n ? j0 + u : n - 1;
+                ev[u] = e[j * entry], tv[u] = t[j * p.heads];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j0 + u >= n) break;
+                const double f = exp2(tv[u]);
+                const float fh = (float)f;
+                S = fmaf(S, fh, fmaf(S, (float)(f - (double)fh), ev[u]));
+                e[(j0 + u) * entry] = S;
+            }
+        }
+    }
 }
 
 // One token per sequence: 4 x CG columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in
@@ -477,7 +579,7 @@ __global__ __launch_bounds__(256) void la_step(LaParams p) {
         if (j < nc) out[j] = Io<T>::to(p.scale * s[j]);
 }
 
-constexpr int64_t kMaxStride = INT64_C(1) << 26;
+constexpr int64_t kMaxStride = INT64_C(1) << 23;  // 64 rows within 31 bits
 
 struct LaArgs {
     const void *q;
@@ -548,6 +650,40 @@ LaParams la_params(const LaArgs &a, int columns) {
     return p;
 }
 
+// Tokens per segment, or 0: whole sequences.  A workgroup's time is counted in chunks of 64 tokens.
+constexpr int64_t kSlots = 512;  // two workgroups to each of 256 compute units
+
+int split_size(int64_t tokens, int64_t max_seqlen, int64_t heads, int64_t dv) {
+    const int64_t lanes = heads * ((dv + 63) / 64), longest = max_seqlen < tokens ? max_seqlen : tokens;
+    const int64_t share = (tokens * lanes + kSlots * 64 - 1) / (kSlots * 64), whole = (longest + 63) / 64;
+    if (whole <= 2 * share + 8) return 0;
+    const int64_t size = share < 2 ? 2 : share > 64 ? 64 : share;
+    return 2 * size <= whole ? (int)size * 64 : 0;
+}
+bool la_sizes(int64_t heads, int64_t dk, int64_t dv) {
+    return heads > 0 && dk > 0 && dv > 0 && dk <= kMaxKeys && dv <= kMaxValues && heads <= kMaxStride;
+}
+size_t totals_bytes(int64_t entries, int64_t heads) { return ((size_t)entries * heads * 8 + 15) / 16 * 16; }
+
+constexpr int64_t kGridY = 65535;
+
+template <typename T, int KB, bool VEC>
+int launch_packed(const LaParams &p, int64_t blocks, void *stream) {
+    int rc = enqueue(la_packed<T, KB, VEC, 0>, dim3((unsigned)blocks), dim3(256), p, stream);
+    if (rc != SELSCAN_OK || !p.seg) return rc;
+    const int64_t entry = (int64_t)p.heads * p.dk * p.dv, y = p.s.nseq < p.entries ? p.s.nseq : p.entries;
+    rc = enqueue(la_join, dim3((unsigned)((entry + 63) / 64), (unsigned)(y < kGridY ? y : kGridY)), dim3(64), p, stream);
+    if (rc != SELSCAN_OK) return rc;
+    return enqueue(la_packed<T, KB, VEC, 1>, dim3((unsigned)((int64_t)p.entries * p.heads * p.vblocks)), dim3(256), p, stream);
+}
+template <typename T, bool VEC>
+int launch_packed_keys(const LaParams &p, int64_t blocks, void *stream) {
+    return p.dk <= 32    ? launch_packed<T, 1, VEC>(p, blocks, stream)
+           : p.dk <= 64  ? launch_packed<T, 2, VEC>(p, blocks, stream)
+           : p.dk <= 128 ? launch_packed<T, 4, VEC>(p, blocks, stream)
+                         : launch_packed<T, 8, VEC>(p, blocks, stream);
+}
+
 template <typename T, int CG, int ND>
 int launch_step(const LaParams &p, int64_t blocks, bool vec, void *stream) {
     return enqueue(vec ? la_step<T, CG, ND, true> : la_step<T, CG, ND, false>, dim3((unsigned)blocks), dim3(256), p, stream);
@@ -559,7 +695,11 @@ extern "C" {
 
 size_t linear_attn_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t heads, int64_t dk,
                                           int64_t dv) {
-    return 0;
+    if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || tokens > kMaxTokens || nseq > INT32_MAX / 2 || !la_sizes(heads, dk, dv)) return 0;
+    const int size = split_size(tokens, max_seqlen, heads, dv);
+    if (!size) return 0;
+    const int64_t entries = tokens / size;
+    return totals_bytes(entries, heads) + (size_t)entries * heads * dk * dv * 4;
 }
 
 int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -574,14 +714,24 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
     bool nothing;
     const int rc = la_check(a, &nothing);
     if (rc != SELSCAN_OK || nothing) return rc;
-    const LaParams p = la_params(a, 64);
+    LaParams p = la_params(a, 64);
     const int64_t per = heads * p.vblocks;
-    if (mul_size(nseq, per) < 0 || !grid_fits(nseq * per, 256)) return SELSCAN_E_UNSUPPORTED;
-    void (*kernel)(LaParams) = nullptr;
-#define PICK(T) (dk <= 32 ? la_packed<T, 1> : dk <= 64 ? la_packed<T, 2> : dk <= 128 ? la_packed<T, 4> : la_packed<T, 8>)
-    kernel = io_dtype == SELSCAN_BF16 ? PICK(uint16_t) : PICK(float);
-#undef PICK
-    return enqueue(kernel, dim3((unsigned)(nseq * per)), dim3(256), p, stream);
+    int64_t pieces = nseq;
+    if (need) {
+        p.size = split_size(tokens, max_seqlen, heads, dv);
+        p.dsize = make_div((uint32_t)p.size);
+        p.entries = (int)(tokens / p.size);
+        pieces = tokens / p.size + nseq;
+        p.total = (double *)workspace;
+        p.seg = (float *)((char *)workspace + totals_bytes(p.entries, heads));
+    }
+    if (mul_size(pieces, per) < 0 || !grid_fits(pieces * per, 256) || (need && !grid_fits(heads * dk * dv / 64 + 1, 64))) return SELSCAN_E_UNSUPPORTED;
+    const int64_t e = io_dtype == SELSCAN_BF16 ? 8 : 4, word = io_dtype == SELSCAN_BF16 ? 2 : 1;
+    const bool vec = dk % e == 0 && dv % e == 0 && q_stride % word == 0 && k_stride % word == 0 && v_stride % word == 0 &&
+                     span_aligned(q, 4) && span_aligned(k, 4) && span_aligned(v, 4) && span_aligned(out, 4);
+    if (io_dtype == SELSCAN_BF16)
+        return vec ? launch_packed_keys<uint16_t, true>(p, pieces * per, stream) : launch_packed_keys<uint16_t, false>(p, pieces * per, stream);
+    return vec ? launch_packed_keys<float, true>(p, pieces * per, stream) : launch_packed_keys<float, false>(p, pieces * per, stream);
 }
 
 int linear_attn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
