@@ -263,8 +263,8 @@ int linear_attn_step(const void *q, int64_t q_stride, const void *k, int64_t k_s
  *   logprob : [rows] fp32, the log of the token's weight over the weights of all that stay
  *   kept    : [rows] int32, how many tokens stay
  *   vocab   : 1..2^21 (SELSCAN_E_SHAPE, SELSCAN_E_UNSUPPORTED)
- * Weights are whole multiples of 2^-45 (for vocab 2^17; of vocab 2^-62, rounded up to a power of 2, and at least 2^-52), summed as whole numbers: what is drawn does not
- * depend on how a row is split.  A logit of -infinity never stays.  A row of nothing else has token -1, logprob -infinity and
+ * Weights are whole multiples of 2^-45 (for a vocab of 2^17; of 2^-62 times the vocab rounded up to a power of 2, and of 2^-51 at
+ * least), summed as whole numbers: what is drawn does not depend on how a row is split.  A logit of -infinity never stays.  A row of nothing else has token -1, logprob -infinity and
  * kept 0; a row with a NaN or +infinity has token -1, logprob NaN and kept 0.
  */
 int token_sample(const void *logits, int64_t logits_stride, const float *uniform, const float *temperature,
