@@ -234,7 +234,7 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
                            int64_t tokens, int64_t nseq, int64_t nslots, int64_t max_seqlen, int64_t heads, int64_t groups,
                            int64_t dk, int64_t dv, int io_dtype, void *workspace, size_t workspace_bytes, void *stream);
 size_t linear_attn_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t heads, int64_t dk,
-                                          int64_t dv);
+                                          int64_t dv, int io_dtype);
 
 /*
  * linear_attn_step - one token for each of `rows` running sequences: the call above with every sequence one token long,

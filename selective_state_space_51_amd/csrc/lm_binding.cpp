@@ -438,7 +438,7 @@ Tensor linattn_packed(const Tensor &q, const Tensor &k, const Tensor &v, const T
     const int64_t longest = max_seqlen.value_or(s.rows);
     const Tensor out = out_ ? *out_ : empty({s.rows, s.heads, s.dv}, q, dt);
     want_shape("out", out, {s.rows, s.heads, s.dv});
-    const Workspace ws = workspace(linear_attn_packed_workspace_bytes(s.rows, p.nseq, longest, s.heads, s.dk, s.dv), ws_, q);
+    const Workspace ws = workspace(linear_attn_packed_workspace_bytes(s.rows, p.nseq, longest, s.heads, s.dk, s.dv, io), ws_, q);
     const Rows qr = heads_of("q", q, dt), kr = heads_of("k", k, dt), vr = heads_of("v", v, dt), dr = decay_rows(decay);
     check(linear_attn_packed_fwd(qr.p, qr.stride, kr.p, kr.stride, vr.p, vr.stride, (const float *)dr.p, dr.stride, (float)scale,
                                  p.cu, p.slots, p.carry, ptr<float>("state", state, at::kFloat), ptr("out", out, dt), s.rows,

@@ -16,9 +16,9 @@ struct LaParams {
     int heads, share, dk, dv, vblocks;  // share: heads of a group
     float scale;
     // sequences in segments of `size` tokens: what each entry holds (the state at the end of a segment that another
-    // follows, from zero but for a sequence's first), and the sum of its log decays (base 2)
+    // follows, from zero but for a sequence's first), and what its decays make of a state before it
     float *seg;    // [entries][heads][dk][dv]
-    double *total; // [entries][heads]
+    float2 *factor; // [entries][heads], in two parts
     int size, entries;
     FastDiv dsize;
 };
@@ -68,15 +68,17 @@ __device__ __forceinline__ B8 pack8(const F4 &a, const F4 &b) {
 template <typename T, int KB>
 struct Chunk {
     static constexpr bool BF = sizeof(T) == 2;
-    static constexpr int C = BF || KB <= 2 ? 64 : 32, NT = C / 16;  // tokens, and tiles of 16 of them
+    static constexpr int C = BF ? 64 : 32, NT = C / 16;  // tokens, and tiles of 16 of them
     static constexpr int D = 32 * KB;                               // rows of the state, padded
     static constexpr int E = 16 / sizeof(T);                        // elements of 16 bytes
     // Row strides in LDS: rows start at different banks, for 16 rows of 16 bytes and (bf16) for 4 rows of 4 pieces 16 bytes apart
     static constexpr int LQ = BF ? D + (KB >= 4 ? 40 : 8) : D + 4, LV = 64 + E, LP = C + E;
     static constexpr int NQ = C * D / E / 256, NV = C * 64 / E / 256;  // 16-byte pieces of a thread
     T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP];
-    float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
-    float fh, fl;              // 2^G_C in two parts
+    struct Decay {
+        float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
+        float fh, fl;              // 2^G_C in two parts
+    } decay[2];                    // of this chunk and the next
     // row of the state that register r of tile d has in lanes 16 g .. 16 g + 15
     static __device__ __forceinline__ int row_of(int d, int g, int r) {
         return BF ? 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r : 16 * d + 4 * g + r;
@@ -173,7 +175,31 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                 vr[i] = r < rows && c < nv ? load_piece(v1 + r * p.v_stride, c, nv) : make_uint4(0, 0, 0, 0);
             }
         }
-        if (wave == 0) gr = lane < rows ? decay[(first + lane) * p.decay_stride] : 0.f;
+    };
+    // The last wave, which has the fewest tiles of the scores, sums the decays, a chunk ahead.
+    const bool sums = wave == 3;
+    const auto fetch_decay = [&](int first) { gr = lane < C && first + lane < w.n ? decay[(first + lane) * p.decay_stride] : 0.f; };
+    double sum = 0.;
+    const auto sum_decays = [&](typename M::Decay &to) {
+        // sums of up to 64 x 16384 whose differences count: 64 bits, then two parts of 32
+        double G = (double)finite_decay(gr) * 1.44269504088896340735992468100;
+        G += dpp_or_zero<0x111, 0xF>(G);
+        G += dpp_or_zero<0x112, 0xF>(G);
+        G += dpp_or_zero<0x114, 0xF>(G);
+        G += dpp_or_zero<0x118, 0xF>(G);
+        G += dpp_or_zero<0x142, 0xA>(G);
+        G += dpp_or_zero<0x143, 0xC>(G);
+        const int64_t b = __double_as_longlong(G);
+        const double all = __longlong_as_double((int64_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32 |
+                                                (uint32_t)__builtin_amdgcn_readlane((int)b, 63));
+        if (lane < C) {
+            const float hi = (float)G;
+            to.gh[lane] = hi, to.gl[lane] = (float)(G - (double)hi);
+            to.w[lane] = __builtin_amdgcn_exp2f((float)(all - G));
+        }
+        const double f = exp2(all);
+        if (lane == 0) to.fh = (float)f, to.fl = (float)(f - (double)(float)f);
+        sum += all;
     };
     // tiles of the scores that are this wave's: pair i is key tile jt and query tile tt, jt <= tt
     const auto pair_of = [&](int i, int &jt, int &tt) {
@@ -185,9 +211,17 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         return at < NT * (NT + 1) / 2;
     };
     const int vrow = 8 * g + (l >> 2), vcol = 16 * wave + 4 * (l & 3);  // of a transposed read
-    double sum = 0.;
-    if (w.n > 0) fetch(0);
-    for (int first = 0; first < w.n; first += C) {
+    if (w.n > 0) {
+        fetch(0);
+        if (sums) {
+            fetch_decay(0);
+            sum_decays(m.decay[0]);
+            fetch_decay(C);
+        }
+    }
+    int now = 0;  // which of the two decays
+    for (int first = 0; first < w.n; first += C, now ^= 1) {
+        const typename M::Decay &dc = m.decay[now];
         lds_barrier();  // the chunk before is no longer read
         T *to = m.k + tid / PQ * M::LQ + tid % PQ * E, *qto = m.q + tid / PQ * M::LQ + tid % PQ * E;
 #pragma unroll
@@ -197,35 +231,18 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         }
 #pragma unroll
         for (int i = 0; i < M::NV; ++i) *(uint4 *)(m.v + (tid / PV + i * (256 / PV)) * M::LV + tid % PV * E) = vr[i];
-        if (wave == 0) {
-            // sums of up to 64 x 16384 whose differences count: 64 bits, then two parts of 32
-            double G = (double)finite_decay(gr) * 1.44269504088896340735992468100;
-            G += dpp_or_zero<0x111, 0xF>(G);
-            G += dpp_or_zero<0x112, 0xF>(G);
-            G += dpp_or_zero<0x114, 0xF>(G);
-            G += dpp_or_zero<0x118, 0xF>(G);
-            G += dpp_or_zero<0x142, 0xA>(G);
-            G += dpp_or_zero<0x143, 0xC>(G);
-            const int64_t b = __double_as_longlong(G);
-            const double all = __longlong_as_double((int64_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32 |
-                                                    (uint32_t)__builtin_amdgcn_readlane((int)b, 63));
-            if (lane < C) {
-                const float hi = (float)G;
-                m.gh[lane] = hi, m.gl[lane] = (float)(G - (double)hi);
-                m.w[lane] = __builtin_amdgcn_exp2f((float)(all - G));
-            }
-            const double f = exp2(all);
-            if (lane == 0) m.fh = (float)f, m.fl = (float)(f - (double)(float)f);
-            sum += all;
-        }
         if (first + C < w.n) fetch(first + C);
         lds_barrier();
+        if (sums && first + C < w.n) {
+            sum_decays(m.decay[now ^ 1]);
+            fetch_decay(first + 2 * C);
+        }
         if (w.outputs) {
             // scores, keys down, so that a lane's four are adjacent in a row of p
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
                 int jt, tt;
-                if (pair_of(i, jt, tt)) {
+                if (pair_of(i, jt, tt) || 4 * (i + 1) <= NT * (NT + 1) / 2) {
                     const T *kp = m.k + (16 * jt + l) * M::LQ, *qp = m.q + (16 * tt + l) * M::LQ;
                     F4 acc = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (M::BF) {
@@ -240,8 +257,8 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                         }
                     }
                     const int t = 16 * tt + l, j = 16 * jt + 4 * g;
-                    const float th = m.gh[t], tl = m.gl[t];
-                    const F4 jh = *(const F4 *)(m.gh + j), jl = *(const F4 *)(m.gl + j);
+                    const float th = dc.gh[t], tl = dc.gl[t];
+                    const F4 jh = *(const F4 *)(dc.gh + j), jl = *(const F4 *)(dc.gl + j);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = __builtin_amdgcn_exp2f((th - jh[r]) + (tl - jl[r]));
@@ -313,60 +330,71 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
             const int rows = w.n - first < C ? w.n - first : C, left = nv - 16 * wave - 4 * g;
             T *out1 = out + first * out_stride;
             const __amdgpu_buffer_rsrc_t ob = rows_buffer(out1, rows, out_stride, nv);
+            // (all tiles before the branch: their products do not wait for one another, and a result of the matrix cores is
+            // read in the block that makes it)
+            F4 o[NT];
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt) {
                 const int t = 16 * tt + l;
                 const T *qp = m.q + t * M::LQ, *pp = m.p + t * M::LP;
-                F4 o = {0.f, 0.f, 0.f, 0.f};
+                o[tt] = (F4){0.f, 0.f, 0.f, 0.f};
                 if constexpr (M::BF) {
 #pragma unroll
-                    for (int s = 0; s < KB; ++s) o = mma(sf[s], *(const B8 *)(qp + 32 * s + 8 * g), o);
+                    for (int s = 0; s < KB; ++s) o[tt] = mma(sf[s], *(const B8 *)(qp + 32 * s + 8 * g), o[tt]);
                 } else {
 #pragma unroll
                     for (int d = 0; d < 2 * KB; ++d) {
                         const F4 b = *(const F4 *)(qp + 16 * d + 4 * g);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) o = mma(S[d][r], b[r], o);
+                        for (int r = 0; r < 4; ++r) o[tt] = mma(S[d][r], b[r], o[tt]);
                     }
                 }
-                o *= __builtin_amdgcn_exp2f(m.gh[t] + m.gl[t]);
+                o[tt] *= __builtin_amdgcn_exp2f(dc.gh[t] + dc.gl[t]);
                 if constexpr (M::BF) {
 #pragma unroll
-                    for (int s = 0; s <= tt / 2; ++s) o = mma(vf[s], *(const B8 *)(pp + 32 * s + 8 * g), o);
+                    for (int s = 0; s <= tt / 2; ++s) o[tt] = mma(vf[s], *(const B8 *)(pp + 32 * s + 8 * g), o[tt]);
                 } else {
 #pragma unroll
                     for (int s = 0; s <= tt; ++s) {
                         const F4 b = *(const F4 *)(pp + 16 * s + 4 * g);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) o = mma(vx[s][r], b[r], o);
+                        for (int r = 0; r < 4; ++r) o[tt] = mma(vx[s][r], b[r], o[tt]);
                     }
                 }
-                // (before the branch: a result of the matrix cores is read in the block that makes it)
-                o *= p.scale;
-                if (odd) {
+                o[tt] *= p.scale;
+            }
+            if (odd) {
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt) {
+                    const int t = 16 * tt + l;
+#pragma unroll 1
                     for (int j = 0; j <= t; ++j)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const float x = Io<T>::f32(m.v[j * M::LV + 16 * wave + 4 * g + r]);
-                            if (!(fabsf(x) < INFINITY)) o[r] = fmaf(Io<T>::f32(pp[j]) * p.scale, x, o[r]);
+                            if (!(fabsf(x) < INFINITY)) o[tt][r] = fmaf(Io<T>::f32(m.p[t * M::LP + j]) * p.scale, x, o[tt][r]);
                         }
                 }
+            }
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+                const int t = 16 * tt + l;
                 if constexpr (VEC) {
                     const uint32_t at = left > 0 ? (uint32_t)(t * (int)out_stride + 16 * wave + 4 * g) * sizeof(T) : kNowhere;
                     if constexpr (M::BF)
-                        __builtin_amdgcn_raw_buffer_store_b64((U2){Io<T>::to2(o[0], o[1]), Io<T>::to2(o[2], o[3])}, ob, at, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, o), ob, at, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b64((U2){Io<T>::to2(o[tt][0], o[tt][1]), Io<T>::to2(o[tt][2], o[tt][3])}, ob, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, o[tt]), ob, at, 0, 0);
                 } else if (t < rows) {
                     T *oto = out1 + t * out_stride + 16 * wave + 4 * g;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (r < left) oto[r] = Io<T>::to(o[r]);
+                        if (r < left) oto[r] = Io<T>::to(o[tt][r]);
                 }
             }
         }
         // the state
         read_values();
-        const float fh = m.fh, fl = m.fl;
+        const float fh = dc.fh, fl = dc.fl;
         if constexpr (M::BF) {
             // (the rounding of a chunk's factor, 2^-25 of a state, is far below a sum's with k and v in bf16)
 #pragma unroll
@@ -375,7 +403,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
             B8 part[C / 32][3];
 #pragma unroll
             for (int s = 0; s < C / 32; ++s) {
-                F4 x[2] = {*(const F4 *)(m.w + 32 * s + 8 * g), *(const F4 *)(m.w + 32 * s + 8 * g + 4)};
+                F4 x[2] = {*(const F4 *)(dc.w + 32 * s + 8 * g), *(const F4 *)(dc.w + 32 * s + 8 * g + 4)};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] *= (float)vf[s][e];
 #pragma unroll
@@ -402,7 +430,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                 for (int r = 0; r < 4; ++r) S[d][r] = fmaf(S[d][r], fh, S[d][r] * fl);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
-                const F4 x = *(const F4 *)(m.w + 16 * s + 4 * g);
+                const F4 x = *(const F4 *)(dc.w + 16 * s + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) vx[s][r] *= x[r];
             }
@@ -419,9 +447,16 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
 }
 
 // Packed prompts.  A workgroup has 64 columns of a head's values and a whole sequence or one of its segments.  Segments take
-// two launches: the first (LAUNCH 0) reads every sequence's first segment for good, and of every other one that a further one
-// follows only what it makes of a state of zero; the states are joined; the second (LAUNCH 1) reads the segments but the first
-// from the states that they start from.
+// two launches: the first (LAUNCH 0) reads sequences of one segment for good, and of the others what each segment that a further
+// one follows makes of the sequence's first state or of a state of zero; the states are joined; the second (LAUNCH 1) reads
+// the others' segments from the states that they start from.  (Outputs of every first segment in the first launch make that
+// launch as long as the second: 4,097 tokens x 24 heads of 64 x 64 fp32 take 60 us, and took 70.)
+// What bounds it: the chunks of the longest sequence or segment, one after another, 64 tokens in 2.4 us (bf16, 64 x 64) to
+// 4.1 us (bf16, 128 x 64, two workgroups to a compute unit).  27,591 tokens of 24 prompts x 64 heads of 128 x 64 bf16: 267 us, 2.1 TB/s of what
+// has to pass; LDS is busy for half of the clocks, the vector units for 40 %.  Two 64-column pieces or two heads in a workgroup of
+// eight waves 302 us, 32 columns per wave 409 (fewer waves, each with longer chains), chunks of 32 tokens 281, and segments of 512,
+// 1,024 or 2,048 tokens are slower there than whole sequences.  fp32 chunks are of 32 tokens: 31 KB of LDS at 64
+// keys, five workgroups to a compute unit, where 64 tokens take 70 KB and allow two.
 template <typename T, int KB, bool VEC, int LAUNCH>
 __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     typedef Chunk<T, KB> M;
@@ -429,16 +464,18 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, gq = lane >> 4;
     const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads, seg = hs / p.heads;
     const bool split = p.seg != nullptr;
-    const auto div = [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); };
-    const Segment g = LAUNCH == 1 ? find_segment<true>(p.s, seg, div, lane) : split ? find_segment(p.s, seg, div, lane) : whole_sequence(p.s, seg);
+    const Segment g = split ? find_segment(p.s, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane) : whole_sequence(p.s, seg);
     const int first = split ? g.j * p.size : 0;
-    if (g.j < LAUNCH || (g.j > 0 && first >= g.len)) return;
-    const bool last = !split || g.len - first <= p.size;
-    if (LAUNCH == 0 && g.j > 0 && last) return;
+    if (g.j > 0 && first >= g.len) return;
+    const bool last = !split || g.len - first <= p.size, only = last && g.j == 0;
     const int c0 = vb * 64, c = c0 + 16 * wave + l;
     const int64_t head = (int64_t)p.dk * p.dv;
     float *cache = p.state && g.slot >= 0 ? p.state + ((int64_t)g.slot * p.heads + h) * head : nullptr;
-    const float *from = LAUNCH == 1 ? p.seg + ((int64_t)seg * p.heads + h) * head : g.j == 0 && g.carry ? cache : nullptr;
+    const int64_t entry = (int64_t)(seg - g.s) * p.heads + h;  // of this segment
+    const float *from = g.j == 0 ? g.carry ? cache : nullptr : LAUNCH == 1 ? p.seg + (entry - p.heads) * head : nullptr;
+    // (a first segment that starts from the cache is read for good before the launch whose last segment writes there)
+    const bool early = only || (g.j == 0 && from);
+    if (LAUNCH == 0 ? last && !only : early) return;
     F4 S[2 * KB];
 #pragma unroll
     for (int d = 0; d < 2 * KB; ++d)
@@ -448,12 +485,16 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
             S[d][r] = from && c < p.dv && row < p.dk ? from[row * p.dv + c] : 0.f;
         }
     double total;
-    la_piece<T, KB, VEC>(p, {g.t0 + first, last ? g.len - first : p.size, LAUNCH == 1 || g.j == 0}, m, h, c0, S, &total);
+    // (the same in all lanes, for the buffers' descriptors)
+    const int t0 = __builtin_amdgcn_readfirstlane(g.t0 + first), n = __builtin_amdgcn_readfirstlane(last ? g.len - first : p.size);
+    la_piece<T, KB, VEC>(p, {t0, n, LAUNCH == 1 || early}, m, h, c0, S, &total);
     float *to = last ? cache : nullptr;
     if (LAUNCH == 0 && !last) {
-        const int64_t e = (int64_t)(seg - g.s) * p.heads + h;
-        to = p.seg + e * head;
-        if (threadIdx.x == 0 && vb == 0) p.total[e] = total;
+        to = p.seg + entry * head;
+        if (threadIdx.x == 192 && vb == 0) {  // (of the wave that sums the decays)
+            const double f = exp2(total);
+            p.factor[entry] = make_float2((float)f, (float)(f - (double)(float)f));
+        }
     }
     if (!to || c >= p.dv) return;
 #pragma unroll
@@ -486,12 +527,12 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
         if (n < 2 || !live) continue;
         const int64_t first = div(rg.t0);
         float *e = p.seg + first * entry + i;
-        const double *t = p.total + first * p.heads + h;
+        const float2 *t = p.factor + first * p.heads + h;
         float S = e[0];
-        constexpr int U = 8;  // loaded ahead
+        constexpr int U = 16;  // loaded ahead
         for (int j0 = 1; j0 < n; j0 += U) {
             float ev[U];
-            double tv[U];
+            float2 tv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t j = j0 + u < n ? j0 + u : n - 1;
@@ -500,17 +541,17 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (j0 + u >= n) break;
-                const double f = exp2(tv[u]);
-                const float fh = (float)f;
-                S = fmaf(S, fh, fmaf(S, (float)(f - (double)fh), ev[u]));
+                S = fmaf(S, tv[u].x, fmaf(S, tv[u].y, ev[u]));
                 e[(j0 + u) * entry] = S;
             }
         }
     }
 }
 
-// One token per sequence: 4 x CG columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in
-// each thread, all of them in flight at once.
+// One token per sequence: S' = e^g S + k v^T, out = scale q^T S'.  The state is read and written once, and that bounds it: 4 x CG
+// columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in each thread, all of them in flight at
+// once.  128 rows x 64 heads of 128 x 64 (fp32 states of 268 MB): 114 us, 4.7 TB/s of the 5.1 of a copy.  A decay near 1 is taken
+// as S + (e^g - 1) S: rounded to 24 bits itself, it would be off in the same direction at every step.
 template <typename T, int CG, int ND, bool VEC>
 __global__ __launch_bounds__(256) void la_step(LaParams p) {
     __shared__ float4 part[4][CG];
@@ -544,13 +585,16 @@ __global__ __launch_bounds__(256) void la_step(LaParams p) {
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = j < nc ? Io<T>::f32(v[j]) : 0.f;
-    const float e = __builtin_amdgcn_exp2f(finite_decay(p.decay[row * p.decay_stride + h]) * kLog2e);
+    const float decay = finite_decay(p.decay[row * p.decay_stride + h]);
+    const bool slow = fabsf(decay) < 0.5f;
+    const float e = slow ? expm1f(decay) : __builtin_amdgcn_exp2f(decay * kLog2e);
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            S[i][j] = fmaf(e, S[i][j], kv[i] * x[j]);
+            const float kx = slow ? fmaf(kv[i], x[j], S[i][j]) : kv[i] * x[j];
+            S[i][j] = fmaf(e, S[i][j], kx);
             o[j] = fmaf(qv[i], S[i][j], o[j]);
         }
         if (d0 + i < p.dk && slot >= 0) {
@@ -650,20 +694,26 @@ LaParams la_params(const LaArgs &a, int columns) {
     return p;
 }
 
-// Tokens per segment, or 0: whole sequences.  A workgroup's time is counted in chunks of 64 tokens.
-constexpr int64_t kSlots = 512;  // two workgroups to each of 256 compute units
+// Tokens per segment, or 0: whole sequences.  In chunks of 64 tokens, the longest sequence takes `whole` of them one after another,
+// and all take `share` if they are even.  Measured, whole and in segments (us): bf16, 24 heads of 64 x 64, 512 tokens 24 and 24,
+// 768 33 and 25, 2,048 79 and 32, four of 1,024 44 and 50, eight of 2,048 80 and 103; 64 heads of 128 x 64, 1,024 tokens 66 and
+// 59, two of 2,048 124 and 123, four of 4,096 238 and 256.  fp32, whose chunks take longer, 24 heads of 64 x 64, 768 tokens 65 and
+// 32, four of 1,024 87 and 60, eight of 2,048 167 and 153; 64 heads of 128 x 64, two of 2,048 268 and 245, four of 4,096 528
+// and 614.  Segments of 192 tokens of one of 4,097 fp32: 63 us, of 128 70, of 256 70, of 384 76.
+constexpr int64_t kSlots = 768;  // three workgroups to each of 256 compute units
 
-int split_size(int64_t tokens, int64_t max_seqlen, int64_t heads, int64_t dv) {
+int split_size(int64_t tokens, int64_t max_seqlen, int64_t heads, int64_t dv, int io) {
     const int64_t lanes = heads * ((dv + 63) / 64), longest = max_seqlen < tokens ? max_seqlen : tokens;
-    const int64_t share = (tokens * lanes + kSlots * 64 - 1) / (kSlots * 64), whole = (longest + 63) / 64;
-    if (whole <= 2 * share + 8) return 0;
-    const int64_t size = share < 2 ? 2 : share > 64 ? 64 : share;
+    const int64_t whole = (longest + 63) / 64, times = io == SELSCAN_BF16 ? 5 : 3;
+    const double share = (double)tokens * (double)lanes / (double)(kSlots * 64);
+    if ((double)whole <= share * times + 7.) return 0;
+    const int64_t even = (int64_t)ceil(share), size = even < 2 ? 2 : even > 64 ? 64 : even;
     return 2 * size <= whole ? (int)size * 64 : 0;
 }
 bool la_sizes(int64_t heads, int64_t dk, int64_t dv) {
     return heads > 0 && dk > 0 && dv > 0 && dk <= kMaxKeys && dv <= kMaxValues && heads <= kMaxStride;
 }
-size_t totals_bytes(int64_t entries, int64_t heads) { return ((size_t)entries * heads * 8 + 15) / 16 * 16; }
+size_t factors_bytes(int64_t entries, int64_t heads) { return ((size_t)entries * heads * 8 + 15) / 16 * 16; }
 
 constexpr int64_t kGridY = 65535;
 
@@ -674,7 +724,7 @@ int launch_packed(const LaParams &p, int64_t blocks, void *stream) {
     const int64_t entry = (int64_t)p.heads * p.dk * p.dv, y = p.s.nseq < p.entries ? p.s.nseq : p.entries;
     rc = enqueue(la_join, dim3((unsigned)((entry + 63) / 64), (unsigned)(y < kGridY ? y : kGridY)), dim3(64), p, stream);
     if (rc != SELSCAN_OK) return rc;
-    return enqueue(la_packed<T, KB, VEC, 1>, dim3((unsigned)((int64_t)p.entries * p.heads * p.vblocks)), dim3(256), p, stream);
+    return enqueue(la_packed<T, KB, VEC, 1>, dim3((unsigned)blocks), dim3(256), p, stream);
 }
 template <typename T, bool VEC>
 int launch_packed_keys(const LaParams &p, int64_t blocks, void *stream) {
@@ -693,13 +743,13 @@ int launch_step(const LaParams &p, int64_t blocks, bool vec, void *stream) {
 
 extern "C" {
 
-size_t linear_attn_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t heads, int64_t dk,
-                                          int64_t dv) {
-    if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || tokens > kMaxTokens || nseq > INT32_MAX / 2 || !la_sizes(heads, dk, dv)) return 0;
-    const int size = split_size(tokens, max_seqlen, heads, dv);
+size_t linear_attn_packed_workspace_bytes(int64_t tokens, int64_t nseq, int64_t max_seqlen, int64_t heads, int64_t dk, int64_t dv,
+                                          int io_dtype) {
+    if (tokens <= 0 || nseq <= 0 || max_seqlen <= 0 || tokens > kMaxTokens || nseq > INT32_MAX / 2 || !la_sizes(heads, dk, dv) || !io_known(io_dtype)) return 0;
+    const int size = split_size(tokens, max_seqlen, heads, dv, io_dtype);
     if (!size) return 0;
     const int64_t entries = tokens / size;
-    return totals_bytes(entries, heads) + (size_t)entries * heads * dk * dv * 4;
+    return factors_bytes(entries, heads) + (size_t)entries * heads * dk * dv * 4;
 }
 
 int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -708,7 +758,7 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
                            int64_t tokens, int64_t nseq, int64_t nslots, int64_t max_seqlen, int64_t heads, int64_t groups,
                            int64_t dk, int64_t dv, int io_dtype, void *workspace, size_t workspace_bytes, void *stream) {
     if (max_seqlen < 0) return SELSCAN_E_SHAPE;
-    const size_t need = linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv);
+    const size_t need = linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv, io_dtype);
     const LaArgs a{q, q_stride, k, k_stride, v, v_stride, log_decay, decay_stride, scale, cu_seqlens, slots, carry, state, out,
                    tokens, nseq, nslots, heads, groups, dk, dv, io_dtype, workspace, need, workspace_bytes, true};
     bool nothing;
@@ -718,12 +768,12 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
     const int64_t per = heads * p.vblocks;
     int64_t pieces = nseq;
     if (need) {
-        p.size = split_size(tokens, max_seqlen, heads, dv);
+        p.size = split_size(tokens, max_seqlen, heads, dv, io_dtype);
         p.dsize = make_div((uint32_t)p.size);
         p.entries = (int)(tokens / p.size);
         pieces = tokens / p.size + nseq;
-        p.total = (double *)workspace;
-        p.seg = (float *)((char *)workspace + totals_bytes(p.entries, heads));
+        p.factor = (float2 *)workspace;
+        p.seg = (float *)((char *)workspace + factors_bytes(p.entries, heads));
     }
     if (mul_size(pieces, per) < 0 || !grid_fits(pieces * per, 256) || (need && !grid_fits(heads * dk * dv / 64 + 1, 64))) return SELSCAN_E_UNSUPPORTED;
     const int64_t e = io_dtype == SELSCAN_BF16 ? 8 : 4, word = io_dtype == SELSCAN_BF16 ? 2 : 1;

@@ -46,7 +46,7 @@ def _load():
     sig("token_logprobs_bwd", [vp, i64] + [vp] * 5 + [cf, vp, i64, i64, ci, vp])
     sig("w4_matvec", [vp, i64] + [vp] * 5 + [i64] * 4 + [ci, vp])
     sig("linear_attn_packed_fwd", [vp, i64] * 4 + [cf] + [vp] * 5 + [i64] * 8 + [ci, vp, sz, vp])
-    sig("linear_attn_packed_workspace_bytes", [i64] * 6, sz)
+    sig("linear_attn_packed_workspace_bytes", [i64] * 6 + [ci], sz)
     sig("linear_attn_step", [vp, i64] * 4 + [cf] + [vp] * 3 + [i64] * 6 + [ci, vp])
     sig("token_sample", [vp, i64, vp, vp, cf, vp, ci, vp, cf, vp, cf] + [vp] * 3 + [i64, i64, ci, vp])
     sig("cache_entries_copy", [vp, vp, i64, vp, vp, i64, i64, vp])
@@ -56,7 +56,7 @@ def _load():
 
 
 lm_lib = _load()
-from . import _launch_stream, _lm_binding as _C  # noqa: E402
+from . import SELSCAN_BF16, _launch_stream, _lm_binding as _C  # noqa: E402
 
 
 def lm_abi_version() -> int:
@@ -160,8 +160,9 @@ def w4_matvec(x, qweight, scales, zeros=None, group=128, bias=None, out=None, st
     return _run(stream, _C.w4_matvec, x, qweight, scales, zeros, group, bias, out)
 
 
-def linear_attn_packed_workspace_bytes(tokens: int, nseq: int, max_seqlen: int, heads: int, dk: int, dv: int) -> int:
-    return int(lm_lib.linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv))
+def linear_attn_packed_workspace_bytes(tokens: int, nseq: int, max_seqlen: int, heads: int, dk: int, dv: int,
+                                       io_dtype: int = SELSCAN_BF16) -> int:
+    return int(lm_lib.linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv, io_dtype))
 
 
 def linear_attn_packed_fwd(q, k, v, log_decay, cu_seqlens, state=None, scale=1.0, slots=None, carry=None, max_seqlen=None,

@@ -40,12 +40,14 @@ def test_linear_attn_packed_refusals():
 
 def test_linear_attn_workspace():
     need = S.linear_attn_packed_workspace_bytes(20000, 1, 20000, 4, 64, 64)
-    if need:
-        big = dict(tokens=20000, nseq=1, nslots=1, longest=20000)
-        assert packed(**big, wsb=need - 1) == WORKSPACE and packed(**big, ws=None) == WORKSPACE and packed(**big, ws=A(7) + 8) == ALIGN
-        assert packed(**big, ws=A(6)) == ALIAS
+    assert need > 0 and S.linear_attn_packed_workspace_bytes(64, 1, 64, 4, 64, 64) == 0
+    big = dict(tokens=20000, nseq=1, nslots=1, longest=20000)
+    assert packed(**big, wsb=need - 1) == WORKSPACE and packed(**big, ws=None) == WORKSPACE and packed(**big, ws=A(7) + 8) == ALIGN
+    assert packed(**big, ws=A(6)) == ALIAS
+    # what is kept of segments is kept of those that another follows: sequences do not count
+    assert need == S.linear_attn_packed_workspace_bytes(20000, 5000, 20000, 4, 64, 64)
     for bad in ((0, 1, 10, 4, 64, 64), (10, 0, 10, 4, 64, 64), (10, 1, 0, 4, 64, 64), (10, 1, 10, 0, 64, 64), (10, 1, 10, 4, 0, 64),
-                (10, 1, 10, 4, 64, 0), (10, 1, 10, 4, 300, 64), (-5, -5, -5, -5, -5, -5)):
+                (10, 1, 10, 4, 64, 0), (10, 1, 10, 4, 300, 64), (-5, -5, -5, -5, -5, -5), (20000, 1, 20000, 4, 64, 64, 7)):
         assert S.linear_attn_packed_workspace_bytes(*bad) == 0
 
 
