@@ -550,9 +550,9 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
 
 // One token per sequence: S' = e^g S + k v^T, out = scale q^T S'.  The state is read and written once, and that bounds it: 4 x CG
 // columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in each thread, all of them in flight at
-// once.  128 rows x 64 heads of 128 x 64 (fp32 states of 268 MB): 114 us, 4.7 TB/s of the 5.1 of a copy.  A decay near 1 is taken
+// once.  128 rows x 64 heads of 128 x 64 (fp32 states of 268 MB): 109 us, 4.9 TB/s of the 5.1 of a copy.  A decay near 1 is taken
 // as S + (e^g - 1) S: rounded to 24 bits itself, it would be off in the same direction at every step.
-template <typename T, int CG, int ND, bool VEC>
+template <typename T, int CG, int ND, bool VEC, bool PAST>
 __global__ __launch_bounds__(256) void la_step(LaParams p) {
     __shared__ float4 part[4][CG];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cg = lane % CG;
@@ -571,8 +571,10 @@ __global__ __launch_bounds__(256) void la_step(LaParams p) {
         const bool on = d0 + i < p.dk && slot >= 0;
         const float *at = cache + (int64_t)(d0 + i) * p.dv;
         if constexpr (VEC) {
-            const float4 w = on && nc > 0 ? *(const float4 *)at : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[i][0] = w.x, S[i][1] = w.y, S[i][2] = w.z, S[i][3] = w.w;
+            F4 w = {0.f, 0.f, 0.f, 0.f};
+            if (on && nc > 0) w = *(const F4 *)at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[i][j] = w[j];
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) S[i][j] = on && j < nc ? at[j] : 0.f;
@@ -600,7 +602,11 @@ __global__ __launch_bounds__(256) void la_step(LaParams p) {
         if (d0 + i < p.dk && slot >= 0) {
             float *at = cache + (int64_t)(d0 + i) * p.dv;
             if constexpr (VEC) {
-                if (nc > 0) *(float4 *)at = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+                const F4 w = {S[i][0], S[i][1], S[i][2], S[i][3]};
+                if (nc > 0) {
+                    if constexpr (PAST) __builtin_nontemporal_store(w, (F4 *)at);
+                    else *(F4 *)at = w;
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -734,9 +740,16 @@ int launch_packed_keys(const LaParams &p, int64_t blocks, void *stream) {
                          : launch_packed<T, 8, VEC>(p, blocks, stream);
 }
 
+// Bytes of states from which on they are written past the caches, of which the last holds as many: 256 MB of them are 89 us either way
+// (114 and 109 where other work comes between), 400 MB 133 us for 165, 800 MB 289 for 327; 192 MB 69 for 68.  (Read past
+// them too: 150 and 303.)
+constexpr int64_t kPast = INT64_C(256) << 20;
+
 template <typename T, int CG, int ND>
 int launch_step(const LaParams &p, int64_t blocks, bool vec, void *stream) {
-    return enqueue(vec ? la_step<T, CG, ND, true> : la_step<T, CG, ND, false>, dim3((unsigned)blocks), dim3(256), p, stream);
+    const bool past = blocks * 4 * CG * p.dk * 4 >= kPast;
+    return enqueue(!vec ? la_step<T, CG, ND, false, false> : past ? la_step<T, CG, ND, true, true> : la_step<T, CG, ND, true, false>,
+                   dim3((unsigned)blocks), dim3(256), p, stream);
 }
 
 }  // namespace

@@ -324,3 +324,23 @@ def test_logits_past_32_bit_offsets(rows, vocab, dtype):
         alone = SA.check(x[r:r + 1], u[r:r + 1], 0.9, 0, 0.9, 0.001)
         for a, b in zip(got, alone):
             assert torch.equal(a[r:r + 1], b), r
+
+
+def test_states_past_the_caches_are_the_rows_in_parts():
+    import torch
+
+    import selective_state_space_51_amd as S
+    rows, H, dk, dv = 131, 32, 128, 128
+    assert rows * H * dk * dv * 4 >= 256 << 20 > (rows + 1) // 2 * H * dk * dv * 4
+    _say("many states", rows)
+    i = LA.make([1] * rows, H, 2, dk, dv, "bf16", nslots=rows + 3, seed=6)
+    slots = torch.randperm(rows + 3, device="cuda")[:rows].int()
+    slots[5] = -1
+    a, b = i["state"].clone(), i["state"].clone()
+    whole = S.linear_attn_step(i["q"], i["k"], i["v"], i["g"], a, slots=slots)
+    half = (rows + 1) // 2
+    parts = [S.linear_attn_step(i["q"][p], i["k"][p], i["v"][p], i["g"][p], b, slots=slots[p]) for p in (slice(0, half), slice(half, rows))]
+    torch.cuda.synchronize()
+    assert torch.equal(whole, torch.cat(parts)) and torch.equal(a, b) and not torch.equal(a, i["state"])
+    few = dict(i, lens=[1] * 4, **{n: i[n][:4] for n in "qkvg"}, state=i["state"][slots[:4].long()])
+    LA.compare(few, whole[:4], a[slots[:4].long()], LA.reference(few, None, [1] * 4))
