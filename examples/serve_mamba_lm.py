@@ -1,6 +1,6 @@
 """A small Mamba language model (random weights) that reads packed prompts, generates token by token from the cached
-states, scores what it generated, and takes a training step of its last norm: the operators of include/selscan_lm.h
-as a program would run them.
+states, forks what it has read into several continuations that are drawn at random, scores what it generated, and takes a
+training step of its last norm: the operators of include/selscan_lm.h as a program would run them.
 
     python examples/serve_mamba_lm.py [--layers 4] [--width 512] [--tokens 16]
 
@@ -129,6 +129,27 @@ class MambaLM:
                 x, residual = self.step(idx[:, 0], slots)
         return tuple(torch.stack(o, 1) for o in zip(*out))
 
+    def continuations(self, prompts, n, count, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, generator=None):
+        """`count` continuations of n tokens drawn for each prompt, which is read once: ([sequences * count][n] tokens, their
+        log probabilities among those that could be drawn).  Takes as many entries of the cache as there are continuations."""
+        if not all(prompts):
+            raise ValueError("a prompt without tokens has no last one to go on from")
+        dev = self.embed.device
+        slots = torch.arange(len(prompts) * count, dtype=torch.int32, device=dev)
+        first = slots[::count].contiguous()
+        x, residual, last = self.prefill(prompts, first)
+        src, caches = first.repeat_interleave(count), [*self.conv, *self.state]
+        S.cache_entries_copy(caches, src, slots)
+        x, residual = x[last].repeat_interleave(count, 0), residual[last].repeat_interleave(count, 0)
+        out = []
+        for i in range(n):
+            u = torch.rand(len(slots), device=dev, generator=generator)
+            token, logp, _ = S.token_sample(self.logits(x, residual), u, temperature, top_k, top_p, min_p)
+            out.append((token, logp))
+            if i + 1 < n:
+                x, residual = self.step(token, slots)
+        return tuple(torch.stack(o, 1) for o in zip(*out))
+
     def score(self, sequences):
         """Log probability of every token of `sequences` given those before it (0 for the first of each)."""
         x, residual, last = self.prefill(sequences, list(range(len(sequences))))
@@ -172,6 +193,9 @@ def main():
     tokens, logp, ent = m.generate(prompts, a.tokens)
     for p, t, l, e in zip(prompts, tokens.tolist(), logp, ent):
         print(f"prompt of {len(p):3d} -> {t[:8]}...  mean log probability {float(l.mean()):.3f}, entropy {float(e.mean()):.3f}")
+    drawn, _ = m.continuations(prompts[:2], a.tokens, 4, temperature=0.9, top_k=50, top_p=0.95)
+    for i, t in enumerate(drawn.tolist()):
+        print(f"prompt of {len(prompts[i // 4]):3d}, drawn -> {t[:8]}...")
     whole = [p + t for p, t in zip(prompts, tokens.tolist())]
     score = m.score(whole)
     at = len(whole[0]) - 1  # the first sequence's generated tokens, scored in one pass over it

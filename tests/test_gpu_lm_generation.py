@@ -344,3 +344,24 @@ def test_states_past_the_caches_are_the_rows_in_parts():
     assert torch.equal(whole, torch.cat(parts)) and torch.equal(a, b) and not torch.equal(a, i["state"])
     few = dict(i, lens=[1] * 4, **{n: i[n][:4] for n in "qkvg"}, state=i["state"][slots[:4].long()])
     LA.compare(few, whole[:4], a[slots[:4].long()], LA.reference(few, None, [1] * 4))
+
+
+def test_drawn_continuations_of_the_example():
+    """At temperature 0 they are the greedy ones; without limits a drawn token's log probability is the one that a pass over the
+    whole sequence gives (fp32 through two layers; 1e-3 as in the example's own tests)."""
+    import torch
+
+    from tests.test_gpu_lm_example import _example, _prompts
+    m = _example().MambaLM(vocab=301, width=128, layers=2, slots=6, dtype=torch.float32, seed=3)
+    prompts = _prompts((3, 40))
+    greedy, _, _ = m.generate(prompts, 5)
+    same, logp = m.continuations(prompts, 5, 3, temperature=0.0)
+    assert torch.equal(same, greedy.repeat_interleave(3, 0)) and not logp.any()
+    drawn, logp = m.continuations(prompts, 5, 3, generator=torch.Generator(device="cuda").manual_seed(1))
+    whole = [prompts[i // 3] + t for i, t in enumerate(drawn.tolist())]
+    score, at = m.score(whole), 0
+    for i, w in enumerate(whole):
+        assert float((score[at + len(w) - 6:at + len(w) - 1] - logp[i]).abs().max()) <= 1e-3
+        at += len(w)
+    with pytest.raises(ValueError, match="without tokens"):
+        m.continuations([[1], []], 2, 2)
