@@ -167,9 +167,13 @@ __device__ __forceinline__ u64 weight_of(const SampleLds &m, float x, double top
 // them, one in each thread.  Else the same is done on the row itself; top-p on bf16 logits by counting equal ones first, so that a
 // weight is formed for each value and not for each token.
 //
-// A pass over a row costs a compute unit an instruction's issue for every 64 logits' step, and most of the code runs once or twice
-// for a row and has to be fetched for that: loops are not unrolled over rounds.  Weights of eight logits are formed side by
-// side, without a branch between them, or not at all where no lane of the wave has one that counts.
+// Instructions bound it: each logit passes three to six passes, 4 instructions in the first and about 30 where its weight is formed.
+// 1,000 rows of 32,001 fp32 logits without limits take 59 us (vector units busy for 73 %, 2.2 TB/s), 64 of 131,072 bf16 with top-p 67
+// (83 % of 64 compute units), 256 of 50,280 with mixed settings 36, three of them 21 (the chain of passes of one row).  A pass over a
+// row costs a compute unit an instruction's issue for every 64 logits' step, and most of the code runs once or twice for a row and has to be
+// fetched for that: loops are not unrolled over rounds.  Weights of eight logits are formed
+// side by side, without a branch between them, or not at all where no lane of the wave has one that counts (one after another for
+// those that count: 64 rows 66 us for 67, 256 rows 39 for 36).
 template <typename T, int kWaves, bool HELD>
 __global__ __launch_bounds__(64 * kWaves, 4) void sample_row(SampleParams p) {
     constexpr int kThreads = 64 * kWaves, kOwn = kBins / kThreads, kFew = kThreads;
@@ -461,14 +465,36 @@ __global__ __launch_bounds__(64 * kWaves, 4) void sample_row(SampleParams p) {
                     const int bin = (int)m.found[0], to = bin - 2048;
                     const uint32_t some = (uint32_t)m.found[1], n = counts[bin];
                     const float v = __uint_as_float((uint32_t)((to >= 0 ? to : ~to) + lowest) << 16 | (to >= 0 ? 0x80000000u : 0u));
-                    if (some == n || some <= (uint32_t)kFew) {
-                        if (some < n) {
-                            take([&](float f) { return f == v; });
-                            bi = m.few_at[some - 1];
+                    if (some < n) {
+                        const auto picked = [&](const Raw8<T> &r) {
+                            uint32_t bits = 0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) bits |= (uint32_t)(raw_f32(r, e) == v) << e;
+                            return bits;
+                        };
+                        uint32_t mine = 0;
+                        each([&](int, const Raw8<T> &r) { mine += __popc(picked(r)); });
+                        u64 all;
+                        const uint32_t first = (uint32_t)block_scan<kWaves>(m, mine, 1, all);
+                        uint32_t place = (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
+                        // (the wave that has the last one that stays)
+                        if (place < some && some <= (uint32_t)__builtin_amdgcn_readlane((int)(first + mine), 63)) {
+                            each([&](int i, const Raw8<T> &r) {
+                                uint32_t bits = picked(r);
+                                if (!__any(bits != 0) || place >= some) return;
+                                const uint32_t own = __popc(bits), up = place + (uint32_t)wave_scan(own, Add());
+                                if (up - own < some && some <= up) {
+                                    for (uint32_t j = up - own + 1; j < some; ++j) bits &= bits - 1;
+                                    m.found[0] = (u64)(i + __builtin_ctz(bits));
+                                }
+                                place = (uint32_t)__builtin_amdgcn_readlane((int)up, 63);
+                            });
                         }
-                        bv = v;
-                        more = false;
+                        lds_barrier();
+                        bi = (int)m.found[0];
                     }
+                    bv = v;
+                    more = false;
                 }
             }
         }
@@ -680,7 +706,10 @@ extern "C" int token_sample(const void *logits, int64_t logits_stride, const flo
     int bits = 0;
     while ((INT64_C(1) << bits) < vocab) ++bits;
     p.shift = 62 - bits < 51 ? 62 - bits : 51;  // sums stay below 2^63, weights below 2^52
-    const bool two = rows > 512;  // two workgroups to a compute unit
+    // Up to 256 rows each has a compute unit, 16 waves and, if it fits, a place in LDS (200 rows of 32,001 bf16 17.3 us, with 8 waves that
+    // read it again 19.5).  More have 8 waves, several to a compute unit, so that one's barriers pass while another works (512 rows 30.5
+    // us for 33, 1,024 53 for 62, with top-p 88 for 95, fp32 122 for 139; 400 rows of 131,072 bf16 149 for 156).
+    const bool two = rows > 256;
     if (io_dtype == SELSCAN_BF16) return two ? launch_sample<uint16_t, 8>(p, rows, stream) : launch_sample<uint16_t, 16>(p, rows, stream);
     return two ? launch_sample<float, 8>(p, rows, stream) : launch_sample<float, 16>(p, rows, stream);
 }
