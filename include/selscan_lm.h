@@ -25,7 +25,9 @@
  *    (SELSCAN_E_UNSUPPORTED, before any launch).  Workgroups of 256 are: of the packed scan, 64 channels of a sequence or of one of
  *    its segments; of the packed convolution, 2,048 channels of at least 4 tokens; of the log probabilities, a row of up to 8,192
  *    logits or 4,096 and more of a longer one's; of the norm, four rows up to width 1,024, one up to 8,192 (beyond, 1,024
- *    threads each: 4,194,303 rows); of the 4-bit product, 64 rows of the matrix.
+ *    threads each: 4,194,303 rows); of the 4-bit product, 64 rows of the matrix; of linear attention, 64 columns of a head's values of a
+ *    sequence or of one of its segments, and of its step of a row (16 or 32 columns of heads that are no wider).  Sampling takes
+ *    4,194,303 rows; a move of entries is counted in pieces of 16 bytes to 1 KB of an entry, of 256 to 1,024 threads.
  */
 #ifndef SELSCAN_LM_H
 #define SELSCAN_LM_H
@@ -221,6 +223,7 @@ int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *
  *   log_decay  : [tokens][heads] fp32, row stride decay_stride; decay_stride 0: one row for all tokens (a fixed decay for
  *                each head).  Usually <= 0; -infinity clears the state before the token's own product is added (the
  *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow.
+ *                An infinity in q, k, v or a state comes out as an infinity or as NaN, from its token on.
  *   state      : [nslots][heads][dk][dv] fp32, 16-byte aligned, nullable (no cache); in place
  *   dk         : 1..256, dv : 1..1024, heads a multiple of groups (SELSCAN_E_UNSUPPORTED, SELSCAN_E_SHAPE); row strides at
  *                most 2^23 (SELSCAN_E_UNSUPPORTED)
@@ -264,8 +267,9 @@ int linear_attn_step(const void *q, int64_t q_stride, const void *k, int64_t k_s
  *   kept    : [rows] int32, how many tokens stay
  *   vocab   : 1..2^21 (SELSCAN_E_SHAPE, SELSCAN_E_UNSUPPORTED)
  * Weights are whole multiples of 2^-45 (for a vocab of 2^17; of 2^-62 times the vocab rounded up to a power of 2, and of 2^-51 at
- * least), summed as whole numbers: what is drawn does not depend on how a row is split.  A logit of -infinity never stays.  A row of nothing else has token -1, logprob -infinity and
- * kept 0; a row with a NaN or +infinity has token -1, logprob NaN and kept 0.
+ * least), summed as whole numbers: what is drawn does not depend on how a row is split.  A logit of -infinity never stays.  A
+ * row of nothing else has token -1, logprob -infinity and kept 0; a row with a NaN or +infinity has token -1, logprob NaN and kept
+ * 0.
  */
 int token_sample(const void *logits, int64_t logits_stride, const float *uniform, const float *temperature,
                  float temperature_all, const int32_t *top_k, int top_k_all, const float *top_p, float top_p_all,
