@@ -14,6 +14,7 @@ struct LaParams {
     Seqs s;
     int64_t q_stride, k_stride, v_stride, decay_stride;
     int heads, share, dk, dv, vblocks;  // share: heads of a group
+    int round;  // whole sequences are dealt out longest first (64: a round of all), or (0) as they come
     float scale;
     // sequences in segments of `size` tokens: what each entry holds (the state at the end of a segment that another
     // follows, from zero but for a sequence's first), and what its decays make of a state before it
@@ -452,7 +453,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
 // the others' segments from the states that they start from.  (Outputs of every first segment in the first launch make that
 // launch as long as the second: 4,097 tokens x 24 heads of 64 x 64 fp32 take 60 us, and took 70.)
 // What bounds it: the chunks of the longest sequence or segment, one after another, 64 tokens in 2.4 us (bf16, 64 x 64) to
-// 4.1 us (bf16, 128 x 64, two workgroups to a compute unit).  27,591 tokens of 24 prompts x 64 heads of 128 x 64 bf16: 267 us, 2.1 TB/s of what
+// 4.1 us (bf16, 128 x 64, two workgroups to a compute unit).  27,591 tokens of 24 prompts x 64 heads of 128 x 64 bf16: 260 us, 2.1 TB/s of what
 // has to pass; LDS is busy for half of the clocks, the vector units for 40 %.  Two 64-column pieces or two heads in a workgroup of
 // eight waves 302 us, 32 columns per wave 409 (fewer waves, each with longer chains), chunks of 32 tokens 281, and segments of 512,
 // 1,024 or 2,048 tokens are slower there than whole sequences.  fp32 chunks are of 32 tokens: 31 KB of LDS at 64
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, gq = lane >> 4;
     const int vb = blockIdx.x % p.vblocks, hs = blockIdx.x / p.vblocks, h = hs % p.heads, seg = hs / p.heads;
     const bool split = p.seg != nullptr;
-    const Segment g = split ? find_segment(p.s, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane) : whole_sequence(p.s, seg);
+    const Segment g = split ? find_segment(p.s, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane) : p.round ? dealt_sequence(p.s, seg, p.round, lane) : whole_sequence(p.s, seg);
     const int first = split ? g.j * p.size : 0;
     if (g.j > 0 && first >= g.len) return;
     const bool last = !split || g.len - first <= p.size, only = last && g.j == 0;
@@ -788,6 +789,10 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
         p.factor = (float2 *)workspace;
         p.seg = (float *)((char *)workspace + factors_bytes(p.entries, heads));
     }
+    // Whole sequences longest first where they take more workgroups than there are compute units (24 prompts, 27,591 tokens x 64
+    // heads of 128 x 64 bf16 in rising order 383 us as they come and 266 dealt out, in three other orders 312..342 and 253..258; fp32 992
+    // and 700.  With every second round of sequences in rising order, as the scan has them, 272 and 260..264.)
+    else if (nseq > 1 && nseq <= 64 && nseq * per > 256) p.round = 64;
     if (mul_size(pieces, per) < 0 || !grid_fits(pieces * per, 256) || (need && !grid_fits(heads * dk * dv / 64 + 1, 64))) return SELSCAN_E_UNSUPPORTED;
     const int64_t e = io_dtype == SELSCAN_BF16 ? 8 : 4, word = io_dtype == SELSCAN_BF16 ? 2 : 1;
     const bool vec = dk % e == 0 && dv % e == 0 && q_stride % word == 0 && k_stride % word == 0 && v_stride % word == 0 &&

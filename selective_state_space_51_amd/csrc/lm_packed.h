@@ -92,7 +92,7 @@ __device__ __forceinline__ Segment whole_sequence(const Seqs &q, int s) {
 
 // The sequence that stands at place `place` when whole sequences are dealt to the chip (up to 64 of them): longest first, and
 // every second round of `round` sequences (those whose workgroups fill the compute units once) in rising order, so that the
-// units that got a round's longest get the next one's shortest. Twenty-four prompts of 1 to 4,096 tokens, 27,591 in all, x 4,096
+// units that got a round's longest get the next one's shortest; `round` of 64 or more: longest first. Twenty-four prompts of 1 to 4,096 tokens, 27,591 in all, x 4,096
 // channels: 636 us against 675 as they come, and 532 to 566 against 600 to 708 in four other orders of the same prompts.
 __device__ __forceinline__ Segment dealt_sequence(const Seqs &q, int place, int round, int lane) {
     const int n = q.nseq, i = lane < n ? lane : n - 1;

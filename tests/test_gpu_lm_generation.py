@@ -365,3 +365,25 @@ def test_drawn_continuations_of_the_example():
         at += len(w)
     with pytest.raises(ValueError, match="without tokens"):
         m.continuations([[1], []], 2, 2)
+
+
+@pytest.mark.parametrize("nseq", [5, 63, 64, 65])
+def test_prompts_dealt_out_by_length_are_the_prompts_alone(nseq):
+    """More whole sequences than compute units have room for at once, of mixed and equal lengths and empty ones: each gives the
+    bits that it gives alone."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    H = 60
+    lens = [int(n) for n in np.random.default_rng(nseq).choice([0, 1, 40, 64, 64, 130, 200], nseq)]
+    _say("dealt", nseq, lens[:8])
+    assert nseq * H > 256 and S.linear_attn_packed_workspace_bytes(sum(lens), nseq, max(lens), H, 16, 32) == 0
+    i = LA.make(lens, H, 1, 16, 32, "bf16", nslots=nseq, seed=nseq)
+    slots = list(np.random.default_rng(1).permutation(nseq))
+    out, st = LA.run(i, slots, [s % 2 for s in range(nseq)])
+    for s in sorted(set(range(0, nseq, 9)) | {1, 2, nseq - 1}):
+        b = sum(lens[:s])
+        own = {n: i[n][b:b + lens[s]] for n in "qkvg"}
+        one = dict(i, lens=[lens[s]], cu=torch.tensor([0, lens[s]], dtype=torch.int32, device="cuda"), state=i["state"][slots[s]:slots[s] + 1], **own)
+        alone, st1 = LA.run(one, None, [s % 2])
+        assert torch.equal(alone, out[b:b + lens[s]]) and torch.equal(st1[0], st[slots[s]]), s
