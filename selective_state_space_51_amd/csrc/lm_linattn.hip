@@ -467,7 +467,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     const bool split = p.seg != nullptr;
     const Segment g = split ? find_segment(p.s, seg, [&](int v) { return (int)fdiv((uint32_t)v, p.dsize); }, lane) : p.round ? dealt_sequence(p.s, seg, p.round, lane) : whole_sequence(p.s, seg);
     const int first = split ? g.j * p.size : 0;
-    if (g.j > 0 && first >= g.len) return;
+    if (g.j < 0 || (g.j > 0 && first >= g.len)) return;
     const bool last = !split || g.len - first <= p.size, only = last && g.j == 0;
     const int c0 = vb * 64, c = c0 + 16 * wave + l;
     const int64_t head = (int64_t)p.dk * p.dv;

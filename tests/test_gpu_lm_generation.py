@@ -387,3 +387,43 @@ def test_prompts_dealt_out_by_length_are_the_prompts_alone(nseq):
         one = dict(i, lens=[lens[s]], cu=torch.tensor([0, lens[s]], dtype=torch.int32, device="cuda"), state=i["state"][slots[s]:slots[s] + 1], **own)
         alone, st1 = LA.run(one, None, [s % 2])
         assert torch.equal(alone, out[b:b + lens[s]]) and torch.equal(st1[0], st[slots[s]]), s
+
+
+@pytest.mark.parametrize("cu", [[700, 2300], [1500, 1500, 2300], [0, 1200, 100, 2300, 50], [2300, 0, 2300, 0], [900, 100, 60, 20]])
+def test_segments_of_offsets_that_start_late_or_fall(cu):
+    """Offsets that begin past 0, or fall, in a call of several segments: sequences before the first fall are right, and nothing is
+    written outside the output and the cache."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    T, H, n = 2300, 2, len(cu) - 1
+    _say("late or falling", cu)
+    assert S.linear_attn_packed_workspace_bytes(T, n, T, H, 32, 32) > 0
+    i = LA.make([T], H, 1, 32, 32, "bf16", nslots=n, seed=8)
+    guard, cache = torch.full((T + 800, H, 32), 7.0, device="cuda", dtype=torch.bfloat16), torch.full((n + 8, H, 32, 32), 7.0, device="cuda")
+    out, st = guard[400:T + 400], cache[4:n + 4]
+    need = S.linear_attn_packed_workspace_bytes(T, n, T, H, 32, 32)
+    ws = torch.full((need + 65536,), 7, dtype=torch.uint8, device="cuda")
+    S.linear_attn_packed_fwd(i["q"], i["k"], i["v"], i["g"], torch.tensor(cu, dtype=torch.int32, device="cuda"), st, out=out,
+                             max_seqlen=T, workspace=ws[32768:need + 32768])
+    torch.cuda.synchronize()
+    assert bool((guard[:400] == 7).all()) and bool((guard[T + 400:] == 7).all())
+    assert bool((cache[:4] == 7).all()) and bool((cache[n + 4:] == 7).all())
+    assert bool((ws[:32768] == 7).all()) and bool((ws[need + 32768:] == 7).all())
+    if sorted(cu) == cu:
+        for s in range(n):
+            b, e = cu[s], cu[s + 1]
+            one = dict(i, lens=[e - b], **{x: i[x][b:e] for x in "qkvg"}, state=torch.zeros_like(st[:1]))
+            LA.compare(one, out[b:e], st[s:s + 1], LA.reference(one))
+
+
+@pytest.mark.parametrize("carry", [None, [1, 0, 1]])
+def test_prompts_without_tokens(carry):
+    import torch
+
+    import selective_state_space_51_amd as S
+    i = LA.make([0, 0, 0], 2, 1, 32, 32, "bf16", nslots=3)
+    out, st = LA.run(i, None, carry)
+    assert out.shape == (0, 2, 32)
+    for s in range(3):
+        assert torch.equal(st[s], i["state"][s]) if carry and carry[s] else not st[s].any()
