@@ -168,8 +168,8 @@ __device__ __forceinline__ u64 weight_of(const SampleLds &m, float x, double top
 // weight is formed for each value and not for each token.
 //
 // Instructions bound it: each logit passes three to six passes, 4 instructions in the first and about 30 where its weight is formed.
-// 1,000 rows of 32,001 fp32 logits without limits take 59 us (vector units busy for 73 %, 2.2 TB/s), 64 of 131,072 bf16 with top-p 67
-// (83 % of 64 compute units), 256 of 50,280 with mixed settings 36, three of them 21 (the chain of passes of one row).  A pass over a
+// 1,000 rows of 32,001 fp32 logits without limits take 59 us (vector units busy for 70 %, 2.2 TB/s), 64 of 131,072 bf16 with top-p 67
+// (80 % of 64 compute units), 256 of 50,280 with mixed settings 36, three of them 21 (the chain of passes of one row).  A pass over a
 // row costs a compute unit an instruction's issue for every 64 logits' step, and most of the code runs once or twice for a row and has to be
 // fetched for that: loops are not unrolled over rounds.  Weights of eight logits are formed
 // side by side, without a branch between them, or not at all where no lane of the wave has one that counts (one after another for
