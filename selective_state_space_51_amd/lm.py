@@ -162,6 +162,8 @@ def w4_matvec(x, qweight, scales, zeros=None, group=128, bias=None, out=None, st
 
 def linear_attn_packed_workspace_bytes(tokens: int, nseq: int, max_seqlen: int, heads: int, dk: int, dv: int,
                                        io_dtype: int = SELSCAN_BF16) -> int:
+    """Bytes of linear_attn_packed_fwd's workspace (it allocates one itself if none is given) for inputs of io_dtype, SELSCAN_BF16
+    or SELSCAN_F32; 0 where sequences are read whole."""
     return int(lm_lib.linear_attn_packed_workspace_bytes(tokens, nseq, max_seqlen, heads, dk, dv, io_dtype))
 
 
