@@ -558,8 +558,16 @@ __global__ __launch_bounds__(64 * kWaves, 4) void sample_row(SampleParams p) {
         lds_barrier();
         const int count = m.count;
         if (bin < kBins && count > kList) {
-            hi = block_reduce<kWaves>(m, order_of(most_v), 0, Larger()) << 32 | 0xFFFFFFFFu;
-            lo = (u64)(~(uint32_t)block_reduce<kWaves>(m, (uint32_t)~order_of(least_v), 1, Larger())) << 32 | (uint32_t)~(p.vocab - 1);
+            // The entry numbers of the bin: those of the values in it and, where it was one of entry numbers, no others than
+            // its own (what lies before it is in the base; a value of more than 2^19 tokens takes two such rounds).  Each of
+            // these leaves a 2,048th of the numbers, so that six of them end the search.
+            u64 first = block_reduce<kWaves>(m, order_of(most_v), 0, Larger()) << 32 | 0xFFFFFFFFu;
+            u64 last = (u64)(~(uint32_t)block_reduce<kWaves>(m, (uint32_t)~order_of(least_v), 1, Larger())) << 32 | (uint32_t)~(p.vocab - 1);
+            if (sh >= 0) {
+                const u64 from = hi - ((u64)bin << sh), to = from - ((1ull << sh) - 1);
+                first = first < from ? first : from, last = last > to ? last : to;
+            }
+            hi = first, lo = last;
             sh = 64 - __builtin_clzll((hi - lo) | 1) - 11;
             sh = sh < 0 ? 0 : sh;
             continue;

@@ -186,3 +186,21 @@ def test_largest_vocabulary():
     x, u = logits(2, 1 << 21, "bf16", seed=12)
     check(x, u, 1.0, 0, 0.9, 0.0)
     check(x, u, 1.0, 1000, 1.0, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [1 << 19, (1 << 19) + 1, (1 << 20) + 3, 1 << 21])
+def test_ties_of_large_vocabularies(vocab, dtype):
+    """Borders of top-k and top-p among so many tokens of one value that they are told apart in more than one round."""
+    import torch
+    io = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    u = torch.rand(3, generator=g, device="cuda")
+    # one value, two values next to each other, and four
+    x = torch.zeros(3, vocab, device="cuda", dtype=io)
+    x[1] = 1 - torch.finfo(io).eps * torch.randint(0, 2, (vocab,), generator=g, device="cuda") / 2
+    x[2] = torch.randint(0, 4, (vocab,), generator=g, device="cuda")
+    for T, k, p, m in ((1.0, vocab // 3, 1.0, 0.0), (1.0, vocab - 1, 1.0, 0.0), (1.0, 0, 0.37, 0.0), (1.0, 0, 0.9, 0.0),
+                       (1.0, vocab // 3, 0.9, 0.0), (2.0, 70_000, 0.37, 0.01)):
+        _say("large ties", vocab, dtype, T, k, p, m)
+        check(x, u, T, k, p, m)
