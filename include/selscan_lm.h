@@ -222,7 +222,10 @@ int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *
  *   v          : [tokens][heads][dv] io_dtype, row stride v_stride;  out : [tokens][heads][dv], contiguous
  *   log_decay  : [tokens][heads] fp32, row stride decay_stride; decay_stride 0: one row for all tokens (a fixed decay for
  *                each head).  Usually <= 0; -infinity clears the state before the token's own product is added (the
- *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow.
+ *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow (up to 16384; beyond
+ *                are taken as that): a state of 0 stays 0 however large they are, others come out as the numbers that they grow to,
+ *                infinities where fp32 ends.  Where those of a block of 64 tokens add up to more than 44 the block is read
+ *                token by token.
  *                An infinity in q, k, v or a state comes out as an infinity or as NaN, from its token on.
  *   state      : [nslots][heads][dk][dv] fp32, 16-byte aligned, nullable (no cache); in place
  *   dk         : 1..256, dv : 1..1024, heads a multiple of groups (SELSCAN_E_UNSUPPORTED, SELSCAN_E_SHAPE); row strides at

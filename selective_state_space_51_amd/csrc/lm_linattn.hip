@@ -6,6 +6,12 @@ namespace {
 
 constexpr int kMaxKeys = 256, kMaxValues = 1024;
 
+// 2^x for what multiplies the state before a segment: (hi + lo) 2^n, n of 0 unless x is above kWhole
+struct alignas(16) Factor {
+    float hi, lo;
+    int n;
+};
+
 struct LaParams {
     const void *q, *k, *v;
     const float *decay;
@@ -19,14 +25,27 @@ struct LaParams {
     // sequences in segments of `size` tokens: what each entry holds (the state at the end of a segment that another
     // follows, from zero but for a sequence's first), and what its decays make of a state before it
     float *seg;    // [entries][heads][dk][dv]
-    float2 *factor; // [entries][heads], in two parts
+    Factor *factor; // [entries][heads]
     int size, entries;
     FastDiv dsize;
 };
 
 // A log decay as it is used: one of -infinity, or below any whose exponential is not 0 in fp32, is a number of which a
-// chunk's worth can be added and subtracted again.
-__device__ __forceinline__ float finite_decay(float g) { return g < -16384.f ? -16384.f : g; }
+// chunk's worth can be added and subtracted again; so is one of infinity.
+__device__ __forceinline__ float finite_decay(float g) { return g < -16384.f ? -16384.f : g > 16384.f ? 16384.f : g; }
+
+// Exponents (base 2) up to which a power is formed whole.  Powers beyond are 2^(x - n) 2^n with n = floor(x), and what is multiplied
+// takes the two one after another: a state of zero stays zero, and a small one comes out as the number that it grows to.  (Half of
+// what fp32 holds: the power is multiplied by values and keys before the sums.)
+constexpr float kWhole = 64.f;
+constexpr double kLog2e64 = 1.44269504088896340735992468100;
+// the power of a segment's sum (one past 2^20 counts as 2^20: zero alone survives it)
+__device__ __forceinline__ Factor factor_of(double x) {
+    const int n = x > (double)kWhole ? __double2int_rd(x < 1048576. ? x : 1048576.) : 0;
+    const double f = exp2(n ? x < 1048576. ? x - n : 0. : x);
+    const float hi = (float)f;
+    return {hi, (float)(f - (double)hi), n};
+}
 
 typedef float F4 __attribute__((ext_vector_type(4)));
 typedef __bf16 B8 __attribute__((ext_vector_type(8)));
@@ -76,9 +95,10 @@ struct Chunk {
     static constexpr int LQ = BF ? D + (KB >= 4 ? 40 : 8) : D + 4, LV = 64 + E, LP = C + E;
     static constexpr int NQ = C * D / E / 256, NV = C * 64 / E / 256;  // 16-byte pieces of a thread
     T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP];
-    struct Decay {
+    struct alignas(16) Decay {
         float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
         float fh, fl;              // 2^G_C in two parts
+        int grows;                 // decays above 0 add up to more than kWhole: token t's power is gh[t] 2^gl[t]
     } decay[2];                    // of this chunk and the next
     // row of the state that register r of tile d has in lanes 16 g .. 16 g + 15
     static __device__ __forceinline__ int row_of(int d, int g, int r) {
@@ -183,7 +203,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
     double sum = 0.;
     const auto sum_decays = [&](typename M::Decay &to) {
         // sums of up to 64 x 16384 whose differences count: 64 bits, then two parts of 32
-        double G = (double)finite_decay(gr) * 1.44269504088896340735992468100;
+        double G = (double)finite_decay(gr) * kLog2e64;
         G += dpp_or_zero<0x111, 0xF>(G);
         G += dpp_or_zero<0x112, 0xF>(G);
         G += dpp_or_zero<0x114, 0xF>(G);
@@ -193,6 +213,21 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         const int64_t b = __double_as_longlong(G);
         const double all = __longlong_as_double((int64_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32 |
                                                 (uint32_t)__builtin_amdgcn_readlane((int)b, 63));
+        sum += all;
+        bool grows = false;
+        if (__any(gr > 0.f)) {
+            float up = gr > 0.f ? finite_decay(gr) * kLog2e : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) up += __shfl_xor(up, d);
+            grows = up > kWhole;
+        }
+        if (lane == 0) to.grows = grows;
+        if (grows) {
+            const double one = (double)finite_decay(gr) * kLog2e64;
+            const int n = __double2int_rd(one);
+            if (lane < C) to.gh[lane] = __builtin_amdgcn_exp2f((float)(one - n)), to.gl[lane] = (float)n;
+            return;
+        }
         if (lane < C) {
             const float hi = (float)G;
             to.gh[lane] = hi, to.gl[lane] = (float)(G - (double)hi);
@@ -200,7 +235,6 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         }
         const double f = exp2(all);
         if (lane == 0) to.fh = (float)f, to.fl = (float)(f - (double)(float)f);
-        sum += all;
     };
     // tiles of the scores that are this wave's: pair i is key tile jt and query tile tt, jt <= tt
     const auto pair_of = [&](int i, int &jt, int &tt) {
@@ -224,6 +258,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
     for (int first = 0; first < w.n; first += C, now ^= 1) {
         const typename M::Decay &dc = m.decay[now];
         lds_barrier();  // the chunk before is no longer read
+        const int grows = dc.grows;
         T *to = m.k + tid / PQ * M::LQ + tid % PQ * E, *qto = m.q + tid / PQ * M::LQ + tid % PQ * E;
 #pragma unroll
         for (int i = 0; i < M::NQ; ++i) {
@@ -237,6 +272,39 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
         if (sums && first + C < w.n) {
             sum_decays(m.decay[now ^ 1]);
             fetch_decay(first + 2 * C);
+        }
+        if (__builtin_amdgcn_readfirstlane(grows)) {
+            // Powers that products would not take: the recurrence, a token after another.  A lane has its column's rows, the four
+            // lanes of a column add up their parts of the output.
+            int self = lane;  // (known here alone: what is formed from it would take registers of the other path)
+            asm volatile("" : "+v"(self));
+            const int rows = w.n - first < C ? w.n - first : C, c = 16 * wave + (self & 15), g = self >> 4;
+            T *oto = out + first * out_stride + c;
+#pragma unroll 1
+            for (int t = 0; t < rows; ++t) {
+                const float e = dc.gh[t], x = Io<T>::f32(m.v[t * M::LV + c]);
+                const int n = (int)dc.gl[t];
+                float o = 0.f;
+#pragma unroll
+                for (int d = 0; d < 2 * KB; ++d) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = M::row_of(d, g, r);
+                        S[d][r] = fmaf(ldexpf(S[d][r], n), e, Io<T>::f32(m.k[t * M::LQ + row]) * x);
+                        if (w.outputs) o = fmaf(Io<T>::f32(m.q[t * M::LQ + row]), S[d][r], o);
+                    }
+                    // (four rows at a time, each kept where it was: the other registers hold the next chunk; without it up to 47 of a
+                    // wave's went to memory at every chunk of the other path)
+                    if constexpr (KB == 8) asm volatile("" : "+a"(S[d]));
+                    else asm volatile("" : "+v"(S[d]));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (!w.outputs) continue;
+                o += __shfl_xor(o, 16);
+                o += __shfl_xor(o, 32);
+                if (g == 0 && c < nv) oto[t * out_stride] = Io<T>::to(o * p.scale);
+            }
+            continue;
         }
         if (w.outputs) {
             // scores, keys down, so that a lane's four are adjacent in a row of p
@@ -492,10 +560,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     float *to = last ? cache : nullptr;
     if (LAUNCH == 0 && !last) {
         to = p.seg + entry * head;
-        if (threadIdx.x == 192 && vb == 0) {  // (of the wave that sums the decays)
-            const double f = exp2(total);
-            p.factor[entry] = make_float2((float)f, (float)(f - (double)(float)f));
-        }
+        if (threadIdx.x == 192 && vb == 0) p.factor[entry] = factor_of(total);  // (of the wave that sums the decays)
     }
     if (!to || c >= p.dv) return;
 #pragma unroll
@@ -528,12 +593,12 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
         if (n < 2 || !live) continue;
         const int64_t first = div(rg.t0);
         float *e = p.seg + first * entry + i;
-        const float2 *t = p.factor + first * p.heads + h;
+        const Factor *t = p.factor + first * p.heads + h;
         float S = e[0];
         constexpr int U = 16;  // loaded ahead
         for (int j0 = 1; j0 < n; j0 += U) {
             float ev[U];
-            float2 tv[U];
+            Factor tv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t j = j0 + u < n ? j0 + u : n - 1;
@@ -542,7 +607,8 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (j0 + u >= n) break;
-                S = fmaf(S, tv[u].x, fmaf(S, tv[u].y, ev[u]));
+                S = ldexpf(S, tv[u].n);
+                S = fmaf(S, tv[u].hi, fmaf(S, tv[u].lo, ev[u]));
                 e[(j0 + u) * entry] = S;
             }
         }
@@ -590,7 +656,16 @@ __global__ __launch_bounds__(256) void la_step(LaParams p) {
     for (int j = 0; j < 4; ++j) x[j] = j < nc ? Io<T>::f32(v[j]) : 0.f;
     const float decay = finite_decay(p.decay[row * p.decay_stride + h]);
     const bool slow = fabsf(decay) < 0.5f;
-    const float e = slow ? expm1f(decay) : __builtin_amdgcn_exp2f(decay * kLog2e);
+    float e = slow ? expm1f(decay) : __builtin_amdgcn_exp2f(decay * kLog2e);
+    if (decay >= 0.5f) {  // growth: the power in two parts, as in a chunk that grows
+        const double G = (double)decay * kLog2e64;
+        const int n = __double2int_rd(G);
+        e = __builtin_amdgcn_exp2f((float)(G - n));
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[i][j] = ldexpf(S[i][j], n);
+    }
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
@@ -720,7 +795,7 @@ int split_size(int64_t tokens, int64_t max_seqlen, int64_t heads, int64_t dv, in
 bool la_sizes(int64_t heads, int64_t dk, int64_t dv) {
     return heads > 0 && dk > 0 && dv > 0 && dk <= kMaxKeys && dv <= kMaxValues && heads <= kMaxStride;
 }
-size_t factors_bytes(int64_t entries, int64_t heads) { return ((size_t)entries * heads * 8 + 15) / 16 * 16; }
+size_t factors_bytes(int64_t entries, int64_t heads) { return ((size_t)entries * heads * sizeof(Factor) + 15) / 16 * 16; }
 
 constexpr int64_t kGridY = 65535;
 
@@ -786,7 +861,7 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
         p.dsize = make_div((uint32_t)p.size);
         p.entries = (int)(tokens / p.size);
         pieces = tokens / p.size + nseq;
-        p.factor = (float2 *)workspace;
+        p.factor = (Factor *)workspace;
         p.seg = (float *)((char *)workspace + factors_bytes(p.entries, heads));
     }
     // Whole sequences longest first where they take more workgroups than there are compute units (24 prompts, 27,591 tokens x 64

@@ -275,3 +275,99 @@ def test_rows_of_no_sequence_and_falling_offsets():
     torch.cuda.synchronize()
     i["lens"] = [64]
     compare(i, out[:20], st[:1], tuple(w[:20] if w.shape[0] == 144 else w[:1] for w in want))
+
+
+def growing(kind, lens, heads, groups, dk, dv, dtype, decay="token"):
+    """Inputs whose decays grow by more than fp32 holds over a few tokens, on states so small, or zero, that all results are
+    finite; and which sequences start from the cache."""
+    import torch
+    i = make(lens, heads, groups, dk, dv, dtype, seed=13)
+    at = [0] + list(np.cumsum(lens))
+    d, st = i["g"].mul_(0.02), i["state"]
+    carry = [0] * len(lens)
+    for s, n in enumerate(lens):
+        b, e = at[s], at[s + 1]
+        if kind == "first":  # powers that meet a state of zeros, then ones that do not
+            d[b:b + 1], d[b + 1:b + 2] = 60.0, 50.0
+            d[b + 2:b + 3] = -100.0
+        elif kind == "zeros":  # the state stays zero while it would grow
+            h = n // 2
+            i["k"][b:b + h] = 0
+            d[b:b + h] = 1.5
+        elif kind == "small":  # a carried state of 1e-30 grows by e^100 on few tokens, by e^-30 on the others
+            carry[s] = 1
+            m = min(n, 40)
+            k0 = b + (n - m) // 2
+            st[s] *= 1e-30
+            d[b:e] -= 30.0 / n
+            d[k0:k0 + m] = 100.0 / m
+            i["k"][b:k0 + m] = 0
+        elif kind == "cleared":  # it was cleared, then would grow
+            carry[s] = 1
+            d[b:b + 1] = -math.inf
+            d[b + 1:b + 2] = 70.0
+            d[b + 2:b + 3] = -60.0
+            d[b + 3:b + 4] = 60.0
+    return i, carry
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,groups,dk,dv", [(2, 1, 64, 64), (1, 1, 37, 33), (2, 2, 128, 48), (1, 1, 256, 64)])
+@pytest.mark.parametrize("kind", ["first", "zeros", "small", "cleared"])
+def test_decays_above_zero_that_pass_fp32(kind, heads, groups, dk, dv, dtype):
+    """A power that fp32 does not hold, times a state that is zero or small: what the recurrence gives in 64 bits."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    for lens in ([2, 3, 70, 200, 1], [700, 1500]):
+        _say("growing", kind, heads, groups, dk, dv, dtype, lens[:3])
+        i, carry = growing(kind, lens, heads, groups, dk, dv, dtype)
+        want = reference(i, None, carry)
+        assert all(np.isfinite(w).all() and np.abs(w).max() < 1e37 for w in want)
+        code = 1 if dtype == "bf16" else 0
+        if len(lens) == 2:
+            assert S.linear_attn_packed_workspace_bytes(sum(lens), 2, max(lens), heads, dk, dv, code) > 0
+        out, st = run(i, None, carry)
+        compare(i, out, st, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (37, 33)])
+def test_step_decays_that_pass_fp32(dk, dv, dtype):
+    import torch
+
+    import selective_state_space_51_amd as S
+    i = make([1] * 6, 2, 1, dk, dv, dtype, nslots=6, seed=14)
+    i["g"][:] = torch.tensor([100.0, 120.0, 89.0, 30.0, 0.7, 170.0], device="cuda")[:, None]
+    scale = torch.tensor([1e-30, 0.0, 1e-37, 1.0, 1.0, 1e-42], device="cuda")  # (the last: numbers below fp32's normal ones)
+    i["state"] *= scale[:, None, None, None]
+    want = reference(i, None, [1] * 6)
+    assert all(np.isfinite(w).all() and np.abs(w).max() < 1e37 for w in want)
+    st = i["state"].clone()
+    out = S.linear_attn_step(i["q"], i["k"], i["v"], i["g"], st)
+    torch.cuda.synchronize()
+    compare(i, out, st, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_growth_of_nothing_is_nothing(dtype):
+    """A log decay of +infinity is a number: a state of zeros stays one, any other becomes infinite."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    i = make([3, 1500, 4], 2, 1, 64, 64, dtype, seed=15)
+    for t in (0, 3, 1503):
+        i["g"][t] = math.inf
+    plain = dict(i, g=i["g"].clone())
+    for t in (0, 3, 1503):
+        plain["g"][t] = 0
+    out, st = run(i, None, [0, 0, 1])
+    want = reference(plain, None, [0, 0, 0])
+    compare(dict(i, lens=[3, 1500]), out[:1503], st[:2], tuple(w[:1503] if len(w) == 1507 else w[:2] for w in want))
+    assert not bool(out[1503:].isfinite().any()) and not bool(st[2].isfinite().any())
+    one = {n: i[n][:2] for n in "qkv"}
+    st = torch.zeros(2, 2, 64, 64, device="cuda")
+    st[1] = 1.0
+    S.linear_attn_step(one["q"], one["k"], one["v"], torch.full((2,), math.inf, device="cuda"), st)
+    kv = one["k"].float()[:, :, :, None] * one["v"].float()[:, :, None, :]
+    assert torch.equal(st[0], kv[0]) and bool((st[1] == math.inf).all())
