@@ -78,6 +78,22 @@ __device__ __forceinline__ B8 pack8(const F4 &a, const F4 &b) {
     return __builtin_bit_cast(B8, w);
 }
 
+// Eight numbers as bf16 that are exact in their bits (rounded towards zero, so that none becomes infinite) and bf16 of what is left:
+// together they are off by 2^-15 of a number at most, where bf16 alone is by 2^-8.
+struct Parts {
+    B8 hi, lo;
+};
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float left_over(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ Parts split8(const F4 &a, const F4 &b) {
+    const uint4 w = {high_halves(a[0], a[1]), high_halves(a[2], a[3]), high_halves(b[0], b[1]), high_halves(b[2], b[3])};
+    const F4 la = {left_over(a[0]), left_over(a[1]), left_over(a[2]), left_over(a[3])};
+    const F4 lb = {left_over(b[0]), left_over(b[1]), left_over(b[2]), left_over(b[3])};
+    return {__builtin_bit_cast(B8, w), pack8(la, lb)};
+}
+
 // A chunk of C tokens of one head, with G_t the sum of the log decays up to token t and S the state before it:
 //     out_t = scale (e^{G_t} q_t S + sum_{j <= t} e^{G_t - G_j} (q_t . k_j) v_j),
 //     S' = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
@@ -85,6 +101,8 @@ __device__ __forceinline__ B8 pack8(const F4 &a, const F4 &b) {
 // columns of S that are its own in registers from chunk to chunk, in the places in which the matrix cores leave a result.
 // bf16: these places are also those of an operand, if of the 32 rows of a step two tiles hold rows 8 g .. 8 g + 3 and 8 g + 4 .. 8 g +
 // 7 in lanes 16 g .. 16 g + 15.  So S never leaves the registers: row_of says which row a place is.
+// bf16: q, k and v go in as they are; scores and S, which are sums in 32 bits, in two parts, and what is added to S in three (the
+// outputs of one 24-prompt batch were 0.0023 of their size off with scores and S rounded to one, where rounding the output alone is 0.0017).
 template <typename T, int KB>
 struct Chunk {
     static constexpr bool BF = sizeof(T) == 2;
@@ -94,7 +112,7 @@ struct Chunk {
     // Row strides in LDS: rows start at different banks, for 16 rows of 16 bytes and (bf16) for 4 rows of 4 pieces 16 bytes apart
     static constexpr int LQ = BF ? D + (KB >= 4 ? 40 : 8) : D + 4, LV = 64 + E, LP = C + E;
     static constexpr int NQ = C * D / E / 256, NV = C * 64 / E / 256;  // 16-byte pieces of a thread
-    T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP];
+    T q[C * LQ], k[C * LQ], v[C * LV], p[C * LP], pl[BF ? C * LP : 1];  // (pl: the second parts of p)
     struct alignas(16) Decay {
         float gh[C], gl[C], w[C];  // G_t (base 2) in two parts; 2^(G_C - G_t)
         float fh, fl;              // 2^G_C in two parts
@@ -153,6 +171,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
     constexpr int C = M::C, NT = M::NT, E = M::E, PQ = M::D / E, PV = 64 / E, PAIRS = (NT * (NT + 1) / 2 + 3) / 4;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane & 15, g = lane >> 4;
     const int group = h / p.share;
+    const float scale = p.scale;  // (read in the loop, the compiler keeps it and its neighbours in memory)
     const T *q = (const T *)p.q + w.t0 * p.q_stride + (int64_t)group * p.dk;
     const T *k = (const T *)p.k + w.t0 * p.k_stride + (int64_t)group * p.dk;
     const T *v = (const T *)p.v + w.t0 * p.v_stride + (int64_t)h * p.dv + c0;
@@ -302,7 +321,7 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                 if (!w.outputs) continue;
                 o += __shfl_xor(o, 16);
                 o += __shfl_xor(o, 32);
-                if (g == 0 && c < nv) oto[t * out_stride] = Io<T>::to(o * p.scale);
+                if (g == 0 && c < nv) oto[t * out_stride] = Io<T>::to(o * scale);
             }
             continue;
         }
@@ -335,8 +354,10 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                     }
                     T *pto = m.p + t * M::LP + j;
                     if constexpr (M::BF) {
-                        *(uint2 *)pto = make_uint2(Io<T>::to2(acc[0], acc[1]), Io<T>::to2(acc[2], acc[3]));
-                        if (jt == tt && !(tt & 1)) *(uint2 *)(pto + 16) = make_uint2(0, 0);  // the other half of a step of 32
+                        T *plto = m.pl + t * M::LP + j;
+                        *(uint2 *)pto = make_uint2(high_halves(acc[0], acc[1]), high_halves(acc[2], acc[3]));
+                        *(uint2 *)plto = make_uint2(Io<T>::to2(left_over(acc[0]), left_over(acc[1])), Io<T>::to2(left_over(acc[2]), left_over(acc[3])));
+                        if (jt == tt && !(tt & 1)) *(uint2 *)(pto + 16) = *(uint2 *)(plto + 16) = make_uint2(0, 0);  // the other half of a step of 32
                     } else {
                         *(F4 *)pto = acc;
                     }
@@ -390,39 +411,69 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                         if (!(fabsf(vx[i >> 2][i & 3]) < INFINITY)) vx[i >> 2][i & 3] = 0.f;
                 }
             }
-            lds_barrier();  // the scores are there
-            B8 sf[M::BF ? KB : 1];
-            if constexpr (M::BF) {
+            // (all tiles side by side and before the next branch: their products do not wait for one another, and a result of the
+            // matrix cores is read in the block that makes it.  bf16: what a step's products read is on its way during the last
+            // step's, which the compiler does not do by itself: four prompts of 1,024 tokens x 24 heads of 64 x 64 44 us for 51.)
+            F4 o[NT];
 #pragma unroll
-                for (int s = 0; s < KB; ++s) sf[s] = pack8(S[2 * s], S[2 * s + 1]);
+            for (int tt = 0; tt < NT; ++tt) o[tt] = (F4){0.f, 0.f, 0.f, 0.f};
+            if constexpr (M::BF) {
+                B8 qb[2][NT];
+                const auto read_q = [&](int s) {
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt) qb[s & 1][tt] = *(const B8 *)(m.q + (16 * tt + l) * M::LQ + 32 * s + 8 * g);
+                };
+                read_q(0);
+#pragma unroll
+                for (int s = 0; s < KB; ++s) {
+                    if (s + 1 < KB) read_q(s + 1);
+                    const Parts a = split8(S[2 * s], S[2 * s + 1]);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt) o[tt] = mma(a.lo, qb[s & 1][tt], o[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt) o[tt] = mma(a.hi, qb[s & 1][tt], o[tt]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
+            lds_barrier();  // the scores are there
             const int rows = w.n - first < C ? w.n - first : C, left = nv - 16 * wave - 4 * g;
             T *out1 = out + first * out_stride;
             const __amdgpu_buffer_rsrc_t ob = rows_buffer(out1, rows, out_stride, nv);
-            // (all tiles before the branch: their products do not wait for one another, and a result of the matrix cores is
-            // read in the block that makes it)
-            F4 o[NT];
+            if constexpr (M::BF) {
+                B8 pb[2][NT];
+                const auto read_p = [&](int s) {
+#pragma unroll
+                    for (int tt = 2 * s; tt < NT; ++tt) {
+                        pb[0][tt] = *(const B8 *)(m.pl + (16 * tt + l) * M::LP + 32 * s + 8 * g);
+                        pb[1][tt] = *(const B8 *)(m.p + (16 * tt + l) * M::LP + 32 * s + 8 * g);
+                    }
+                };
+                read_p(0);
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt) o[tt] *= __builtin_amdgcn_exp2f(dc.gh[16 * tt + l] + dc.gl[16 * tt + l]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < C / 32; ++s) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int tt = 2 * s; tt < NT; ++tt) o[tt] = mma(vf[s], pb[i][tt], o[tt]);
+                    if (s + 1 < C / 32) read_p(s + 1);
+                }
+            }
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt) {
-                const int t = 16 * tt + l;
-                const T *qp = m.q + t * M::LQ, *pp = m.p + t * M::LP;
-                o[tt] = (F4){0.f, 0.f, 0.f, 0.f};
-                if constexpr (M::BF) {
-#pragma unroll
-                    for (int s = 0; s < KB; ++s) o[tt] = mma(sf[s], *(const B8 *)(qp + 32 * s + 8 * g), o[tt]);
-                } else {
+                if constexpr (!M::BF) {
+                    const int t = 16 * tt + l;
+                    const T *pp = m.p + t * M::LP;
 #pragma unroll
                     for (int d = 0; d < 2 * KB; ++d) {
-                        const F4 b = *(const F4 *)(qp + 16 * d + 4 * g);
+                        const F4 b = *(const F4 *)(m.q + t * M::LQ + 16 * d + 4 * g);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) o[tt] = mma(S[d][r], b[r], o[tt]);
                     }
-                }
-                o[tt] *= __builtin_amdgcn_exp2f(dc.gh[t] + dc.gl[t]);
-                if constexpr (M::BF) {
-#pragma unroll
-                    for (int s = 0; s <= tt / 2; ++s) o[tt] = mma(vf[s], *(const B8 *)(pp + 32 * s + 8 * g), o[tt]);
-                } else {
+                    o[tt] *= __builtin_amdgcn_exp2f(dc.gh[t] + dc.gl[t]);
 #pragma unroll
                     for (int s = 0; s <= tt; ++s) {
                         const F4 b = *(const F4 *)(pp + 16 * s + 4 * g);
@@ -430,19 +481,22 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                         for (int r = 0; r < 4; ++r) o[tt] = mma(vx[s][r], b[r], o[tt]);
                     }
                 }
-                o[tt] *= p.scale;
+                o[tt] *= scale;
             }
             if (odd) {
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt) {
                     const int t = 16 * tt + l;
 #pragma unroll 1
-                    for (int j = 0; j <= t; ++j)
+                    for (int j = 0; j <= t; ++j) {
+                        float score = Io<T>::f32(m.p[t * M::LP + j]);
+                        if constexpr (M::BF) score += Io<T>::f32(m.pl[t * M::LP + j]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const float x = Io<T>::f32(m.v[j * M::LV + 16 * wave + 4 * g + r]);
-                            if (!(fabsf(x) < INFINITY)) o[tt][r] = fmaf(Io<T>::f32(m.p[t * M::LP + j]) * p.scale, x, o[tt][r]);
+                            if (!(fabsf(x) < INFINITY)) o[tt][r] = fmaf(score * scale, x, o[tt][r]);
                         }
+                    }
                 }
             }
 #pragma unroll
@@ -482,15 +536,26 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
                     for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] -= (float)part[s][i][e];
                 }
             }
+            B8 kb[2][2][C / 32];
+            const auto read_k = [&](int e) {  // of tiles 2 e and 2 e + 1
 #pragma unroll
-            for (int d = 0; d < 2 * KB; ++d) {
-                const T *kp = m.k + vrow * M::LQ + 8 * (l & 3) + 32 * (d >> 1) + 4 * (d & 1);
+                for (int d = 0; d < 2; ++d)
 #pragma unroll
-                for (int s = 0; s < C / 32; ++s) {
-                    const B8 a = join8(read_transposed(kp + 32 * s * M::LQ), read_transposed(kp + (32 * s + 4) * M::LQ));
+                    for (int s = 0; s < C / 32; ++s) {
+                        const T *kp = m.k + (32 * s + vrow) * M::LQ + 8 * (l & 3) + 32 * e + 4 * d;
+                        kb[e & 1][d][s] = join8(read_transposed(kp), read_transposed(kp + 4 * M::LQ));
+                    }
+            };
+            read_k(0);
 #pragma unroll
-                    for (int i = 2; i >= 0; --i) S[d] = mma(a, part[s][i], S[d]);
-                }
+            for (int e = 0; e < KB; ++e) {
+                if (e + 1 < KB) read_k(e + 1);
+#pragma unroll
+                for (int s = 0; s < C / 32; ++s)
+#pragma unroll
+                    for (int i = 2; i >= 0; --i)
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) S[2 * e + d] = mma(kb[e & 1][d][s], part[s][i], S[2 * e + d]);
             }
         } else {
 #pragma unroll

@@ -371,3 +371,21 @@ def test_infinite_growth_of_nothing_is_nothing(dtype):
     S.linear_attn_step(one["q"], one["k"], one["v"], torch.full((2,), math.inf, device="cuda"), st)
     kv = one["k"].float()[:, :, :, None] * one["v"].float()[:, :, None, :]
     assert torch.equal(st[0], kv[0]) and bool((st[1] == math.inf).all())
+
+
+@pytest.mark.parametrize("lens", [[5, 1, 64, 130], [1100]])
+@pytest.mark.parametrize("dk", [1, 8, 20])
+def test_bf16_sums_are_held_in_32_bits(dk, lens):
+    """A term of the output passes one product with a number of 32 bits (a score, or a state), whose two bf16 parts are off by
+    2^-15 of it (cut to 8 bits, what is left, below 2^-7 of it, rounded by 2^-8 of itself at most); the output is rounded once.  Short
+    memories and few keys, so that outputs next to 0 are of few terms."""
+    import torch
+    _say("32 bits", dk, lens)
+    i = make(lens, 4, 1, dk, 64, "bf16", seed=dk)
+    i["g"] = -0.5 - 2 * torch.rand(i["g"].shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    carry = [1] * len(lens)
+    want, _, mag, _ = reference(i, None, carry)
+    out, _ = run(i, None, carry)
+    err = np.abs(out.double().cpu().numpy() - want)
+    bar = (2.0 ** -15 + (16 + 4 * max(lens) + dk) * 2.0 ** -24) * mag + 2.0 ** -8 * np.abs(want) + 1e-37
+    assert (err <= bar).all(), float((err / bar).max())
