@@ -113,11 +113,19 @@ class MambaLM:
     def logits(self, x, residual):
         return S.w4_matvec(S.add_rms_norm_fwd(x, self.norm, residual=residual)[0], **self.head)
 
+    def _entries(self, n):
+        """n, if the cache has as many entries: a sequence without one would start every token from zeros."""
+        if n > self.state.shape[1]:
+            raise ValueError(f"{n} sequences do not fit into the {self.state.shape[1]} entries of the cache")
+        return n
+
     def generate(self, prompts, n, slots=None):
         """n greedy tokens after each prompt: ([sequences][n] tokens, their log probabilities, the entropies)."""
         if not all(prompts):
             raise ValueError("a prompt without tokens has no last one to go on from")
-        slots = torch.as_tensor(range(len(prompts)) if slots is None else slots, dtype=torch.int32, device=self.embed.device)
+        if slots is None:
+            slots = range(self._entries(len(prompts)))
+        slots = torch.as_tensor(slots, dtype=torch.int32, device=self.embed.device)
         x, residual, last = self.prefill(prompts, slots)
         out = []
         x, residual = x[last], residual[last]
@@ -135,7 +143,7 @@ class MambaLM:
         if not all(prompts):
             raise ValueError("a prompt without tokens has no last one to go on from")
         dev = self.embed.device
-        slots = torch.arange(len(prompts) * count, dtype=torch.int32, device=dev)
+        slots = torch.arange(self._entries(len(prompts) * count), dtype=torch.int32, device=dev)
         first = slots[::count].contiguous()
         x, residual, last = self.prefill(prompts, first)
         src, caches = first.repeat_interleave(count), [*self.conv, *self.state]

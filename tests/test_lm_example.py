@@ -32,3 +32,24 @@ def test_prompts_and_slots(monkeypatch):
         with pytest.raises(RuntimeError, match="no device"):
             m.generate([[1, 2], [3]], 2, slots)
     assert read[0].tolist() == [2, 0] and read[1].tolist() == [0, 1] and read[0].dtype == torch.int32
+
+
+def test_more_sequences_than_entries(monkeypatch):
+    import torch
+    m = _example().MambaLM(vocab=40, width=64, layers=1, slots=5, dtype=torch.float32, device="cpu")
+    read = []
+
+    def prefill(prompts, slots, carry=None):
+        read.append(slots)
+        raise RuntimeError("no device here")
+
+    monkeypatch.setattr(m, "prefill", prefill)
+    for call in (lambda: m.continuations([[1], [2]], 2, 3), lambda: m.generate([[1]] * 6, 2)):
+        with pytest.raises(ValueError, match="6 sequences do not fit into the 5 entries"):
+            call()
+    assert not read
+    with pytest.raises(RuntimeError, match="no device"):
+        m.continuations([[1]], 2, 5)
+    with pytest.raises(RuntimeError, match="no device"):
+        m.generate([[1]] * 5, 2)
+    assert [s.tolist() for s in read] == [[0], [0, 1, 2, 3, 4]]
