@@ -475,7 +475,12 @@ Setting setting(const char *name, const py::object &o, int64_t rows, at::ScalarT
         want_shape(name, t, {rows});
         return {ptr(name, t, dt), 0.};
     }
-    return {nullptr, o.cast<double>()};
+    const double all = PyFloat_AsDouble(o.ptr());
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        throw py::type_error(std::string(name) + " must be a number or a tensor");
+    }
+    return {nullptr, all};
 }
 
 std::tuple<Tensor, Tensor, Tensor> sample(const Tensor &logits, const Tensor &uniform, const py::object &temperature,

@@ -204,3 +204,36 @@ def test_ties_of_large_vocabularies(vocab, dtype):
                        (1.0, vocab // 3, 0.9, 0.0), (2.0, 70_000, 0.37, 0.01)):
         _say("large ties", vocab, dtype, T, k, p, m)
         check(x, u, T, k, p, m)
+
+
+def test_settings_that_are_no_numbers():
+    import torch
+
+    import selective_state_space_51_amd as S
+    x, u = logits(2, 50, "f32")
+    for name in ("temperature", "top_k", "top_p", "min_p"):
+        for bad in (None, "1", [1.0, 1.0]):
+            with pytest.raises(TypeError, match=f"{name} must be a number or a tensor"):
+                S.token_sample(x, u, **{name: bad})
+    want = S.token_sample(x, u, temperature=0.5, top_k=3, top_p=0.5, min_p=0.25)
+    got = S.token_sample(x, u, temperature=np.float32(0.5), top_k=np.int64(3), top_p=np.float64(0.5), min_p=np.float32(0.25))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ties_of_large_vocabularies_in_large_batches(dtype):
+    """More rows than compute units, whose workgroups are smaller: the rows alone, bit for bit."""
+    import torch
+
+    import selective_state_space_51_amd as S
+    vocab = (1 << 19) + 3
+    _say("large ties, 258 rows", dtype)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.zeros(258, vocab, device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    x[1::2] = torch.randint(0, 3, (129, vocab), generator=g, device="cuda").to(x.dtype)
+    u = torch.rand(258, generator=g, device="cuda")
+    for kw in (dict(top_p=0.6), dict(top_k=vocab // 2), dict(top_k=300_000, top_p=0.9)):
+        whole = S.token_sample(x, u, **kw)
+        for r in (0, 1, 256, 257):
+            assert all(torch.equal(a[r:r + 1], b) for a, b in zip(whole, S.token_sample(x[r:r + 1], u[r:r + 1], **kw))), (kw, r)
+    check(x[:2], u[:2], 1.0, vocab // 2, 0.9, 0.0)
