@@ -4,7 +4,7 @@
 // A workgroup takes CW pieces of 16 bytes of an entry of one cache, and all n pairs of entries: it reads those pieces of
 // every source, waits, and writes them to every destination.  No other workgroup touches these pieces, so that any set of
 // moves, rings among them, needs neither an order nor a second copy of the data.  Bytes bound it: every entry is read and written once,
-// 60 pairs of 8 MB in four layers together at 5.7 TB/s (a copy of 1 GB: 5.1).
+// 60 pairs of 2 MB in each of four layers at 5.4 TB/s (a copy of 1 GiB: 5.1); 10,000 pairs of 8 KB, whose strips are 16 bytes wide, at 1.0.
 #include "lm_common.h"
 
 namespace {
@@ -106,9 +106,10 @@ extern "C" int cache_entries_copy(void *const *caches, const int64_t *entry_byte
     }
     // As wide as 1,024 threads leave it: 1 KB next to each other, while 4 or 8 pairs in a thread are enough.  (60 pairs of entries of 2
     // MB in 4 layers: 1,024 threads with 4 pairs each 161 us, 512 with 8 167, 256 with 16 192, 16 pieces wide and 16 pairs 221; 7 pairs
-    // of small ones in 24 layers: 256 threads 8.3, 1,024 14.)  More than 16 pairs are written past the caches: what is
-    // read stays there (161 us for 181, 250 pairs of 1 MB 208 for 214, 500 of 256 KB 94 for 116, 16 pairs 20.9 for 21.1); not where a
-    // row of pieces is less than a cache line (4,000 pairs of 32 KB 161 us, past the caches 166, 10,000 of 8 KB 337 and 564).
+    // of small ones in 24 layers: 256 threads 8.3, 1,024 14.  Times are of the same moves again and again: the first one takes 169
+    // where others come between.)  More than 16 pairs are written past the caches: what is read stays there (161 us for 181; in one
+    // cache, 250 pairs of 1 MB 87 for 112, 500 of 256 KB 39 for 37); not where a row of pieces is less than a cache line (4,000 pairs
+    // of 32 KB 57 us, past the caches 66, 10,000 of 8 KB 164 and 279).
     void (*kernel)(CopyParams) = copy_entries<1024, 1, 16, false>;
     int threads = 1024, cw = 1;
     if (n <= 4) kernel = copy_entries<256, 64, 1, false>, threads = 256, cw = 64;

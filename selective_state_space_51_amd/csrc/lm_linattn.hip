@@ -585,12 +585,15 @@ __device__ __forceinline__ void la_piece(const LaParams &p, const LaPiece &w, Ch
 // one follows makes of the sequence's first state or of a state of zero; the states are joined; the second (LAUNCH 1) reads
 // the others' segments from the states that they start from.  (Outputs of every first segment in the first launch make that
 // launch as long as the second: 4,097 tokens x 24 heads of 64 x 64 fp32 take 60 us, and took 70.)
-// What bounds it: the chunks of the longest sequence or segment, one after another, 64 tokens in 2.4 us (bf16, 64 x 64) to
-// 4.1 us (bf16, 128 x 64, two workgroups to a compute unit).  27,591 tokens of 24 prompts x 64 heads of 128 x 64 bf16: 260 us, 2.1 TB/s of what
-// has to pass; LDS is busy for half of the clocks, the vector units for 40 %.  Two 64-column pieces or two heads in a workgroup of
-// eight waves 302 us, 32 columns per wave 409 (fewer waves, each with longer chains), chunks of 32 tokens 281, and segments of 512,
-// 1,024 or 2,048 tokens are slower there than whole sequences.  fp32 chunks are of 32 tokens: 31 KB of LDS at 64
-// keys, five workgroups to a compute unit, where 64 tokens take 70 KB and allow two.
+// What bounds it: where sequences are few, the chunks of the longest one after another, 64 tokens in 2.6 us (bf16, 64 x 64; four
+// waves in one compute unit, each with its own chain of reads, products and exponentials) or 3.4 us (128 x 64).  Where they fill the
+// chip, what a chunk costs: 27,591 tokens of 24 prompts x 64 heads of 128 x 64 bf16 are 28,224 chunks, two at a time on each of 256 compute
+// units and 5.0 us then, so 277 us if they are even; 271 to 286 are measured, 2.0 TB/s of what has to pass.  A wave has some 520
+// vector instructions, 102 products and 120 accesses of LDS to a chunk; LDS is busy for 58 % of the clocks, the vector units for 46 %.
+// Other paddings of LDS and priorities of waves change nothing (270 to 275).  Before scores and states had two parts (258): two
+// 64-column pieces or two heads in a workgroup of eight waves 302 us, 32 columns per wave 409 (fewer waves, each with longer
+// chains), chunks of 32 tokens 281, and segments of 512, 1,024 or 2,048 tokens slower than whole sequences longest first.  fp32
+// chunks are of 32 tokens: 31 KB of LDS at 64 keys, five workgroups to a compute unit, where 64 tokens take 70 KB and allow two.
 template <typename T, int KB, bool VEC, int LAUNCH>
 __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void la_packed(LaParams p) {
     typedef Chunk<T, KB> M;
@@ -682,7 +685,8 @@ __global__ __launch_bounds__(64) void la_join(LaParams p) {
 
 // One token per sequence: S' = e^g S + k v^T, out = scale q^T S'.  The state is read and written once, and that bounds it: 4 x CG
 // columns of a head's state in a workgroup, CG lanes side by side in a row of it, ND rows in each thread, all of them in flight at
-// once.  128 rows x 64 heads of 128 x 64 (fp32 states of 268 MB): 109 us, 4.9 TB/s of the 5.1 of a copy.  A decay near 1 is taken
+// once.  128 rows x 64 heads of 128 x 64 (fp32 states of 268 MB): 96 us in a trace, 5.6 TB/s, where a copy of 1 GiB reaches 5.1; 110
+// between calls on other states, 88 on the same ones again and again.  A decay near 1 is taken
 // as S + (e^g - 1) S: rounded to 24 bits itself, it would be off in the same direction at every step.
 template <typename T, int CG, int ND, bool VEC, bool PAST>
 __global__ __launch_bounds__(256) void la_step(LaParams p) {
@@ -843,11 +847,14 @@ LaParams la_params(const LaArgs &a, int columns) {
 
 // Tokens per segment, or 0: whole sequences.  In chunks of 64 tokens, the longest sequence takes `whole` of them one after another,
 // and all take `share` if they are even.  Measured, whole and in segments (us): bf16, 24 heads of 64 x 64, 512 tokens 24 and 24,
-// 768 33 and 25, 2,048 79 and 32, four of 1,024 44 and 50, eight of 2,048 80 and 103; 64 heads of 128 x 64, 1,024 tokens 66 and
-// 59, two of 2,048 124 and 123, four of 4,096 238 and 256.  fp32, whose chunks take longer, 24 heads of 64 x 64, 768 tokens 65 and
-// 32, four of 1,024 87 and 60, eight of 2,048 167 and 153; 64 heads of 128 x 64, two of 2,048 268 and 245, four of 4,096 528
-// and 614.  Segments of 192 tokens of one of 4,097 fp32: 63 us, of 128 70, of 256 70, of 384 76.
-constexpr int64_t kSlots = 768;  // three workgroups to each of 256 compute units
+// 768 34 and 22, 2,048 85 and 29, four of 1,024 45 and 46, eight of 2,048 84 and 99; 64 heads of 128 x 64, 1,024 tokens 58 and
+// 42, two of 2,048 113 and 109, four of 4,096 222 and 262; 16 heads of 256 x 64, 512 tokens 47 and 38, four of 1,024 91 and 84, 64 heads,
+// four of 2,048 175 and 318; 24 heads of 32 x 64, four of 1,024 38 and 36, eight of 2,048 72 and 80; of 16 x 16, 768 tokens 28 and 17.
+// fp32, whose chunks take longer, 24 heads of 64 x 64, 768 tokens 62 and 29, four of 1,024 82 and 56, eight of 2,048 160 and 145; 64
+// heads of 128 x 64, two of 2,048 270 and 227, four of 4,096 536 and 612; 16 heads of 256 x 64, 512 tokens 126 and 67, four of
+// 1,024 253 and 141, 64 heads, four of 2,048 502 and 755.  The three constants below and kSlots are fits to these.  Segments of 192
+// tokens of one of 4,097 fp32: 63 us, of 128 70, of 256 70, of 384 76.
+constexpr int64_t kSlots = 768;  // workgroups, three to each of 256 compute units: between what 128 keys (two) and 64 in fp32 (five) allow
 
 int split_size(int64_t tokens, int64_t max_seqlen, int64_t heads, int64_t dv, int io) {
     const int64_t lanes = heads * ((dv + 63) / 64), longest = max_seqlen < tokens ? max_seqlen : tokens;
@@ -882,7 +889,7 @@ int launch_packed_keys(const LaParams &p, int64_t blocks, void *stream) {
 }
 
 // Bytes of states from which on they are written past the caches, of which the last holds as many: 256 MB of them are 89 us either way
-// (114 and 109 where other work comes between), 400 MB 133 us for 165, 800 MB 289 for 327; 192 MB 69 for 68.  (Read past
+// (114 and 110 where other work comes between), 400 MB 133 us for 165, 800 MB 289 for 327; 192 MB 69 for 68.  (Read past
 // them too: 150 and 303.)
 constexpr int64_t kPast = INT64_C(256) << 20;
 
@@ -930,8 +937,8 @@ int linear_attn_packed_fwd(const void *q, int64_t q_stride, const void *k, int64
         p.seg = (float *)((char *)workspace + factors_bytes(p.entries, heads));
     }
     // Whole sequences longest first where they take more workgroups than there are compute units (24 prompts, 27,591 tokens x 64
-    // heads of 128 x 64 bf16 in rising order 383 us as they come and 266 dealt out, in three other orders 312..342 and 253..258; fp32 992
-    // and 700.  With every second round of sequences in rising order, as the scan has them, 272 and 260..264.)
+    // heads of 128 x 64 bf16 in rising order 388 us as they come and 282 dealt out, in three other orders 351..393 and 282; fp32 in rising
+    // order 992 and 700.  With every second round of sequences in rising order, as the scan has them, 2 % slower.)
     else if (nseq > 1 && nseq <= 64 && nseq * per > 256) p.round = 64;
     if (mul_size(pieces, per) < 0 || !grid_fits(pieces * per, 256) || (need && !grid_fits(heads * dk * dv / 64 + 1, 64))) return SELSCAN_E_UNSUPPORTED;
     const int64_t e = io_dtype == SELSCAN_BF16 ? 8 : 4, word = io_dtype == SELSCAN_BF16 ? 2 : 1;

@@ -389,3 +389,16 @@ def test_bf16_sums_are_held_in_32_bits(dk, lens):
     err = np.abs(out.double().cpu().numpy() - want)
     bar = (2.0 ** -15 + (16 + 4 * max(lens) + dk) * 2.0 ** -24) * mag + 2.0 ** -8 * np.abs(want) + 1e-37
     assert (err <= bar).all(), float((err / bar).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,groups,dk,dv", [(6, 2, 256, 100), (4, 1, 200, 64), (3, 3, 129, 33)])
+def test_segments_of_wide_keys(heads, groups, dk, dv, dtype):
+    import selective_state_space_51_amd as S
+    lens = [900, 3, 1500]
+    _say("wide segments", heads, groups, dk, dv, dtype)
+    assert S.linear_attn_packed_workspace_bytes(sum(lens), 3, max(lens), heads, dk, dv, 1 if dtype == "bf16" else 0) > 0
+    i = make(lens, heads, groups, dk, dv, dtype, nslots=5, seed=dk)
+    slots, carry = [4, 0, 2], [1, 1, 0]
+    out, st = run(i, slots, carry, scale=0.3)
+    compare(i, out, st, reference(i, slots, carry, 0.3))
