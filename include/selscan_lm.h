@@ -224,7 +224,7 @@ int w4_matvec(const void *x, int64_t x_stride, const void *qweight, const void *
  *                each head).  Usually <= 0; -infinity clears the state before the token's own product is added (the
  *                number is taken as -16384, whose exponential is 0 too).  Values above 0 make the state grow (up to 16384; beyond
  *                are taken as that): a state of 0 stays 0 however large they are, others come out as the numbers that they grow to,
- *                infinities where fp32 ends.  Where those of a block of 64 tokens add up to more than 44 the block is read
+ *                infinities where fp32 ends.  Where those of a block of 64 tokens (fp32: 32) add up to more than 44 it is read
  *                token by token.  (A product formed on the way, of q and k or of a value and its power, that passes fp32 comes
  *                out as an infinity or as NaN; of a state nothing is left by a power below 2^-149 within a block.)
  *                An infinity in q, k, v or a state comes out as an infinity or as NaN, from its token on.
